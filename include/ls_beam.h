@@ -245,6 +245,118 @@ LS_API ls_status ls_backtrack(const int32_t* token_hist, const int32_t* parent_h
                               void* stream);
 
 /*
+ * A tensor of 4 (or, with `layer`, 5) dimensions [layer, row, pos, head, head_dim] that lies
+ * in memory as its strides say: element (l, r, t, h, d) is data[l * layer + r * row + t * pos +
+ * h * head + d] (strides in elements, none negative; the last dimension is contiguous).
+ */
+typedef struct {
+  void* data; /* device */
+  int64_t layer, row, pos, head;
+} ls_view;
+
+/* Largest number of nodes of a tree of drafted tokens. */
+#define LS_MAX_NODES 64
+
+/*
+ * Cross attention of a decoder's beams to the encoder's states (article: the decoder layers of
+ * the Transformer whose logits the beam step reads).  Every query of beam j of sentence b reads
+ * the keys n < src_len[b] of its sentence:
+ *   out[b*k+j, t, h] = sum_n softmax_n(scale * q[b*k+j, t, h] . key[b, n, h / g]) value[b, n, h / g]
+ * with g = heads / kv_heads query heads per key head.  A sentence of length 0 gives zeros.
+ *
+ *  q, out      [batch*k, q_len, heads, head_dim] views of dtype; out's elements are distinct
+ *              and apart from the inputs.  q_len = 1 is the decode step; longer for a forced
+ *              prefix or for scoring whole targets.
+ *  key, value  [batch, max_src, kv_heads, head_dim] views of dtype: one copy per sentence,
+ *              read once for all its beams.  Positions at or past src_len[b] are not used,
+ *              whatever they hold.
+ *  dtype       f32, f16 or bf16 (one for all).  Scores, softmax and sums are f32; for 16-bit
+ *              types the softmax weights are rounded to the type for the product with the
+ *              values, and the result is rounded once.
+ *  src_len     [batch] int32, device.  A length outside [0, max_src] is clamped and sets
+ *              LS_ERR_INTERNAL in the workspace's status word.
+ *  heads       a multiple of kv_heads; head_dim 1..256; k >= 1, not limited by LS_MAX_K.
+ *  workspace   >= ls_cross_attention_workspace_size(...) bytes, 256-byte aligned, initialised
+ *              once by ls_workspace_init (its status word is used); the size grows with the
+ *              queries per sentence and with head_dim only, so one of the largest call serves
+ *              the others.  Calls sharing it must be ordered.
+ *  Inputs that a query reads are finite; otherwise its result is unspecified (no fault).
+ *  batch == 0 or q_len == 0 is a no-op.  Fastest when every stride and address is a multiple of
+ *  16 bytes.  More than 2^31 - 1 blocks of work return LS_ERR_UNSUPPORTED.
+ */
+LS_API size_t ls_cross_attention_workspace_size(int batch, int k, int q_len, int heads, int kv_heads, int max_src,
+                                                int head_dim);
+LS_API ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view* value, ls_dtype dtype,
+                                    const int32_t* src_len, float scale, int batch, int k, int q_len, int heads,
+                                    int kv_heads, int max_src, int head_dim, const ls_view* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Self-attention of a tree of drafted tokens over a row's cache (no counterpart in the article;
+ * nodes = 1 is the attention of its ordinary single-token step).  Node i of row r reads the
+ * cache's positions [0, cache_len[r]) and, of the drafted tokens, itself and its ancestors:
+ *   out[r, i, h] = softmax-weighted sum over those keys, as in ls_cross_attention.
+ * The drafted keys and values lie apart from the cache: only those of the branch that is
+ * confirmed in the end are written to it (ls_tree_commit).
+ *
+ *  q, out      [rows, nodes, heads, head_dim] views; draft_key, draft_value [rows, nodes,
+ *              kv_heads, head_dim] views.
+ *  cache_key, cache_value  [rows, max_len, kv_heads, head_dim] views, e.g. one layer of a cache
+ *              [layers, rows, kv_heads, max_len, head_dim] (row = kv_heads * max_len * head_dim,
+ *              head = max_len * head_dim, pos = head_dim).  Positions at or past cache_len are
+ *              not used, whatever they hold.
+ *  cache_len   [rows] int32, device; clamped to [0, max_len] as src_len is.
+ *  parent      [rows, nodes] int32, device: each node's parent, which comes before it; -1: the
+ *              node follows the cache directly; below -1: an empty place.  An empty place and
+ *              the nodes under it give zeros and are seen by no other node, and their keys and
+ *              values may hold anything.  A parent that is not before its node sets
+ *              LS_ERR_INTERNAL in the status word; the node is then an empty place.
+ *  nodes       1..LS_MAX_NODES.  Everything else as in ls_cross_attention; rows == 0 is a no-op.
+ */
+LS_API size_t ls_tree_attention_workspace_size(int rows, int nodes, int heads, int kv_heads, int max_len, int head_dim);
+LS_API ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls_view* cache_value,
+                                   const int32_t* cache_len, const ls_view* draft_key, const ls_view* draft_value,
+                                   const int32_t* parent, ls_dtype dtype, float scale, int rows, int nodes, int heads,
+                                   int kv_heads, int max_len, int head_dim, const ls_view* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * The end of a step on a tree of drafted tokens: find the branch that the model's own choices
+ * confirm and append its keys and values to the cache of every layer.  Node 0 (parent -1) holds
+ * the token chosen by the step before; target[r, n] is the model's choice after node n (e.g.
+ * ls_sample on the nodes' logits).  Node i > 0 is confirmed when its parent is and
+ * token[r, i] == target[r, parent[r, i]]; of equal siblings the first counts; the branch ends
+ * before a choice of eos_id, and where the cache is full.
+ *
+ *  cache_key, cache_value  [layers, rows, heads, max_len, head_dim] contiguous, dtype: positions
+ *              cache_len[r] + i of every layer and head receive the branch's i-th node.
+ *  draft_key, draft_value  [layers, rows, nodes, heads, head_dim] views (with `layer`) of dtype;
+ *              the copy is bitwise.  Only confirmed nodes are read.
+ *  cache_len   [rows] int32 in [0, max_len]; parent, token, target  [rows, nodes] int32 (parent
+ *              as in ls_tree_attention).
+ *  finished    [rows] uint8 or NULL: a finished row appends nothing and its next token is eos_id.
+ *  eos_id      the end token, or -1 for none.
+ *  out_len     [rows] int32: cache_len + count; not the array cache_len itself, which every
+ *              layer's block reads.
+ *  out_path    [rows, nodes] int32: the branch's nodes in order, then -1.
+ *  out_count   [rows] int32: nodes appended.
+ *  out_token   [rows] int32: the next token, target of the branch's last node (the next tree's
+ *              node 0); token[r, 0] when nothing could be appended.
+ *  out_finished  [rows] uint8 or NULL: finished, or the next token is eos_id.
+ *  workspace   NULL, or a workspace initialised by ls_workspace_init: a length out of range, a
+ *              full cache or a tree whose node 0 is not its root (each: the row appends nothing)
+ *              sets LS_ERR_INTERNAL in its status word.
+ *  The outputs are apart from the inputs.  nodes 1..LS_MAX_NODES.  Nothing is allocated.
+ *  rows == 0 is a no-op; layers or heads or head_dim == 0 only finds the branch.
+ */
+LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cache_len, const ls_view* draft_key,
+                                const ls_view* draft_value, ls_dtype dtype, const int32_t* parent, const int32_t* token,
+                                const int32_t* target, const uint8_t* finished, int eos_id, int layers, int rows,
+                                int nodes, int heads, int max_len, int head_dim, int32_t* out_len, int32_t* out_path,
+                                int32_t* out_count, int32_t* out_token, uint8_t* out_finished, void* workspace,
+                                void* stream);
+
+/*
  * Synchronise `stream`, return the status the device recorded in `workspace` since
  * the last read, and clear it.  LS_OK when nothing was recorded.
  */

@@ -21,12 +21,14 @@ __all__ = [
     "ls_read_status", "ls_status_string", "ls_read_row_stats", "ls_beam_step_noalloc", "ls_beam_step_noalloc_status",
     "ls_backtrack",
     "ls_sample_workspace_size", "ls_sample", "ls_cache_refresh_inplace", "ls_logits_beam_step",
-    "ls_beam_step_refresh_inplace",
+    "ls_beam_step_refresh_inplace", "LS_MAX_NODES", "ls_cross_attention_workspace_size", "ls_cross_attention",
+    "ls_tree_attention_workspace_size", "ls_tree_attention", "ls_tree_commit",
 ]
 
 LS_OK, LS_ERR_INVALID_ARG, LS_ERR_UNSUPPORTED, LS_ERR_CUDA, LS_ERR_TIMEOUT, LS_ERR_INTERNAL = range(6)
 LS_DTYPE_F32, LS_DTYPE_F16, LS_DTYPE_BF16 = 0, 1, 2
 LS_MAX_K = 64
+LS_MAX_NODES = 64
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -35,6 +37,12 @@ _lib = None
 
 class LsBeamError(RuntimeError):
     pass
+
+
+class _View(ctypes.Structure):
+    """ls_view: a device pointer and the element strides of [layer, row, pos, head, head_dim]."""
+    _fields_ = [("data", ctypes.c_void_p), ("layer", ctypes.c_int64), ("row", ctypes.c_int64), ("pos", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -83,6 +91,19 @@ def load_library():
         lib.ls_beam_step_refresh_inplace.argtypes = [vp, ip, vp, vp, vp, ip, ip, ip, ip, vp, vp, vp, vp, vp, ip, ip,
                                                      ip, ip, ip, ip, vp, sz, vp]
         lib.ls_beam_step_refresh_inplace.restype = ip
+        view, fl = ctypes.POINTER(_View), ctypes.c_float
+        lib.ls_cross_attention_workspace_size.argtypes = [ip] * 7
+        lib.ls_cross_attention_workspace_size.restype = sz
+        lib.ls_cross_attention.argtypes = [view, view, view, ip, vp, fl, ip, ip, ip, ip, ip, ip, ip, view, vp, sz, vp]
+        lib.ls_cross_attention.restype = ip
+        lib.ls_tree_attention_workspace_size.argtypes = [ip] * 6
+        lib.ls_tree_attention_workspace_size.restype = sz
+        lib.ls_tree_attention.argtypes = [view, view, view, vp, view, view, vp, ip, fl, ip, ip, ip, ip, ip, ip, view,
+                                          vp, sz, vp]
+        lib.ls_tree_attention.restype = ip
+        lib.ls_tree_commit.argtypes = [vp, vp, vp, view, view, ip, vp, vp, vp, vp, ip, ip, ip, ip, ip, ip, ip, vp, vp,
+                                       vp, vp, vp, vp, vp]
+        lib.ls_tree_commit.restype = ip
         _lib = lib
         return lib
 
@@ -230,6 +251,121 @@ def ls_cache_refresh_inplace(cache, parent, length: int, workspace=None, stream=
     return load_library().ls_cache_refresh_inplace(
         _ptr(cache), _dtype_code(cache), _ptr(parent), layers, batch, k, heads, max_len, int(length), head_dim,
         _ptr(workspace), _stream(stream))
+
+
+def _view(t, row: int, pos: int, head: int, layer: int | None = None):
+    """ls_view of tensor t, whose dimensions `row`, `pos`, `head` (and `layer`) are those of the view."""
+    st = t.stride()
+    if t.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return _View(t.data_ptr(), st[layer] if layer is not None else 0, st[row], st[pos], st[head])
+
+
+def _same(what: str, *pairs) -> None:
+    for got, want in pairs:
+        if tuple(got) != tuple(want):
+            raise ValueError(f"{what}: shape {tuple(got)}, expected {tuple(want)}")
+
+
+def _plain(what: str, dtype, *tensors) -> None:
+    """Device-side index arrays: of `dtype` and contiguous."""
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError(f"{what}: index arrays must be contiguous {dtype}")
+
+
+def _one_dtype(what: str, *tensors) -> int:
+    if any(t.dtype != tensors[0].dtype for t in tensors):
+        raise ValueError(f"{what}: tensors of different dtypes")
+    return _dtype_code(tensors[0])
+
+
+def ls_cross_attention_workspace_size(batch: int, k: int, q_len: int, heads: int, kv_heads: int, max_src: int,
+                                      head_dim: int) -> int:
+    return int(load_library().ls_cross_attention_workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim))
+
+
+def ls_cross_attention(q, key, value, src_len, out, workspace, scale: float | None = None, stream=None) -> int:
+    """Attention of the beams' queries q [batch, k, q_len, heads, head_dim] over their sentence's keys and values
+    [batch, kv_heads, max_src, head_dim] (positions < src_len [batch] int32), into out of q's shape.  The tensors may
+    be strided views (last dimension contiguous; q's and out's batch and k as one dimension).  scale: 1/sqrt(head_dim)
+    by default.  workspace: ls_cross_attention_workspace_size() bytes."""
+    import torch
+
+    batch, k, q_len, heads, dim = q.shape
+    kv_heads, max_src = key.shape[1], key.shape[2]
+    _same("ls_cross_attention", (key.shape, (batch, kv_heads, max_src, dim)), (value.shape, key.shape),
+          (out.shape, q.shape), (src_len.shape, (batch,)))
+    _plain("ls_cross_attention", torch.int32, src_len)
+    code = _one_dtype("ls_cross_attention", q, key, value, out)
+    for t in (q, out):
+        if batch > 1 and k > 1 and t.stride(0) != k * t.stride(1):
+            raise ValueError("ls_cross_attention: batch and k must be one dimension in memory")
+    views = [_View(t.data_ptr(), 0, t.stride(1) if k > 1 else t.stride(0), t.stride(2), t.stride(3)) for t in (q, out)]
+    if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (q, out)):
+        raise ValueError("the last dimension must be contiguous")
+    return load_library().ls_cross_attention(
+        views[0], _view(key, 0, 2, 1), _view(value, 0, 2, 1), code, _ptr(src_len),
+        float(dim ** -0.5 if scale is None else scale), batch, k, q_len, heads, kv_heads, max_src, dim, views[1],
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def ls_tree_attention_workspace_size(rows: int, nodes: int, heads: int, kv_heads: int, max_len: int,
+                                     head_dim: int) -> int:
+    return int(load_library().ls_tree_attention_workspace_size(rows, nodes, heads, kv_heads, max_len, head_dim))
+
+
+def ls_tree_attention(q, cache_key, cache_value, cache_len, draft_key, draft_value, parent, out, workspace,
+                      scale: float | None = None, stream=None) -> int:
+    """Attention of a tree of drafted tokens: q, out [rows, nodes, heads, head_dim] over one layer of the cache
+    [rows, kv_heads, max_len, head_dim] (positions < cache_len [rows] int32) and over the drafted keys and values
+    [rows, nodes, kv_heads, head_dim] of each node's own branch (parent [rows, nodes] int32: -1 follows the cache,
+    below -1 an empty place).  nodes = 1 is the single-token step.  The tensors may be strided views (last dimension
+    contiguous).  scale: 1/sqrt(head_dim) by default.  workspace: ls_tree_attention_workspace_size() bytes."""
+    import torch
+
+    rows, nodes, heads, dim = q.shape
+    kv_heads, max_len = cache_key.shape[1], cache_key.shape[2]
+    _same("ls_tree_attention", (cache_key.shape, (rows, kv_heads, max_len, dim)), (cache_value.shape, cache_key.shape),
+          (draft_key.shape, (rows, nodes, kv_heads, dim)), (draft_value.shape, draft_key.shape), (out.shape, q.shape),
+          (cache_len.shape, (rows,)), (parent.shape, (rows, nodes)))
+    _plain("ls_tree_attention", torch.int32, cache_len, parent)
+    code = _one_dtype("ls_tree_attention", q, cache_key, cache_value, draft_key, draft_value, out)
+    return load_library().ls_tree_attention(
+        _view(q, 0, 1, 2), _view(cache_key, 0, 2, 1), _view(cache_value, 0, 2, 1), _ptr(cache_len),
+        _view(draft_key, 0, 1, 2), _view(draft_value, 0, 1, 2), _ptr(parent), code,
+        float(dim ** -0.5 if scale is None else scale), rows, nodes, heads, kv_heads, max_len, dim, _view(out, 0, 1, 2),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def ls_tree_commit(cache_key, cache_value, cache_len, draft_key, draft_value, parent, token, target, finished,
+                   eos_id: int, out_len, out_path, out_count, out_token, out_finished=None, workspace=None,
+                   stream=None) -> int:
+    """Finds the branch of each row's tree that `target` confirms (parent, token, target [rows, nodes] int32) and
+    appends its keys and values (draft_* [layers, rows, nodes, heads, head_dim], strided views) at position cache_len
+    of the contiguous caches [layers, rows, heads, max_len, head_dim].  Outputs: out_len, out_count, out_token [rows]
+    int32, out_path [rows, nodes] int32, out_finished [rows] uint8 or None; finished [rows] uint8 or None."""
+    import torch
+
+    layers, rows, heads, max_len, dim = cache_key.shape
+    nodes = parent.shape[1]
+    _same("ls_tree_commit", (cache_value.shape, cache_key.shape), (draft_key.shape, (layers, rows, nodes, heads, dim)),
+          (draft_value.shape, draft_key.shape), (cache_len.shape, (rows,)), (parent.shape, (rows, nodes)),
+          (token.shape, parent.shape), (target.shape, parent.shape), (out_len.shape, (rows,)),
+          (out_path.shape, parent.shape), (out_count.shape, (rows,)), (out_token.shape, (rows,)))
+    _plain("ls_tree_commit", torch.int32, cache_len, parent, token, target, out_len, out_path, out_count, out_token)
+    _plain("ls_tree_commit", torch.uint8, finished, out_finished)
+    for t in (finished, out_finished):
+        if t is not None:
+            _same("ls_tree_commit", (t.shape, (rows,)))
+    if not (cache_key.is_contiguous() and cache_value.is_contiguous()):
+        raise ValueError("ls_tree_commit: the caches must be contiguous")
+    code = _one_dtype("ls_tree_commit", cache_key, cache_value, draft_key, draft_value)
+    return load_library().ls_tree_commit(
+        _ptr(cache_key), _ptr(cache_value), _ptr(cache_len), _view(draft_key, 1, 2, 3, 0), _view(draft_value, 1, 2, 3, 0),
+        code, _ptr(parent), _ptr(token), _ptr(target), _ptr(finished), int(eos_id), layers, rows, nodes, heads, max_len,
+        dim, _ptr(out_len), _ptr(out_path), _ptr(out_count), _ptr(out_token), _ptr(out_finished), _ptr(workspace),
+        _stream(stream))
 
 
 def ls_read_status(workspace, stream=None) -> int:

@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "ls_attend.h"
 #include "ls_beam.h"
 #include "ls_internal.h"
 
@@ -398,6 +399,17 @@ ls_status inplace_check_args(void* cache, ls_dtype dtype, const int32_t* parent,
   }
   return LS_OK;
 }
+
+bool pointers_reachable(const void* const* ptrs, int n) {
+  if (!read_debug().check_ptrs) return true;
+  for (int i = 0; i < n; ++i)
+    if (ptrs[i] && !device_reachable(ptrs[i])) return false;
+  return true;
+}
+
+long long wait_limit_ns() { return read_debug().spin_ns; }
+
+ls_status report_cuda(cudaError_t e) { return e == cudaSuccess ? LS_OK : cuda_fail(e); }
 
 }  // namespace lsb
 

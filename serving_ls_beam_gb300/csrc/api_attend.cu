@@ -1,0 +1,237 @@
+// C-ABI entry points of the decoder's attention and the draft tree's commit (declared in
+// include/ls_beam.h): argument checks on the host, launch plans, and the enqueue of the
+// kernels on the caller's stream.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "ls_attend.h"
+#include "ls_beam.h"
+#include "ls_internal.h"
+
+using namespace lsb;
+
+namespace {
+
+constexpr size_t kAtHeader = 256;  // status word
+constexpr int kAtSms = 152;
+
+int es_of(ls_dtype d) { return d == LS_DTYPE_F32 ? 4 : 2; }
+bool known(ls_dtype d) { return d == LS_DTYPE_F32 || d == LS_DTYPE_F16 || d == LS_DTYPE_BF16; }
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+// A view's pointer and strides; `written`: dimensions of more than one element need a stride.
+bool view_ok(const ls_view* v, int es, bool written, int rows, int pos, int heads) {
+  if (!v || !v->data || misaligned(v->data, (size_t)es)) return false;
+  const int64_t most = INT64_MAX / 8 / (1ll << 31);
+  for (int64_t s : {v->layer, v->row, v->pos, v->head})
+    if (s < 0 || s > most) return false;
+  if (written && ((rows > 1 && v->row == 0) || (pos > 1 && v->pos == 0) || (heads > 1 && v->head == 0))) return false;
+  return true;
+}
+
+AtView view_of(const ls_view* v, int es) {
+  return AtView{static_cast<unsigned char*>(v->data), v->row * es, v->pos * es, v->head * es};
+}
+
+bool shape_ok(int rows, int k, int q_len, int heads, int kv_heads, int max_len, int dim) {
+  return rows >= 0 && k >= 1 && q_len >= 0 && heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && max_len >= 0 &&
+         dim >= 1 && dim <= kAtMaxDim;
+}
+
+size_t workspace_size(int rows, int k, int q_len, int heads, int kv_heads, int max_len, int dim) {
+  if (!shape_ok(rows, k, q_len, heads, kv_heads, max_len, dim)) return 0;
+  const long long m = (long long)k * q_len * (heads / kv_heads);
+  if (m > INT_MAX) return 0;
+  return kAtHeader + (size_t)attend_part_rows((int)m) * (size_t)(dim + 2) * 4;
+}
+
+// Parts of each row's keys so that about `ctas` CTAs run, each with `least` keys or more.
+int split_of(const AttendParams& p, long long base, long long ctas, int least) {
+  long long s = ctas / (base > 0 ? base : 1);
+  const long long by_len = (p.max_len + p.nodes + least - 1) / least;
+  const long long by_part = attend_part_rows(p.m) / ((long long)p.rows * p.kv_heads * p.m);
+  if (s > by_len) s = by_len;
+  if (s > by_part) s = by_part;
+  return s < 1 ? 1 : (int)s;
+}
+
+ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
+  const long long base = (long long)p.rows * p.kv_heads;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.spin_limit_ns = wait_limit_ns();
+  const int mq = attend_simt_queries(dtype, p.m);
+  p.m_tiles = (p.m + mq - 1) / mq;
+  p.splits = split_of(p, base * p.m_tiles, 4 * kAtSms, 128);
+  p.items = base * p.m_tiles * p.splits;
+  if (p.items > INT_MAX || base * p.m > INT_MAX) return LS_ERR_UNSUPPORTED;
+  p.part_ml = reinterpret_cast<float2*>(ws + kAtHeader);
+  p.part_o = reinterpret_cast<float*>(p.part_ml + attend_part_rows(p.m));
+  cudaError_t e = launch_attend_simt(p, dtype, stream);
+  if (e == cudaSuccess && p.splits > 1) e = launch_attend_join(p, dtype, stream);
+  return report_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ls_cross_attention_workspace_size(int batch, int k, int q_len, int heads, int kv_heads, int max_src, int head_dim) {
+  return workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim);
+}
+
+size_t ls_tree_attention_workspace_size(int rows, int nodes, int heads, int kv_heads, int max_len, int head_dim) {
+  if (nodes < 1 || nodes > LS_MAX_NODES) return 0;
+  return workspace_size(rows, 1, nodes, heads, kv_heads, max_len, head_dim);
+}
+
+ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view* value, ls_dtype dtype,
+                             const int32_t* src_len, float scale, int batch, int k, int q_len, int heads, int kv_heads,
+                             int max_src, int head_dim, const ls_view* out, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (!known(dtype) || !shape_ok(batch, k, q_len, heads, kv_heads, max_src, head_dim) || !std::isfinite(scale))
+    return LS_ERR_INVALID_ARG;
+  if (batch == 0 || q_len == 0) return LS_OK;
+  const long long m = (long long)k * q_len * (heads / kv_heads);
+  if ((long long)batch * k > INT_MAX || m > INT_MAX) return LS_ERR_UNSUPPORTED;
+  const int es = es_of(dtype);
+  if (!view_ok(q, es, false, 0, 0, 0) || !view_ok(out, es, true, batch * k, q_len, heads)) return LS_ERR_INVALID_ARG;
+  if (max_src > 0 && (!view_ok(key, es, false, 0, 0, 0) || !view_ok(value, es, false, 0, 0, 0)))
+    return LS_ERR_INVALID_ARG;
+  if (!src_len || misaligned(src_len, 4) || !workspace || misaligned(workspace, 256) ||
+      workspace_bytes < workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim))
+    return LS_ERR_INVALID_ARG;
+  const void* ptrs[] = {q->data, max_src ? key->data : nullptr, max_src ? value->data : nullptr, src_len, out->data,
+                        workspace};
+  if (!pointers_reachable(ptrs, 6)) return LS_ERR_INVALID_ARG;
+  AttendParams p{};
+  p.q = view_of(q, es);
+  p.out = view_of(out, es);
+  if (max_src) {
+    p.key = view_of(key, es);
+    p.value = view_of(value, es);
+  }
+  p.len = src_len;
+  p.scale_log2 = (float)(scale * 1.4426950408889634);
+  p.rows = batch;
+  p.beams = k;
+  p.q_len = q_len;
+  p.kv_heads = kv_heads;
+  p.group = heads / kv_heads;
+  p.dim = head_dim;
+  p.max_len = max_src;
+  p.tokens = k * q_len;
+  p.m = (int)m;
+  return attend(p, dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls_view* cache_value,
+                            const int32_t* cache_len, const ls_view* draft_key, const ls_view* draft_value,
+                            const int32_t* parent, ls_dtype dtype, float scale, int rows, int nodes, int heads,
+                            int kv_heads, int max_len, int head_dim, const ls_view* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!known(dtype) || nodes < 1 || nodes > LS_MAX_NODES || !std::isfinite(scale) ||
+      !shape_ok(rows, 1, nodes, heads, kv_heads, max_len, head_dim))
+    return LS_ERR_INVALID_ARG;
+  if (rows == 0) return LS_OK;
+  const int es = es_of(dtype);
+  if (!view_ok(q, es, false, 0, 0, 0) || !view_ok(out, es, true, rows, nodes, heads) ||
+      !view_ok(draft_key, es, false, 0, 0, 0) || !view_ok(draft_value, es, false, 0, 0, 0))
+    return LS_ERR_INVALID_ARG;
+  if (max_len > 0 && (!view_ok(cache_key, es, false, 0, 0, 0) || !view_ok(cache_value, es, false, 0, 0, 0)))
+    return LS_ERR_INVALID_ARG;
+  if (!cache_len || misaligned(cache_len, 4) || !parent || misaligned(parent, 4) || !workspace ||
+      misaligned(workspace, 256) || workspace_bytes < workspace_size(rows, 1, nodes, heads, kv_heads, max_len, head_dim))
+    return LS_ERR_INVALID_ARG;
+  const void* ptrs[] = {q->data,   max_len ? cache_key->data : nullptr, max_len ? cache_value->data : nullptr,
+                        cache_len, draft_key->data, draft_value->data,  parent, out->data, workspace};
+  if (!pointers_reachable(ptrs, 9)) return LS_ERR_INVALID_ARG;
+  AttendParams p{};
+  p.q = view_of(q, es);
+  p.out = view_of(out, es);
+  if (max_len) {
+    p.key = view_of(cache_key, es);
+    p.value = view_of(cache_value, es);
+  }
+  p.dkey = view_of(draft_key, es);
+  p.dvalue = view_of(draft_value, es);
+  p.len = cache_len;
+  p.parent = parent;
+  p.scale_log2 = (float)(scale * 1.4426950408889634);
+  p.rows = rows;
+  p.beams = 1;
+  p.q_len = nodes;
+  p.kv_heads = kv_heads;
+  p.group = heads / kv_heads;
+  p.dim = head_dim;
+  p.max_len = max_len;
+  p.nodes = nodes;
+  p.tokens = nodes;
+  p.m = nodes * p.group;
+  return attend(p, dtype, workspace, static_cast<cudaStream_t>(stream));
+}
+
+ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cache_len, const ls_view* draft_key,
+                         const ls_view* draft_value, ls_dtype dtype, const int32_t* parent, const int32_t* token,
+                         const int32_t* target, const uint8_t* finished, int eos_id, int layers, int rows, int nodes,
+                         int heads, int max_len, int head_dim, int32_t* out_len, int32_t* out_path, int32_t* out_count,
+                         int32_t* out_token, uint8_t* out_finished, void* workspace, void* stream) {
+  if (!known(dtype) || layers < 0 || rows < 0 || nodes < 1 || nodes > LS_MAX_NODES || heads < 0 || max_len < 0 ||
+      head_dim < 0)
+    return LS_ERR_INVALID_ARG;
+  if (rows == 0) return LS_OK;
+  const int es = es_of(dtype);
+  const bool move = layers > 0 && heads > 0 && head_dim > 0 && max_len > 0;
+  if (move && (!cache_key || !cache_value || cache_key == cache_value || misaligned(cache_key, (size_t)es) ||
+               misaligned(cache_value, (size_t)es) || !view_ok(draft_key, es, false, 0, 0, 0) ||
+               !view_ok(draft_value, es, false, 0, 0, 0)))
+    return LS_ERR_INVALID_ARG;
+  const void* words[] = {cache_len, parent, token, target, out_len, out_path, out_count, out_token};
+  for (const void* w : words)
+    if (!w || misaligned(w, 4)) return LS_ERR_INVALID_ARG;
+  if (out_len == cache_len || (workspace && misaligned(workspace, 256))) return LS_ERR_INVALID_ARG;
+  const void* ptrs[] = {cache_len, parent,    token,     target,       out_len,   out_path, out_count,
+                        out_token, finished,  out_finished, workspace, move ? cache_key : nullptr,
+                        move ? cache_value : nullptr, move ? draft_key->data : nullptr, move ? draft_value->data : nullptr};
+  if (!pointers_reachable(ptrs, 15)) return LS_ERR_INVALID_ARG;
+  const long long head_bytes = (long long)head_dim * es;
+  if (move && (layers > 65535 || (long long)nodes * heads * head_dim > INT_MAX)) return LS_ERR_UNSUPPORTED;
+  CommitParams p{};
+  if (move) {
+    p.cache_key = static_cast<unsigned char*>(cache_key);
+    p.cache_value = static_cast<unsigned char*>(cache_value);
+    p.dkey = view_of(draft_key, es);
+    p.dvalue = view_of(draft_value, es);
+    p.dkey_layer = draft_key->layer * es;
+    p.dvalue_layer = draft_value->layer * es;
+    const uint64_t all = reinterpret_cast<uintptr_t>(cache_key) | reinterpret_cast<uintptr_t>(cache_value) |
+                         reinterpret_cast<uintptr_t>(draft_key->data) | reinterpret_cast<uintptr_t>(draft_value->data) |
+                         (uint64_t)(p.dkey.row | p.dkey.pos | p.dkey.head | p.dkey_layer | p.dvalue.row | p.dvalue.pos |
+                                    p.dvalue.head | p.dvalue_layer | head_bytes);
+    p.unit = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+    p.vec_units = (int)(head_bytes / p.unit);
+  }
+  p.cache_len = cache_len;
+  p.parent = parent;
+  p.token = token;
+  p.target = target;
+  p.finished = finished;
+  p.out_len = out_len;
+  p.out_path = out_path;
+  p.out_count = out_count;
+  p.out_token = out_token;
+  p.out_finished = out_finished;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.layers = move ? layers : 1;
+  p.rows = rows;
+  p.nodes = nodes;
+  p.heads = move ? heads : 0;
+  p.max_len = max_len;
+  p.eos = eos_id;
+  return report_cuda(launch_tree_commit(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

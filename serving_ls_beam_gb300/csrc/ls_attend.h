@@ -1,0 +1,95 @@
+// Internal definitions of the decoder's attention (cross attention and the draft tree's
+// attention) and of the tree's commit, shared by the host entry points (api_attend.cu) and
+// the kernels.  Nothing here is part of the public interface (include/ls_beam.h).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "ls_beam.h"
+
+namespace lsb {
+
+constexpr int kAtMaxDim = 256;   // largest head size
+constexpr int kAtMaxNodes = LS_MAX_NODES;
+
+// A tensor [row, pos, head, head_dim] by its byte strides (head_dim contiguous).
+struct AtView {
+  unsigned char* data;
+  long long row, pos, head;
+};
+
+// One attention call.  The queries that read the same keys are one problem: the key / value
+// row `r` and key head `h`, with m = tokens * group queries (token t = beam * q_len + pos,
+// query i = t * group + its head within the group).
+struct AttendParams {
+  AtView q, out;          // [rows * beams, q_len, kv_heads * group, dim]
+  AtView key, value;      // [rows, max_len, kv_heads, dim]
+  AtView dkey, dvalue;    // [rows, nodes, kv_heads, dim] drafted tokens (nodes == 0: none)
+  const int32_t* len;     // [rows] keys of each row
+  const int32_t* parent;  // [rows, nodes]
+  uint32_t* status;
+  float scale_log2;       // scale * log2(e): the softmax runs in powers of two
+  int rows, beams, q_len, kv_heads, group, dim, max_len, nodes;
+  int tokens;             // beams * q_len
+  int m;                  // tokens * group
+  int m_tiles;            // ceil(m / queries per CTA or warp)
+  int splits;             // parts of a row's keys (each a CTA's); > 1: partial results
+  float* part_o;          // [problem, m, split, dim] f32
+  float2* part_ml;        // [problem, m, split]: maximum (log2 units) and sum
+  long long items;        // rows * kv_heads * m_tiles * splits
+  long long spin_limit_ns;
+};
+
+// Partial results may take this many (query, split) rows of dim + 2 floats: the plan keeps
+// its splits within it, so the workspace depends on the queries and the head size alone.
+__host__ __device__ inline long long attend_part_rows(int m) { return 1024ll * (m < 80 ? m : 80); }
+
+struct CommitParams {
+  unsigned char* cache_key;
+  unsigned char* cache_value;
+  AtView dkey, dvalue;      // [layer][row, node, head, dim]
+  long long dkey_layer, dvalue_layer;
+  const int32_t* cache_len;
+  const int32_t* parent;
+  const int32_t* token;
+  const int32_t* target;
+  const uint8_t* finished;  // may be null
+  int32_t* out_len;
+  int32_t* out_path;
+  int32_t* out_count;
+  int32_t* out_token;
+  uint8_t* out_finished;    // may be null
+  uint32_t* status;         // may be null
+  int layers, rows, nodes, heads, max_len, eos;
+  int vec_units;            // copy units per head vector
+  int unit;                 // bytes of a copy unit
+};
+
+// Raises a kernel's dynamic shared-memory limit once per device (`done`: a bit per device).
+template <class Kernel>
+inline cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+cudaError_t launch_attend_simt(const AttendParams& p, int dtype, cudaStream_t stream);
+int attend_simt_queries(int dtype, int m);  // queries per CTA
+cudaError_t launch_attend_join(const AttendParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
+
+// Shared with api.cu.
+bool pointers_reachable(const void* const* ptrs, int n);  // nulls are skipped
+long long wait_limit_ns();
+ls_status report_cuda(cudaError_t e);
+
+}  // namespace lsb

@@ -1,0 +1,76 @@
+// Device helpers of a tree of drafted tokens, and the addresses of an attention problem.
+#pragma once
+
+#include <stdint.h>
+
+#include "ls_attend.h"
+#include "ls_internal.h"
+
+namespace lsb {
+
+// What the nodes of one row's tree see, in shared memory.
+struct TreeSeen {
+  unsigned long long mask[kAtMaxNodes];  // bit j: the node sees node j (0: an empty place)
+  int up[kAtMaxNodes];
+};
+
+// Fills t for a tree of `nodes` nodes with `n` threads (thread `tid`); `sync` orders those
+// threads' shared memory.  Pointer doubling: after round r a node's mask holds its 2^r nearest
+// ancestors, so a chain of 64 takes six rounds.  A node whose parent is below -1 is an empty
+// place, one whose parent is not before it is invalid (returned true) and treated the same,
+// and so are the nodes under either.
+template <class Sync>
+__device__ __forceinline__ bool tree_seen(TreeSeen& t, const int32_t* parent, int nodes, int tid, int n, Sync sync) {
+  bool bad = false;
+  for (int i = tid; i < nodes; i += n) {
+    const int p = __ldg(parent + i);
+    bad |= p >= i;
+    const bool there = p >= -1 && p < i;
+    t.mask[i] = there ? 1ull << i : 0ull;
+    t.up[i] = there ? p : -2;
+  }
+  sync();
+  for (int reach = 1; reach < nodes; reach <<= 1) {
+    unsigned long long m[kAtMaxNodes / 32];
+    int u[kAtMaxNodes / 32];
+#pragma unroll
+    for (int r = 0; r < kAtMaxNodes / 32; ++r) {
+      const int i = tid + r * n;
+      if (i >= nodes || i < 0) continue;
+      m[r] = t.mask[i];
+      u[r] = t.up[i];
+      if (u[r] >= 0) {
+        const int a = u[r];
+        u[r] = t.up[a];
+        m[r] = u[r] == -2 ? 0ull : m[r] | t.mask[a];
+      }
+    }
+    sync();
+#pragma unroll
+    for (int r = 0; r < kAtMaxNodes / 32; ++r) {
+      const int i = tid + r * n;
+      if (i >= nodes) continue;
+      t.mask[i] = m[r];
+      t.up[i] = u[r];
+    }
+    sync();
+  }
+  return bad;
+}
+
+// The keys of a row, clamped to its places; out of range sets the status word (by `report`).
+__device__ __forceinline__ int row_keys(const AttendParams& p, int r, bool report) {
+  const int n = __ldg(p.len + r);
+  const int c = min(max(n, 0), p.max_len);
+  if (report && n != c) atomicOr(p.status, kDevInternal);
+  return c;
+}
+
+// Query i of problem (r, h).
+__device__ __forceinline__ long long query_offset(const AttendParams& p, const AtView& v, int r, int h, int i) {
+  const int t = i / p.group, g = i - t * p.group;
+  const int b = t / p.q_len, pos = t - b * p.q_len;
+  return ((long long)r * p.beams + b) * v.row + (long long)pos * v.pos + (long long)(h * p.group + g) * v.head;
+}
+
+}  // namespace lsb
