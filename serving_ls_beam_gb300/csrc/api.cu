@@ -55,11 +55,12 @@ struct Debug {
   int ipstage = 0; // in-place bulk-copy kernel: bytes of each staging buffer, 0 = plan's choice
   int stage = -1;  // K2 after K0: 1 = stage the batch's slots, 0 = read them in place, -1 = plan
   bool check_ptrs = true;
+  AttendDebug attend{0, 0, 0};  // attention: kernel, warps per item, parts of a row's keys (0 = plan)
 };
 
 // LS_BEAM_DEBUG: comma-separated "exact", "ipplain", "iptma", "ipwords", "ipstatic", "steprefresh", "chunk", "strips",
 // "fused", "nofused", "cluster", "nocluster", "spin=<ns>", "vpl=<4|8|16>", "stages=<2..8>", "parts=<n>", "ipw=<words>",
-// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck".
+// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atwarps=<1|4>", "atsplits=<n>".
 Debug read_debug() {
   Debug d;
   const char* env = std::getenv("LS_BEAM_DEBUG");
@@ -89,6 +90,11 @@ Debug read_debug() {
     else if (!std::strncmp(tok, "ipstage=", 8)) d.ipstage = std::atoi(tok + 8);
     else if (!std::strncmp(tok, "stage=", 6)) d.stage = std::atoi(tok + 6);
     else if (!std::strcmp(tok, "nocheck")) d.check_ptrs = false;
+    else if (!std::strcmp(tok, "atsimt")) d.attend.kernel = kAtForceSimt;
+    else if (!std::strcmp(tok, "atmma")) d.attend.kernel = kAtForceMma;
+    else if (!std::strcmp(tok, "attc")) d.attend.kernel = kAtForceTc;
+    else if (!std::strncmp(tok, "atwarps=", 8)) d.attend.warps = std::atoi(tok + 8) == 1 ? 1 : 4;
+    else if (!std::strncmp(tok, "atsplits=", 9)) d.attend.splits = std::atoi(tok + 9);
   }
   if (d.spin_ns < 0) d.spin_ns = 0;
   if (vpl_index(d.vpl) < 0) d.vpl = 0;
@@ -408,6 +414,8 @@ bool pointers_reachable(const void* const* ptrs, int n) {
 }
 
 long long wait_limit_ns() { return read_debug().spin_ns; }
+
+AttendDebug attend_debug() { return read_debug().attend; }
 
 ls_status report_cuda(cudaError_t e) { return e == cudaSuccess ? LS_OK : cuda_fail(e); }
 

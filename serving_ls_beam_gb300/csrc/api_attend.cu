@@ -16,7 +16,6 @@ using namespace lsb;
 namespace {
 
 constexpr size_t kAtHeader = 256;  // status word
-constexpr int kAtSms = 152;
 
 int es_of(ls_dtype d) { return d == LS_DTYPE_F32 ? 4 : 2; }
 bool known(ls_dtype d) { return d == LS_DTYPE_F32 || d == LS_DTYPE_F16 || d == LS_DTYPE_BF16; }
@@ -49,28 +48,43 @@ size_t workspace_size(int rows, int k, int q_len, int heads, int kv_heads, int m
 }
 
 // Parts of each row's keys so that about `ctas` CTAs run, each with `least` keys or more.
-int split_of(const AttendParams& p, long long base, long long ctas, int least) {
-  long long s = ctas / (base > 0 ? base : 1);
-  const long long by_len = (p.max_len + p.nodes + least - 1) / least;
+int split_of(const AttendParams& p, long long base, long long ctas, int least, int forced) {
+  long long s = forced > 0 ? forced : ctas / (base > 0 ? base : 1);
+  const long long by_len = ((long long)p.max_len + p.nodes + least - 1) / least;
   const long long by_part = attend_part_rows(p.m) / ((long long)p.rows * p.kv_heads * p.m);
-  if (s > by_len) s = by_len;
+  if (s > by_len && forced <= 0) s = by_len;
   if (s > by_part) s = by_part;
   return s < 1 ? 1 : (int)s;
 }
 
+bool vectors16(const AtView& v) {
+  return ((reinterpret_cast<uintptr_t>(v.data) | (uint64_t)v.row | (uint64_t)v.pos | (uint64_t)v.head) & 15) == 0;
+}
+
 ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
   const long long base = (long long)p.rows * p.kv_heads;
+  if (base * p.m > INT_MAX) return LS_ERR_UNSUPPORTED;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.spin_limit_ns = wait_limit_ns();
-  const int mq = attend_simt_queries(dtype, p.m);
-  p.m_tiles = (p.m + mq - 1) / mq;
-  p.splits = split_of(p, base * p.m_tiles, 4 * kAtSms, 128);
-  p.items = base * p.m_tiles * p.splits;
-  if (p.items > INT_MAX || base * p.m > INT_MAX) return LS_ERR_UNSUPPORTED;
   p.part_ml = reinterpret_cast<float2*>(ws + kAtHeader);
   p.part_o = reinterpret_cast<float*>(p.part_ml + attend_part_rows(p.m));
-  cudaError_t e = launch_attend_simt(p, dtype, stream);
+  const AttendDebug dbg = attend_debug();
+  const bool tensor = dtype != LS_DTYPE_F32 && p.dim % 8 == 0 && vectors16(p.q) && vectors16(p.out) &&
+                      vectors16(p.key) && vectors16(p.value) && vectors16(p.dkey) && vectors16(p.dvalue);
+  const bool mma = tensor && dbg.kernel != kAtForceSimt;
+  const int mq = mma ? attend_mma_queries(p.dim, p.m) : attend_simt_queries(dtype, p.m);
+  p.m_tiles = (p.m + mq - 1) / mq;
+  if (mma) {
+    const long long whole = base * p.m_tiles;
+    p.warps = dbg.warps ? dbg.warps : (whole >= 4 * 2 * kAtSms && p.max_len <= 256 ? 1 : 4);
+    p.splits = p.warps == 1 ? 1 : split_of(p, whole, 2 * kAtSms, 256, dbg.splits);
+  } else {
+    p.splits = split_of(p, base * p.m_tiles, 4 * kAtSms, 128, dbg.splits);
+  }
+  p.items = base * p.m_tiles * p.splits;
+  if (p.items > INT_MAX) return LS_ERR_UNSUPPORTED;
+  cudaError_t e = mma ? launch_attend_mma(p, dtype, stream) : launch_attend_simt(p, dtype, stream);
   if (e == cudaSuccess && p.splits > 1) e = launch_attend_join(p, dtype, stream);
   return report_cuda(e);
 }

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSiThreads) attend_simt_kernel(const AttendPar
     for (int w = 0; w < kSiWarps; ++w) {
       const float f = fast_exp2(wm[w][j] - base);
       L = fmaf(f, wl[w][j], L);
-      O = wl[w][j] != 0.0f ? fmaf(f, acc[(w * MQ + j) * ND * 32 + d], O) : O;
+      O = add_part(O, f, acc[(w * MQ + j) * ND * 32 + d], wl[w][j]);
     }
     if (p.splits == 1) {
       store_elem<DT>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + d * B, L == 0.0f ? 0.0f : O / L);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
     L = fmaf(f, e.y, L);
 #pragma unroll
     for (int c = 0; c < kAtMaxDim / 32; ++c)
-      if (c * 32 + lane < p.dim && e.y != 0.0f) o[c] = fmaf(f, po[(long long)s * p.dim + c * 32 + lane], o[c]);
+      if (c * 32 + lane < p.dim) o[c] = add_part(o[c], f, po[(long long)s * p.dim + c * 32 + lane], e.y);
   }
   unsigned char* out = p.out.data + query_offset(p, p.out, r, h, i);
 #pragma unroll

@@ -19,11 +19,11 @@ struct TreeSeen {
 // ancestors, so a chain of 64 takes six rounds.  A node whose parent is below -1 is an empty
 // place, one whose parent is not before it is invalid (returned true) and treated the same,
 // and so are the nodes under either.
-template <class Sync>
-__device__ __forceinline__ bool tree_seen(TreeSeen& t, const int32_t* parent, int nodes, int tid, int n, Sync sync) {
+template <class Parent, class Sync>
+__device__ __forceinline__ bool tree_seen_from(TreeSeen& t, Parent parent, int nodes, int tid, int n, Sync sync) {
   bool bad = false;
   for (int i = tid; i < nodes; i += n) {
-    const int p = __ldg(parent + i);
+    const int p = parent(i);
     bad |= p >= i;
     const bool there = p >= -1 && p < i;
     t.mask[i] = there ? 1ull << i : 0ull;
@@ -56,6 +56,18 @@ __device__ __forceinline__ bool tree_seen(TreeSeen& t, const int32_t* parent, in
     sync();
   }
   return bad;
+}
+
+template <class Sync>
+__device__ __forceinline__ bool tree_seen(TreeSeen& t, const int32_t* parent, int nodes, int tid, int n, Sync sync) {
+  return tree_seen_from(t, [&](int i) { return __ldg(parent + i); }, nodes, tid, n, sync);
+}
+
+// acc + f * x of a part with the sum l: nothing of an empty part, and an infinite or NaN x as
+// it is (f may have underflowed).
+__device__ __forceinline__ float add_part(float acc, float f, float x, float l) {
+  const float y = isfinite(x) ? f * x : x;
+  return l != 0.0f ? acc + y : acc;
 }
 
 // The keys of a row, clamped to its places; out of range sets the status word (by `report`).
