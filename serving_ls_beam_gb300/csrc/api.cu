@@ -417,6 +417,20 @@ long long wait_limit_ns() { return read_debug().spin_ns; }
 
 AttendDebug attend_debug() { return read_debug().attend; }
 
+bool encode_attend(CUtensorMap* map, const AtView& v, int dtype, int dim, int pos, int heads, int rows, int box) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)pos, (cuuint64_t)heads, (cuuint64_t)rows};
+  // an extent of one needs no stride; any valid one does
+  const cuuint64_t line = (cuuint64_t)((dim * 2 + 15) / 16 * 16);
+  const cuuint64_t strides[3] = {pos > 1 ? (cuuint64_t)v.pos : line, heads > 1 ? (cuuint64_t)v.head : line,
+                                 rows > 1 ? (cuuint64_t)v.row : line};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(map, dtype == LS_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.data,
+            dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 ls_status report_cuda(cudaError_t e) { return e == cudaSuccess ? LS_OK : cuda_fail(e); }
 
 }  // namespace lsb

@@ -61,6 +61,27 @@ bool vectors16(const AtView& v) {
   return ((reinterpret_cast<uintptr_t>(v.data) | (uint64_t)v.row | (uint64_t)v.pos | (uint64_t)v.head) & 15) == 0;
 }
 
+// The tensor-core kernel's tensor maps: key, value and the drafted ones (copies of the key's
+// where there are none).  False where a map cannot describe the tensors.
+bool encode_maps(CUtensorMap (&maps)[4], AttendParams& p, int dtype) {
+  p.kv_row_one = p.rows > 1 && p.key.row == 0;
+  p.kv_head_one = p.kv_heads > 1 && p.key.head == 0;
+  // a stride of 0 means one element: the same for keys and values, or no map
+  if ((p.value.row == 0) != (p.key.row == 0) || (p.value.head == 0) != (p.key.head == 0)) return false;
+  if (p.max_len > 1 && (p.key.pos == 0 || p.value.pos == 0)) return false;
+  const int rows = p.kv_row_one ? 1 : p.rows, heads = p.kv_head_one ? 1 : p.kv_heads;
+  if (!encode_attend(&maps[0], p.key, dtype, p.dim, p.max_len, heads, rows, kAtTcBox) ||
+      !encode_attend(&maps[1], p.value, dtype, p.dim, p.max_len, heads, rows, kAtTcBox))
+    return false;
+  maps[2] = maps[0];
+  maps[3] = maps[1];
+  if (!p.nodes) return true;
+  for (const AtView& v : {p.dkey, p.dvalue})
+    if ((p.rows > 1 && v.row == 0) || (p.kv_heads > 1 && v.head == 0) || (p.nodes > 1 && v.pos == 0)) return false;
+  return encode_attend(&maps[2], p.dkey, dtype, p.dim, p.nodes, p.kv_heads, p.rows, kAtTcBox) &&
+         encode_attend(&maps[3], p.dvalue, dtype, p.dim, p.nodes, p.kv_heads, p.rows, kAtTcBox);
+}
+
 ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
   const long long base = (long long)p.rows * p.kv_heads;
   if (base * p.m > INT_MAX) return LS_ERR_UNSUPPORTED;
@@ -72,10 +93,18 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   const AttendDebug dbg = attend_debug();
   const bool tensor = dtype != LS_DTYPE_F32 && p.dim % 8 == 0 && vectors16(p.q) && vectors16(p.out) &&
                       vectors16(p.key) && vectors16(p.value) && vectors16(p.dkey) && vectors16(p.dvalue);
-  const bool mma = tensor && dbg.kernel != kAtForceSimt;
-  const int mq = mma ? attend_mma_queries(p.dim, p.m) : attend_simt_queries(dtype, p.m);
+  CUtensorMap maps[4];
+  const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
+                  (dbg.kernel ? dbg.kernel == kAtForceTc : p.m > 32) && encode_maps(maps, p, dtype);
+  const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt;
+  const int mq = tc ? kAtTcQueries : mma ? attend_mma_queries(p.dim, p.m) : attend_simt_queries(dtype, p.m);
   p.m_tiles = (p.m + mq - 1) / mq;
-  if (mma) {
+  if (tc) {
+    p.negate = p.scale_log2 < 0.0f;
+    // a scale of 0 as 2^-100: masked scores stay -inf, and every weight still is exactly 1
+    p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
+    p.splits = split_of(p, base * p.m_tiles, kAtSms, 512, dbg.splits);
+  } else if (mma) {
     const long long whole = base * p.m_tiles;
     p.warps = dbg.warps ? dbg.warps : (whole >= 4 * 2 * kAtSms && p.max_len <= 256 ? 1 : 4);
     p.splits = p.warps == 1 ? 1 : split_of(p, whole, 2 * kAtSms, 256, dbg.splits);
@@ -84,7 +113,9 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   }
   p.items = base * p.m_tiles * p.splits;
   if (p.items > INT_MAX) return LS_ERR_UNSUPPORTED;
-  cudaError_t e = mma ? launch_attend_mma(p, dtype, stream) : launch_attend_simt(p, dtype, stream);
+  cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
+                  : mma ? launch_attend_mma(p, dtype, stream)
+                        : launch_attend_simt(p, dtype, stream);
   if (e == cudaSuccess && p.splits > 1) e = launch_attend_join(p, dtype, stream);
   return report_cuda(e);
 }

@@ -44,6 +44,9 @@ struct AttendParams {
   float2* part_ml;        // [problem, m, split]: maximum (log2 units) and sum
   long long items;        // rows * kv_heads * m_tiles * splits
   long long spin_limit_ns;
+  // attend_tc.cu: scale_log2 is its absolute value and the sign goes into the queries; a key
+  // tensor shared by all rows or heads (stride 0) has one row or head in its tensor map
+  int negate, kv_row_one, kv_head_one;
 };
 
 // Partial results may take this many (query, split) rows of dim + 2 floats: the plan keeps
@@ -89,6 +92,10 @@ int attend_simt_queries(int dtype, int m);  // queries per CTA
 // f16 / bf16, every stride and address a multiple of 16 bytes
 cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_mma_queries(int dim, int m);  // queries per item
+// f16 / bf16, head size up to kAtTcDim, every stride and address a multiple of 16 bytes; maps: key,
+// value, drafted key, drafted value
+constexpr int kAtTcDim = 128, kAtTcQueries = 256, kAtTcBox = 64;
+cudaError_t launch_attend_tc(const CUtensorMap (&maps)[4], const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_attend_join(const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
 
@@ -101,6 +108,9 @@ struct AttendDebug {
   int kernel, warps, splits;
 };
 AttendDebug attend_debug();
+// Tensor map of a 16-bit tensor [row, head, pos, dim] by byte strides, in boxes of 64 elements by
+// `box` positions (one swizzle row of 128 bytes each); reads past an extent return zeros.
+bool encode_attend(CUtensorMap* map, const AtView& v, int dtype, int dim, int pos, int heads, int rows, int box);
 ls_status report_cuda(cudaError_t e);
 
 }  // namespace lsb
