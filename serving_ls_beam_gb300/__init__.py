@@ -52,6 +52,8 @@ def library_path() -> str:
 def load_library():
     """Load libls_beam.so (built by ``__graft_entry__.build()``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -108,13 +110,18 @@ def load_library():
         return lib
 
 
-def _dtype_code(t) -> int:
-    import torch
+_codes: dict = {}
 
-    codes = {torch.float32: LS_DTYPE_F32, torch.float16: LS_DTYPE_F16, torch.bfloat16: LS_DTYPE_BF16}
-    if t.dtype not in codes:
+
+def _dtype_code(t) -> int:
+    if not _codes:
+        import torch
+
+        _codes.update({torch.float32: LS_DTYPE_F32, torch.float16: LS_DTYPE_F16, torch.bfloat16: LS_DTYPE_BF16})
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _ptr(t) -> int | None:
@@ -129,6 +136,10 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
+        # the handle alone, a tenth of the cost of torch.cuda.current_stream()'s object
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -253,31 +264,16 @@ def ls_cache_refresh_inplace(cache, parent, length: int, workspace=None, stream=
         _ptr(workspace), _stream(stream))
 
 
-def _view(t, row: int, pos: int, head: int, layer: int | None = None):
-    """ls_view of tensor t, whose dimensions `row`, `pos`, `head` (and `layer`) are those of the view."""
-    st = t.stride()
-    if t.shape[-1] > 1 and st[-1] != 1:
-        raise ValueError("the last dimension must be contiguous")
-    return _View(t.data_ptr(), st[layer] if layer is not None else 0, st[row], st[pos], st[head])
+# The wrappers of the operators below run once per layer and token, where a small call's time is
+# the host's: each checks its shapes in one expression and asks every tensor for its strides once.
+def _index(t, shape, dtype) -> bool:
+    """A device-side index array: of `shape` and `dtype`, contiguous."""
+    return t.shape == shape and t.dtype is dtype and t.is_contiguous()
 
 
-def _same(what: str, *pairs) -> None:
-    for got, want in pairs:
-        if tuple(got) != tuple(want):
-            raise ValueError(f"{what}: shape {tuple(got)}, expected {tuple(want)}")
-
-
-def _plain(what: str, dtype, *tensors) -> None:
-    """Device-side index arrays: of `dtype` and contiguous."""
-    for t in tensors:
-        if t is not None and (t.dtype != dtype or not t.is_contiguous()):
-            raise ValueError(f"{what}: index arrays must be contiguous {dtype}")
-
-
-def _one_dtype(what: str, *tensors) -> int:
-    if any(t.dtype != tensors[0].dtype for t in tensors):
-        raise ValueError(f"{what}: tensors of different dtypes")
-    return _dtype_code(tensors[0])
+def _refuse(what: str, *tensors) -> None:
+    raise ValueError(f"{what}: shapes, dtypes or layouts do not fit: "
+                     + ", ".join(f"{tuple(t.shape)} {t.dtype} strides {t.stride()}" for t in tensors if t is not None))
 
 
 def ls_cross_attention_workspace_size(batch: int, k: int, q_len: int, heads: int, kv_heads: int, max_src: int,
@@ -292,22 +288,23 @@ def ls_cross_attention(q, key, value, src_len, out, workspace, scale: float | No
     by default.  workspace: ls_cross_attention_workspace_size() bytes."""
     import torch
 
-    batch, k, q_len, heads, dim = q.shape
-    kv_heads, max_src = key.shape[1], key.shape[2]
-    _same("ls_cross_attention", (key.shape, (batch, kv_heads, max_src, dim)), (value.shape, key.shape),
-          (out.shape, q.shape), (src_len.shape, (batch,)))
-    _plain("ls_cross_attention", torch.int32, src_len)
-    code = _one_dtype("ls_cross_attention", q, key, value, out)
-    for t in (q, out):
-        if batch > 1 and k > 1 and t.stride(0) != k * t.stride(1):
-            raise ValueError("ls_cross_attention: batch and k must be one dimension in memory")
-    views = [_View(t.data_ptr(), 0, t.stride(1) if k > 1 else t.stride(0), t.stride(2), t.stride(3)) for t in (q, out)]
-    if any(t.shape[-1] > 1 and t.stride(-1) != 1 for t in (q, out)):
-        raise ValueError("the last dimension must be contiguous")
+    shape, dt = q.shape, q.dtype
+    batch, k, q_len, heads, dim = shape
+    _, kv_heads, max_src, _ = key.shape
+    sq, sk, sv, so = q.stride(), key.stride(), value.stride(), out.stride()
+    flat = batch == 1 or k == 1
+    if not (key.shape == (batch, kv_heads, max_src, dim) and value.shape == key.shape and out.shape == shape
+            and key.dtype is dt and value.dtype is dt and out.dtype is dt and _index(src_len, (batch,), torch.int32)
+            and (dim == 1 or sq[4] == sk[3] == sv[3] == so[4] == 1)
+            and (flat or (sq[0] == k * sq[1] and so[0] == k * so[1]))):
+        _refuse("ls_cross_attention", q, key, value, src_len, out)
+    r = 1 if k > 1 else 0
     return load_library().ls_cross_attention(
-        views[0], _view(key, 0, 2, 1), _view(value, 0, 2, 1), code, _ptr(src_len),
-        float(dim ** -0.5 if scale is None else scale), batch, k, q_len, heads, kv_heads, max_src, dim, views[1],
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        _View(q.data_ptr(), 0, sq[r], sq[2], sq[3]), _View(key.data_ptr(), 0, sk[0], sk[2], sk[1]),
+        _View(value.data_ptr(), 0, sv[0], sv[2], sv[1]), _dtype_code(q), src_len.data_ptr(),
+        dim ** -0.5 if scale is None else scale, batch, k, q_len, heads, kv_heads, max_src, dim,
+        _View(out.data_ptr(), 0, so[r], so[2], so[3]), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def ls_tree_attention_workspace_size(rows: int, nodes: int, heads: int, kv_heads: int, max_len: int,
@@ -324,18 +321,25 @@ def ls_tree_attention(q, cache_key, cache_value, cache_len, draft_key, draft_val
     contiguous).  scale: 1/sqrt(head_dim) by default.  workspace: ls_tree_attention_workspace_size() bytes."""
     import torch
 
-    rows, nodes, heads, dim = q.shape
-    kv_heads, max_len = cache_key.shape[1], cache_key.shape[2]
-    _same("ls_tree_attention", (cache_key.shape, (rows, kv_heads, max_len, dim)), (cache_value.shape, cache_key.shape),
-          (draft_key.shape, (rows, nodes, kv_heads, dim)), (draft_value.shape, draft_key.shape), (out.shape, q.shape),
-          (cache_len.shape, (rows,)), (parent.shape, (rows, nodes)))
-    _plain("ls_tree_attention", torch.int32, cache_len, parent)
-    code = _one_dtype("ls_tree_attention", q, cache_key, cache_value, draft_key, draft_value, out)
+    shape, dt, i32 = q.shape, q.dtype, torch.int32
+    rows, nodes, heads, dim = shape
+    _, kv_heads, max_len, _ = cache_key.shape
+    draft = (rows, nodes, kv_heads, dim)
+    sq, sk, sv, so = q.stride(), cache_key.stride(), cache_value.stride(), out.stride()
+    dk, dv = draft_key.stride(), draft_value.stride()
+    if not (cache_key.shape == (rows, kv_heads, max_len, dim) and cache_value.shape == cache_key.shape
+            and draft_key.shape == draft and draft_value.shape == draft and out.shape == shape
+            and cache_key.dtype is dt and cache_value.dtype is dt and draft_key.dtype is dt and draft_value.dtype is dt
+            and out.dtype is dt and _index(cache_len, (rows,), i32) and _index(parent, (rows, nodes), i32)
+            and (dim == 1 or sq[3] == sk[3] == sv[3] == so[3] == dk[3] == dv[3] == 1)):
+        _refuse("ls_tree_attention", q, cache_key, cache_value, cache_len, draft_key, draft_value, parent, out)
     return load_library().ls_tree_attention(
-        _view(q, 0, 1, 2), _view(cache_key, 0, 2, 1), _view(cache_value, 0, 2, 1), _ptr(cache_len),
-        _view(draft_key, 0, 1, 2), _view(draft_value, 0, 1, 2), _ptr(parent), code,
-        float(dim ** -0.5 if scale is None else scale), rows, nodes, heads, kv_heads, max_len, dim, _view(out, 0, 1, 2),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        _View(q.data_ptr(), 0, sq[0], sq[1], sq[2]), _View(cache_key.data_ptr(), 0, sk[0], sk[2], sk[1]),
+        _View(cache_value.data_ptr(), 0, sv[0], sv[2], sv[1]), cache_len.data_ptr(),
+        _View(draft_key.data_ptr(), 0, dk[0], dk[1], dk[2]), _View(draft_value.data_ptr(), 0, dv[0], dv[1], dv[2]),
+        parent.data_ptr(), _dtype_code(q), dim ** -0.5 if scale is None else scale, rows, nodes, heads, kv_heads, max_len,
+        dim, _View(out.data_ptr(), 0, so[0], so[1], so[2]), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def ls_tree_commit(cache_key, cache_value, cache_len, draft_key, draft_value, parent, token, target, finished,
@@ -347,25 +351,28 @@ def ls_tree_commit(cache_key, cache_value, cache_len, draft_key, draft_value, pa
     int32, out_path [rows, nodes] int32, out_finished [rows] uint8 or None; finished [rows] uint8 or None."""
     import torch
 
+    dt, i32, u8 = cache_key.dtype, torch.int32, torch.uint8
     layers, rows, heads, max_len, dim = cache_key.shape
-    nodes = parent.shape[1]
-    _same("ls_tree_commit", (cache_value.shape, cache_key.shape), (draft_key.shape, (layers, rows, nodes, heads, dim)),
-          (draft_value.shape, draft_key.shape), (cache_len.shape, (rows,)), (parent.shape, (rows, nodes)),
-          (token.shape, parent.shape), (target.shape, parent.shape), (out_len.shape, (rows,)),
-          (out_path.shape, parent.shape), (out_count.shape, (rows,)), (out_token.shape, (rows,)))
-    _plain("ls_tree_commit", torch.int32, cache_len, parent, token, target, out_len, out_path, out_count, out_token)
-    _plain("ls_tree_commit", torch.uint8, finished, out_finished)
-    for t in (finished, out_finished):
-        if t is not None:
-            _same("ls_tree_commit", (t.shape, (rows,)))
-    if not (cache_key.is_contiguous() and cache_value.is_contiguous()):
-        raise ValueError("ls_tree_commit: the caches must be contiguous")
-    code = _one_dtype("ls_tree_commit", cache_key, cache_value, draft_key, draft_value)
+    tree = parent.shape
+    nodes = tree[1]
+    draft, row = (layers, rows, nodes, heads, dim), (rows,)
+    dk, dv = draft_key.stride(), draft_value.stride()
+    if not (cache_value.shape == cache_key.shape and cache_key.is_contiguous() and cache_value.is_contiguous()
+            and draft_key.shape == draft and draft_value.shape == draft and (dim == 1 or dk[4] == dv[4] == 1)
+            and cache_value.dtype is dt and draft_key.dtype is dt and draft_value.dtype is dt and tree[0] == rows
+            and _index(parent, tree, i32) and _index(token, tree, i32) and _index(target, tree, i32)
+            and _index(out_path, tree, i32) and _index(cache_len, row, i32) and _index(out_len, row, i32)
+            and _index(out_count, row, i32) and _index(out_token, row, i32)
+            and (finished is None or _index(finished, row, u8))
+            and (out_finished is None or _index(out_finished, row, u8))):
+        _refuse("ls_tree_commit", cache_key, cache_value, cache_len, draft_key, draft_value, parent, token, target,
+                finished, out_len, out_path, out_count, out_token, out_finished)
     return load_library().ls_tree_commit(
-        _ptr(cache_key), _ptr(cache_value), _ptr(cache_len), _view(draft_key, 1, 2, 3, 0), _view(draft_value, 1, 2, 3, 0),
-        code, _ptr(parent), _ptr(token), _ptr(target), _ptr(finished), int(eos_id), layers, rows, nodes, heads, max_len,
-        dim, _ptr(out_len), _ptr(out_path), _ptr(out_count), _ptr(out_token), _ptr(out_finished), _ptr(workspace),
-        _stream(stream))
+        cache_key.data_ptr(), cache_value.data_ptr(), cache_len.data_ptr(),
+        _View(draft_key.data_ptr(), dk[0], dk[1], dk[2], dk[3]), _View(draft_value.data_ptr(), dv[0], dv[1], dv[2], dv[3]),
+        _dtype_code(cache_key), parent.data_ptr(), token.data_ptr(), target.data_ptr(), _ptr(finished), eos_id, layers,
+        rows, nodes, heads, max_len, dim, out_len.data_ptr(), out_path.data_ptr(), out_count.data_ptr(),
+        out_token.data_ptr(), _ptr(out_finished), _ptr(workspace), _stream(stream))
 
 
 def ls_read_status(workspace, stream=None) -> int:
