@@ -60,7 +60,7 @@ struct Debug {
 
 // LS_BEAM_DEBUG: comma-separated "exact", "ipplain", "iptma", "ipwords", "ipstatic", "steprefresh", "chunk", "strips",
 // "fused", "nofused", "cluster", "nocluster", "spin=<ns>", "vpl=<4|8|16>", "stages=<2..8>", "parts=<n>", "ipw=<words>",
-// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atwarps=<1|4>", "atsplits=<n>".
+// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atstep", "atwarps=<1|4>", "atsplits=<n>".
 Debug read_debug() {
   Debug d;
   const char* env = std::getenv("LS_BEAM_DEBUG");
@@ -92,6 +92,7 @@ Debug read_debug() {
     else if (!std::strcmp(tok, "nocheck")) d.check_ptrs = false;
     else if (!std::strcmp(tok, "atsimt")) d.attend.kernel = kAtForceSimt;
     else if (!std::strcmp(tok, "atmma")) d.attend.kernel = kAtForceMma;
+    else if (!std::strcmp(tok, "atstep")) d.attend.kernel = kAtForceStep;
     else if (!std::strcmp(tok, "attc")) d.attend.kernel = kAtForceTc;
     else if (!std::strncmp(tok, "atwarps=", 8)) d.attend.warps = std::atoi(tok + 8) == 1 ? 1 : 4;
     else if (!std::strncmp(tok, "atsplits=", 9)) d.attend.splits = std::atoi(tok + 9);

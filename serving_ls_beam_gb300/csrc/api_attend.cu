@@ -91,29 +91,37 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.part_ml = reinterpret_cast<float2*>(ws + kAtHeader);
   p.part_o = reinterpret_cast<float*>(p.part_ml + attend_part_rows(p.m));
   const AttendDebug dbg = attend_debug();
-  const bool tensor = dtype != LS_DTYPE_F32 && p.dim % 8 == 0 && vectors16(p.q) && vectors16(p.out) &&
-                      vectors16(p.key) && vectors16(p.value) && vectors16(p.dkey) && vectors16(p.dvalue);
+  const int es = es_of(dtype);
+  const bool lines = p.dim * es % 16 == 0 && vectors16(p.q) && vectors16(p.out) && vectors16(p.key) &&
+                     vectors16(p.value) && vectors16(p.dkey) && vectors16(p.dvalue);
+  const bool tensor = lines && dtype != LS_DTYPE_F32;
   CUtensorMap maps[4];
   const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
                   (dbg.kernel ? dbg.kernel == kAtForceTc : p.m > 32) && encode_maps(maps, p, dtype);
-  const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt;
-  const int mq = tc ? kAtTcQueries : mma ? attend_mma_queries(p.dim, p.m) : attend_simt_queries(dtype, p.m);
+  const bool step = !tc && lines && p.dim * es <= 512 &&
+                    (dbg.kernel ? dbg.kernel == kAtForceStep : dtype == LS_DTYPE_F32 || p.m <= 4);
+  const bool mma = tensor && !tc && !step && dbg.kernel != kAtForceSimt;
+  const int mq = tc     ? kAtTcQueries
+                 : step ? attend_step_queries(dtype, p.m)
+                 : mma  ? attend_mma_queries(p.dim, p.m)
+                        : attend_simt_queries(dtype, p.m);
   p.m_tiles = (p.m + mq - 1) / mq;
+  const long long whole = base * p.m_tiles;
   if (tc) {
     p.negate = p.scale_log2 < 0.0f;
     // a scale of 0 as 2^-100: masked scores stay -inf, and every weight still is exactly 1
     p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
-    p.splits = split_of(p, base * p.m_tiles, kAtSms, 512, dbg.splits);
-  } else if (mma) {
-    const long long whole = base * p.m_tiles;
+    p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
+  } else if (mma || step) {
     p.warps = dbg.warps ? dbg.warps : (whole >= 4 * 2 * kAtSms && p.max_len <= 256 ? 1 : 4);
-    p.splits = p.warps == 1 ? 1 : split_of(p, whole, 2 * kAtSms, 256, dbg.splits);
+    p.splits = p.warps == 1 ? 1 : split_of(p, whole, (mma ? 2 : 4) * kAtSms, mma ? 256 : 128, dbg.splits);
   } else {
-    p.splits = split_of(p, base * p.m_tiles, 4 * kAtSms, 128, dbg.splits);
+    p.splits = split_of(p, whole, 4 * kAtSms, 128, dbg.splits);
   }
   p.items = base * p.m_tiles * p.splits;
   if (p.items > INT_MAX) return LS_ERR_UNSUPPORTED;
   cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
+                  : step ? launch_attend_step(p, dtype, stream)
                   : mma ? launch_attend_mma(p, dtype, stream)
                         : launch_attend_simt(p, dtype, stream);
   if (e == cudaSuccess && p.splits > 1) e = launch_attend_join(p, dtype, stream);

@@ -1,0 +1,350 @@
+// Attention of one to a few queries over a row's keys, for every type: the single-token step,
+// the beams of a sentence, fp32 models.  With at most four queries (eight in f32) per key the
+// products are too thin for the matrix instructions (15 of 16 operand rows would be empty), and
+// what counts is how many bytes are under way and how few instructions a key takes.
+//
+//   s_n = (scale q) . k_n,  o = sum_n 2^(s_n - max) v_n / sum_n 2^(s_n - max)
+//
+// in one pass with the running maximum and sum (Milakov and Gimelshein, 2018), all in f32: the
+// weights are not rounded.
+//
+// Keys and values go straight from memory into registers, 16 bytes per lane and load: LPK lanes
+// hold one vector, so a load instruction covers 32 / LPK keys, and a block is 8 such loads of
+// keys and 8 of values, 8 KB under way per warp.  The keys' registers are loaded again as soon as
+// the block's scores are formed, the values' when its sums are.  The 8 dot products of a lane
+// group are reduced together, each exchange halving the products that a lane still holds (7
+// exchanges instead of 24), which leaves every lane with the score of its own key: one
+// exponential per key, not one per lane.  The drafted tokens follow the row's keys without a gap.
+//
+// A warp takes whole problems in turn (AttendParams::warps 1), or the four warps of a CTA take
+// the blocks of one (part of a) problem in turn and merge through shared memory (4).
+#include "ls_device.cuh"
+#include "ls_dtype.cuh"
+#include "ls_tree.cuh"
+
+namespace lsb {
+namespace {
+
+constexpr int kAsWarps = 4;
+constexpr int kAsThreads = kAsWarps * 32;
+constexpr int kAsLoads = 8;  // loads of keys (and of values) per block
+
+__device__ __forceinline__ uint4 load_stream(const unsigned char* p) {
+  uint4 d;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w) : "l"(p));
+  return d;
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack_vec(const float (&x)[Traits<DT>::kVec]) {
+  uint4 d;
+  if constexpr (DT == DT_F32) {
+    d = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == DT_F16) {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    d = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return d;
+}
+
+// The 8 values of each lane summed over the lanes that differ in bits 0 to 2 (and up to LPK):
+// afterwards lane l holds the sum of value (l & 1) << 2 | (l & 2) | (l >> 2 & 1).
+template <int LPK>
+__device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
+  float a[4], b[2], c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool hi = lane & 1;
+    const float keep = hi ? v[i + 4] : v[i], give = hi ? v[i] : v[i + 4];
+    a[i] = keep + __shfl_xor_sync(~0u, give, 1);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool hi = lane & 2;
+    const float keep = hi ? a[i + 2] : a[i], give = hi ? a[i] : a[i + 2];
+    b[i] = keep + __shfl_xor_sync(~0u, give, 2);
+  }
+  {
+    const bool hi = lane & 4;
+    const float keep = hi ? b[1] : b[0], give = hi ? b[0] : b[1];
+    c = keep + __shfl_xor_sync(~0u, give, 4);
+  }
+#pragma unroll
+  for (int x = 8; x < LPK; x <<= 1) c += __shfl_xor_sync(~0u, c, x);
+  return c;
+}
+
+template <int DT, int LPK, int MQ>
+__global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendParams p) {
+  constexpr int E = Traits<DT>::kVec, ES = Traits<DT>::kBytes, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
+  __shared__ TreeSeen trees[kAsWarps];
+  __shared__ float wm[kAsWarps][MQ], wl[kAsWarps][MQ];
+  __shared__ float acc[kAsWarps][MQ][LPK * E + 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPK, gk = lane / LPK;
+  const int W = p.warps, wi = W == 1 ? 0 : warp;
+  const bool cv = c < p.dim / E;  // this lane holds a part of the vectors
+  const int my_u = (lane & 1) << 2 | (lane & 2) | (lane >> 2 & 1);
+  TreeSeen& tree = trees[warp];
+  const long long stride = W == 1 ? (long long)gridDim.x * kAsWarps : gridDim.x;
+  long long it = W == 1 ? (long long)blockIdx.x * kAsWarps + warp : blockIdx.x;
+  const long long per_row = (long long)p.splits * p.m_tiles * p.kv_heads;
+  int next_len = it < p.items ? __ldg(p.len + it / per_row) : 0;
+  for (; it < p.items; it += stride) {
+    const int r = (int)(it / per_row);
+    int e = (int)(it - r * per_row);
+    const int split = e % p.splits;
+    e /= p.splits;
+    const int i0 = (e % p.m_tiles) * MQ, h = e / p.m_tiles;
+    const int nq = min(MQ, p.m - i0);
+    const int len = min(max(next_len, 0), p.max_len);
+    if (len != next_len && lane == 0) atomicOr(p.status, kDevInternal);
+    if (it + stride < p.items) next_len = __ldg(p.len + (it + stride) / per_row);
+    const int total = len + p.nodes, nbt = (total + KB - 1) / KB, per = (nbt + p.splits - 1) / p.splits;
+    const int lo = min(split * per, nbt), hi = min(lo + per, nbt);
+    int b = lo + wi;
+
+    const unsigned char* kb = p.key.data + (long long)r * p.key.row + (long long)h * p.key.head + c * 16;
+    const unsigned char* vb = p.value.data + (long long)r * p.value.row + (long long)h * p.value.head + c * 16;
+    const unsigned char* dkb = p.dkey.data + (long long)r * p.dkey.row + (long long)h * p.dkey.head + c * 16;
+    const unsigned char* dvb = p.dvalue.data + (long long)r * p.dvalue.row + (long long)h * p.dvalue.head + c * 16;
+    auto fetch = [&](uint4(&d)[U], int blk, const unsigned char* cache, long long pos, const unsigned char* draft,
+                     long long dpos) {
+      const int j0 = blk * KB + gk;
+      if (blk * KB + KB <= len) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          d[u] = cv ? load_stream(cache + (long long)(j0 + u * KPL) * pos) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * KPL;
+          const unsigned char* at = j < len ? cache + (long long)j * pos : draft + (long long)(j - len) * dpos;
+          d[u] = cv && j < total && blk < hi ? load_stream(at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    };
+    uint4 kr[U], vr[U];
+    if (b < hi) {
+      fetch(kr, b, kb, p.key.pos, dkb, p.dkey.pos);
+      fetch(vr, b, vb, p.value.pos, dvb, p.dvalue.pos);
+    }
+    float q[MQ][E];
+#pragma unroll
+    for (int j = 0; j < MQ; ++j) {
+      const unsigned char* src = p.q.data + query_offset(p, p.q, r, h, i0 + min(j, nq - 1)) + c * 16;
+      const uint4 d = cv ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+      unpack<DT>(d, q[j]);
+#pragma unroll
+      for (int x = 0; x < E; ++x) q[j][x] *= p.scale_log2;
+    }
+    unsigned alive = ~0u;
+    if (p.nodes) {
+      __syncwarp();
+      if (tree_seen(tree, p.parent + (long long)r * p.nodes, p.nodes, lane, 32, [] { __syncwarp(); }))
+        atomicOr(p.status, kDevInternal);
+      alive = 0;
+#pragma unroll
+      for (int j = 0; j < MQ; ++j)
+        if (j < nq && tree.mask[(i0 + j) / p.group]) alive |= 1u << j;
+    }
+    float m[MQ], l[MQ], o[MQ][E];
+#pragma unroll
+    for (int j = 0; j < MQ; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < E; ++x) o[j][x] = 0.0f;
+    }
+    for (; b < hi; b += W) {
+      float part[MQ][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float k[E];
+        unpack<DT>(kr[u], k);
+#pragma unroll
+        for (int j = 0; j < MQ; ++j) {
+          float2 a = __fmul2_rn(make_float2(q[j][0], q[j][1]), make_float2(k[0], k[1]));
+#pragma unroll
+          for (int x = 2; x < E; x += 2) a = __ffma2_rn(make_float2(q[j][x], q[j][x + 1]), make_float2(k[x], k[x + 1]), a);
+          part[j][u] = a.x + a.y;
+        }
+      }
+      if (b + W < hi) fetch(kr, b + W, kb, p.key.pos, dkb, p.dkey.pos);
+      const int key = b * KB + my_u * KPL + gk;  // this lane's key
+      const bool edge = b * KB + KB > len;
+      float w[MQ];
+#pragma unroll
+      for (int j = 0; j < MQ; ++j) {
+        float s = reduce8<LPK>(part[j], lane);
+        bool sees = (alive >> j) & 1u;
+        if (edge) {
+          if (key >= len) sees = sees && key < total && (tree.mask[(i0 + min(j, nq - 1)) / p.group] >> (key - len) & 1ull);
+        }
+        s = sees ? s : -INFINITY;
+        float bm = s;
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, x));
+#pragma unroll
+        for (int x = LPK; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, x));
+        const float mn = fmaxf(m[j], bm), sub = mn == -INFINITY ? 0.0f : mn;
+        w[j] = fast_exp2(s - sub);
+        if (mn > m[j]) {  // the same in every lane
+          const float f = fast_exp2(m[j] - sub);
+          l[j] *= f;
+#pragma unroll
+          for (int x = 0; x < E; ++x) o[j][x] *= f;
+          m[j] = mn;
+        }
+        l[j] += w[j];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float v[E];
+        unpack<DT>(vr[u], v);
+        const int from = gk * LPK + ((u >> 2) | (u & 2) | (u & 1) << 2);
+#pragma unroll
+        for (int j = 0; j < MQ; ++j) {
+          const float wu = __shfl_sync(~0u, w[j], from);
+          // a drafted value that the query does not see may be anything: left out, not times 0
+          if (!edge || wu != 0.0f) {
+#pragma unroll
+            for (int x = 0; x < E; x += 2) {
+              const float2 y = __ffma2_rn(make_float2(wu, wu), make_float2(v[x], v[x + 1]), make_float2(o[j][x], o[j][x + 1]));
+              o[j][x] = y.x;
+              o[j][x + 1] = y.y;
+            }
+          }
+        }
+      }
+      if (b + W < hi) fetch(vr, b + W, vb, p.value.pos, dvb, p.dvalue.pos);
+    }
+    // over the lane groups
+#pragma unroll
+    for (int j = 0; j < MQ; ++j) {
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], x);
+#pragma unroll
+      for (int x = LPK; x < 32; x <<= 1) {
+        l[j] += __shfl_xor_sync(~0u, l[j], x);
+#pragma unroll
+        for (int y = 0; y < E; ++y) o[j][y] += __shfl_xor_sync(~0u, o[j][y], x);
+      }
+    }
+    if (W == 1) {  // never split
+#pragma unroll
+      for (int j = 0; j < MQ; ++j) {
+        if (j < nq && gk == j % KPL && cv) {
+          float y[E];
+          const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
+#pragma unroll
+          for (int x = 0; x < E; ++x) y[x] = l[j] == 0.0f ? 0.0f : o[j][x] * inv;
+          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + c * 16) = pack_vec<DT>(y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < MQ; ++j) {
+        if (lane == 0) {
+          wm[warp][j] = m[j];
+          wl[warp][j] = l[j];
+        }
+        if (gk == j % KPL) {
+#pragma unroll
+          for (int x = 0; x < E; x += 4)
+            *reinterpret_cast<float4*>(&acc[warp][j][c * E + x]) = make_float4(o[j][x], o[j][x + 1], o[j][x + 2], o[j][x + 3]);
+        }
+      }
+      __syncthreads();
+      for (int e2 = threadIdx.x; e2 < nq * (p.dim / E); e2 += kAsThreads) {
+        const int j = e2 / (p.dim / E), x0 = (e2 - j * (p.dim / E)) * E;
+        float M = wm[0][j];
+#pragma unroll
+        for (int w2 = 1; w2 < kAsWarps; ++w2) M = fmaxf(M, wm[w2][j]);
+        const float sub = M == -INFINITY ? 0.0f : M;
+        float L = 0.0f, y[E];
+#pragma unroll
+        for (int x = 0; x < E; ++x) y[x] = 0.0f;
+#pragma unroll
+        for (int w2 = 0; w2 < kAsWarps; ++w2) {
+          const float lw = wl[w2][j], f = fast_exp2(wm[w2][j] - sub);
+          L = fmaf(f, lw, L);
+#pragma unroll
+          for (int x = 0; x < E; ++x) y[x] = add_part(y[x], f, acc[w2][j][x0 + x], lw);
+        }
+        if (p.splits == 1) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+          for (int x = 0; x < E; ++x) y[x] = L == 0.0f ? 0.0f : y[x] * inv;
+          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + x0 * ES) = pack_vec<DT>(y);
+        } else {
+          const long long row = (((long long)r * p.kv_heads + h) * p.m + i0 + j) * p.splits + split;
+#pragma unroll
+          for (int x = 0; x < E; x += 4)
+            *reinterpret_cast<float4*>(p.part_o + row * p.dim + x0 + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+          if (x0 == 0) p.part_ml[row] = make_float2(M, L);
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int LPK, int MQ>
+cudaError_t run_step(const AttendParams& p, cudaStream_t stream) {
+  long long grid = p.items;
+  if (p.warps == 1) {
+    static int occ = 0;
+    if (occ == 0) {
+      int n = 0;
+      const cudaError_t e =
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attend_step_kernel<DT, LPK, MQ>, kAsThreads, 0);
+      if (e != cudaSuccess) return e;
+      occ = n > 0 ? n : 1;
+    }
+    const long long need = (p.items + kAsWarps - 1) / kAsWarps, fit = (long long)kAtSms * occ;
+    grid = need < fit ? need : fit;
+  }
+  attend_step_kernel<DT, LPK, MQ><<<(unsigned)grid, kAsThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT, int LPK>
+cudaError_t run_step_queries(const AttendParams& p, cudaStream_t stream) {
+  switch (attend_step_queries(DT, p.m)) {
+    case 1: return run_step<DT, LPK, 1>(p, stream);
+    case 2: return run_step<DT, LPK, 2>(p, stream);
+    case 4: return run_step<DT, LPK, 4>(p, stream);
+    default: break;
+  }
+  if constexpr (DT == DT_F32) return run_step<DT, LPK, 8>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+template <int DT>
+cudaError_t run_step_dim(const AttendParams& p, cudaStream_t stream) {
+  const int chunks = p.dim / Traits<DT>::kVec;
+  if (chunks <= 8) return run_step_queries<DT, 8>(p, stream);
+  if (chunks <= 16) return run_step_queries<DT, 16>(p, stream);
+  return run_step_queries<DT, 32>(p, stream);
+}
+
+}  // namespace
+
+int attend_step_queries(int dtype, int m) { return m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 || dtype != DT_F32 ? 4 : 8; }
+
+cudaError_t launch_attend_step(const AttendParams& p, int dtype, cudaStream_t stream) {
+  if (dtype == DT_F32) return run_step_dim<DT_F32>(p, stream);
+  if (dtype == DT_F16) return run_step_dim<DT_F16>(p, stream);
+  return run_step_dim<DT_BF16>(p, stream);
+}
+
+}  // namespace lsb

@@ -38,7 +38,7 @@ struct AttendParams {
   int tokens;             // beams * q_len
   int m;                  // tokens * group
   int m_tiles;            // ceil(m / queries per CTA or warp)
-  int warps;              // attend_mma.cu: warps per item (1 or 4)
+  int warps;              // attend_step.cu, attend_mma.cu: warps per item (1 or 4)
   int splits;             // parts of a row's keys (each a CTA's); > 1: partial results
   float* part_o;          // [problem, m, split, dim] f32
   float2* part_ml;        // [problem, m, split]: maximum (log2 units) and sum
@@ -89,6 +89,9 @@ inline cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t>&
 
 cudaError_t launch_attend_simt(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_simt_queries(int dtype, int m);  // queries per CTA
+// every stride and address a multiple of 16 bytes, vectors of at most 512 bytes
+cudaError_t launch_attend_step(const AttendParams& p, int dtype, cudaStream_t stream);
+int attend_step_queries(int dtype, int m);  // queries per item
 // f16 / bf16, every stride and address a multiple of 16 bytes
 cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_mma_queries(int dim, int m);  // queries per item
@@ -103,7 +106,7 @@ cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
 bool pointers_reachable(const void* const* ptrs, int n);  // nulls are skipped
 long long wait_limit_ns();
 // LS_BEAM_DEBUG's choice of the attention kernel: 0 = the plan's, else one of these
-constexpr int kAtForceSimt = 1, kAtForceMma = 2, kAtForceTc = 3;
+constexpr int kAtForceSimt = 1, kAtForceMma = 2, kAtForceTc = 3, kAtForceStep = 4;
 struct AttendDebug {
   int kernel, warps, splits;
 };

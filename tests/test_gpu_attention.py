@@ -13,7 +13,7 @@ import serving_ls_beam_gb300 as lsb  # noqa: E402
 
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 KERNELS = [None, "atsimt", "atmma,atwarps=1", "atmma,atwarps=4", "atmma,atwarps=4,atsplits=3",
-           "attc", "attc,atsplits=3"]
+           "attc", "attc,atsplits=3", "atstep,atwarps=1", "atstep,atwarps=4,atsplits=3"]
 
 
 @pytest.fixture(scope="module")
