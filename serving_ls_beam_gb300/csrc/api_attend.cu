@@ -63,16 +63,8 @@ bool vectors16(const AtView& v) {
 
 // The tensor-core kernel's tensor maps: key, value and the drafted ones (copies of the key's
 // where there are none).  False where a map cannot describe the tensors.
-bool encode_maps(CUtensorMap (&maps)[4], AttendParams& p, int dtype) {
-  p.kv_row_one = p.rows > 1 && p.key.row == 0;
-  p.kv_head_one = p.kv_heads > 1 && p.key.head == 0;
-  // a stride of 0 means one element: the same for keys and values, or no map
-  if ((p.value.row == 0) != (p.key.row == 0) || (p.value.head == 0) != (p.key.head == 0)) return false;
-  if (p.max_len > 1 && (p.key.pos == 0 || p.value.pos == 0)) return false;
-  const int rows = p.kv_row_one ? 1 : p.rows, heads = p.kv_head_one ? 1 : p.kv_heads;
-  if (!encode_attend(&maps[0], p.key, dtype, p.dim, p.max_len, heads, rows, kAtTcBox) ||
-      !encode_attend(&maps[1], p.value, dtype, p.dim, p.max_len, heads, rows, kAtTcBox))
-    return false;
+bool encode_maps(CUtensorMap (&maps)[4], const AttendParams& p, int dtype) {
+  if (!encode_keys(maps, p, dtype, kAtTcBox)) return false;
   maps[2] = maps[0];
   maps[3] = maps[1];
   if (!p.nodes) return true;
@@ -92,15 +84,18 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.part_o = reinterpret_cast<float*>(p.part_ml + attend_part_rows(p.m));
   const AttendDebug dbg = attend_debug();
   const int es = es_of(dtype);
-  const bool lines = p.dim * es % 16 == 0 && vectors16(p.q) && vectors16(p.out) && vectors16(p.key) &&
+  // whole 16-byte vectors, and steps from key to key that 32 bits hold
+  const bool lines = p.dim * es % 16 == 0 && p.key.pos < INT_MAX && p.value.pos < INT_MAX && vectors16(p.q) && vectors16(p.out) && vectors16(p.key) &&
                      vectors16(p.value) && vectors16(p.dkey) && vectors16(p.dvalue);
   const bool tensor = lines && dtype != LS_DTYPE_F32;
+  p.kv_row_one = p.rows > 1 && p.key.row == 0;
+  p.kv_head_one = p.kv_heads > 1 && p.key.head == 0;
   CUtensorMap maps[4];
   const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
                   (dbg.kernel ? dbg.kernel == kAtForceTc : p.m > 32) && encode_maps(maps, p, dtype);
   const bool step = !tc && lines && p.dim * es <= 512 &&
-                    (dbg.kernel ? dbg.kernel == kAtForceStep : dtype == LS_DTYPE_F32 || p.m <= 4);
-  const bool mma = tensor && !tc && !step && dbg.kernel != kAtForceSimt;
+                    (dbg.kernel ? dbg.kernel == kAtForceStep : dtype == LS_DTYPE_F32);
+  const bool mma = tensor && !tc && !step && dbg.kernel != kAtForceSimt && maps_describe(p);
   const int mq = tc     ? kAtTcQueries
                  : step ? attend_step_queries(dtype, p.m)
                  : mma  ? attend_mma_queries(p.dim, p.m)
@@ -120,6 +115,11 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   }
   p.items = base * p.m_tiles * p.splits;
   if (p.items > INT_MAX) return LS_ERR_UNSUPPORTED;
+  p.by_split.set(p.splits);
+  p.by_tile.set(p.m_tiles);
+  p.by_head.set(p.kv_heads);
+  p.by_group.set(p.group);
+  p.by_q_len.set(p.q_len);
   cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
                   : step ? launch_attend_step(p, dtype, stream)
                   : mma ? launch_attend_mma(p, dtype, stream)
@@ -129,6 +129,24 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
 }
 
 }  // namespace
+
+namespace lsb {
+
+bool maps_describe(const AttendParams& p) {
+  // a stride of 0 means one element: the same for keys and values, or no map
+  if ((p.value.row == 0) != (p.key.row == 0) || (p.value.head == 0) != (p.key.head == 0)) return false;
+  for (const AtView& v : {p.key, p.value})
+    if (v.row >= 1ll << 40 || v.pos >= 1ll << 40 || v.head >= 1ll << 40) return false;
+  return p.max_len <= 1 || (p.key.pos > 0 && p.value.pos > 0);
+}
+
+bool encode_keys(CUtensorMap* maps, const AttendParams& p, int dtype, int box) {
+  const int rows = p.kv_row_one ? 1 : p.rows, heads = p.kv_head_one ? 1 : p.kv_heads;
+  return maps_describe(p) && encode_attend(&maps[0], p.key, dtype, p.dim, p.max_len, heads, rows, box) &&
+         encode_attend(&maps[1], p.value, dtype, p.dim, p.max_len, heads, rows, box);
+}
+
+}  // namespace lsb
 
 extern "C" {
 

@@ -1,20 +1,24 @@
-// Attention of few queries over a row's keys (f16 / bf16): the decode step, small trees, beams
-// of a sentence.  With M queries per key the products take M flops per byte of keys and values
-// read, far below what the tensor cores need to be the limit, so this kernel is built around
-// the stream of keys and values from memory and uses the warp-level matrix instructions
-// (m16n8k16, f32 accumulators), whose 16-row operand fits 1 to 16 (or two of them 32) queries
-// and whose accumulators stay in registers.
+// Attention of few queries over a row's keys (f16 / bf16): the decode step with shared key
+// heads, small trees, the beams of a sentence.  With M queries per key the products take M flops
+// per byte of keys and values read, far below what the tensor cores need to be the limit, so this
+// kernel is built around the stream of keys and values from memory and uses the warp-level
+// matrix instructions (m16n8k16, f32 accumulators in registers).
 //
-//   S = Q K^T,  P = exp2(c S - max),  O = O * correction + P V,  out = O / sum P
+//   S^T = K Q^T,  P = exp2(c S - max),  O^T = O^T * correction + V^T P^T,  out = O / sum P
 //
 // in one pass with the running maximum and sum of the softmax (Milakov and Gimelshein, 2018).
-// P is rounded to the tensors' type for the second product (its error averages out over the
-// keys like the values' own rounding); the sums use the unrounded f32 weights.
+// The products are taken transposed, keys (and head elements) as the instruction's 16 rows and
+// queries as its 8 columns, so that 1 to 8 queries fill what 16 rows would leave empty: half the
+// instructions and accumulators.  P is rounded to the tensors' type for the second product (its
+// error averages out over the keys like the values' own rounding) and turned into that product's
+// operand by an 8 x 8 transpose in registers; the sums use the unrounded f32 weights.
 //
-// A warp streams blocks of KB keys and their values through a ring of its own in shared memory
-// by 16-byte asynchronous copies (zero-filled past the row's keys, so nothing there reaches a
-// product), rows XOR-swizzled for conflict-free ldmatrix; no CTA barrier in the stream.  Two
-// ways to share the work out, by AttendParams::warps:
+// A warp streams blocks of KB keys and their values through a ring of its own in shared memory,
+// no CTA barrier in the stream: whole blocks by TMA (one lane, a mbarrier per ring slot, the
+// 128-byte swizzle for conflict-free ldmatrix), a row's last block by 16-byte asynchronous
+// copies of all lanes into the same layout.  There the drafted tokens follow the row's keys
+// without a gap, and zeros fill the block, so that nothing past the row's end reaches a product.
+// Two ways to share the work out, by AttendParams::warps:
 //   1: a warp takes whole problems, one after the other, and its ring runs ahead into the next
 //      problem (its queries and parents come through the ring as well), so that short rows
 //      stream without a gap;
@@ -22,6 +26,7 @@
 //      results in shared memory.
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"
+#include "ls_tc.cuh"
 #include "ls_tree.cuh"
 
 namespace lsb {
@@ -29,9 +34,10 @@ namespace {
 
 constexpr int kMmWarps = 4;
 constexpr int kMmThreads = kMmWarps * 32;
+constexpr long long kMmDrainNs = 2000000000LL;
 
-__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // bytes read; the rest of the 16 are zeros
+// 16 bytes to shared memory, n of them read (16 or 0) and the rest zeros
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
@@ -103,57 +109,68 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool* hit) {
   return w;
 }
 
-template <int DP, int MT>
+// The 8 x 8 matrix of 16-bit values whose row g lane (g, t) holds two of, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int DP, int NQ>
 struct MmaShape {
-  static constexpr int KB = DP == 64 ? 32 : 16;   // keys per block
-  static constexpr int NS = DP == 256 ? 2 : 3;    // blocks in the ring
-  static constexpr int ROW = DP * 2;              // bytes of a staged vector
-  static constexpr int STAGE = 2 * KB * ROW;
-  static constexpr bool QREG = MT == 1 && DP <= 128;  // the queries' fragments stay in registers
+  static constexpr int KB = DP == 64 ? 32 : 16;        // keys per block
+  static constexpr int NS = 2;                         // blocks in the ring
+  static constexpr int PANELS = DP / 64;
+  static constexpr int PANEL = KB * 128;               // a block's rows of 64 elements
+  static constexpr int STAGE = 2 * PANELS * PANEL;     // keys, then values
+  static constexpr bool QREG = NQ * DP <= 256;         // the queries' fragments stay in registers
+  static constexpr int CTAS = NQ * DP <= 64 ? 4 : NQ * DP <= 128 ? 3 : 2;  // per SM, by registers
 };
 
-// Bytes of one warp's shared memory, and where its parts begin.
+// Bytes of one warp's shared memory after its ring, and where the parts begin.  With four warps
+// to an item there is one item, otherwise one set of queries and parents per ring slot.
 struct MmaSmem {
-  int q, q_one, par, tree, total;
+  int bars, q, q_one, q_row, par, par_one, tree, total;
 };
-template <int DP, int MT>
-__host__ __device__ inline MmaSmem mma_smem(int m, int nodes) {
-  using S = MmaShape<DP, MT>;
+template <int DP, int NQ>
+__host__ __device__ inline MmaSmem mma_smem(int m, int nodes, int warps) {
+  using S = MmaShape<DP, NQ>;
+  const int sets = warps == 1 ? S::NS : 1;
   MmaSmem s;
-  s.q = S::NS * S::STAGE;
-  s.q_one = (S::QREG && m < 16 ? m : 16 * MT) * S::ROW;
-  s.par = s.q + S::NS * s.q_one;
-  const int np = (nodes + 3) / 4 * 16;
-  s.tree = s.par + S::NS * np;
-  s.total = (s.tree + (nodes ? (int)sizeof(TreeSeen) : 0) + 127) / 128 * 128;
+  s.bars = 0;
+  s.q = 16 * ((S::NS * 8 + 15) / 16);
+  s.q_row = DP * 2 + 16;  // padded: eight queries' vectors in distinct banks
+  s.q_one = (S::QREG && m < 8 * NQ ? m : 8 * NQ) * s.q_row;
+  s.par = s.q + sets * s.q_one;
+  s.par_one = (nodes + 3) / 4 * 16;
+  s.tree = s.par + sets * s.par_one;
+  s.total = (s.tree + tree_bytes(nodes) + 15) / 16 * 16;
   return s;
 }
-
-// One item: the problem, the first of its queries, and the blocks [b, b_end) (step) of this warp.
-struct MmaItem {
-  int r, h, i0, nq, split, len, nb, b, b_end;
-};
-
-template <int DP, int MT>
-__device__ __forceinline__ int item_row(const AttendParams& p, long long it) {
-  return (int)(it / ((long long)p.splits * p.m_tiles * p.kv_heads));
+template <int DP, int NQ>
+inline int mma_smem_bytes(int m, int nodes, int warps) {
+  return kMmWarps * (MmaShape<DP, NQ>::NS * MmaShape<DP, NQ>::STAGE + mma_smem<DP, NQ>(m, nodes, warps).total) + 1024;
 }
 
-template <int DP, int MT>
-__device__ __forceinline__ MmaItem open_item(const AttendParams& p, long long it, int len, int w) {
-  constexpr int KB = MmaShape<DP, MT>::KB;
+// One item: the problem, the first of its queries, and the blocks b, b + W, .. < b_end of this
+// warp over the row's keys and drafted tokens.
+struct MmaItem {
+  int r, h, i0, nq, split, len, b, b_end;
+};
+
+template <int KB, int NQ>
+__device__ __forceinline__ MmaItem open_item(const AttendParams& p, int it, int len, int w) {
   MmaItem x;
-  x.split = (int)(it % p.splits);
-  it /= p.splits;
-  x.i0 = (int)(it % p.m_tiles) * 16 * MT;
-  it /= p.m_tiles;
-  x.h = (int)(it % p.kv_heads);
-  x.r = (int)(it / p.kv_heads);
-  x.nq = min(16 * MT, p.m - x.i0);
+  const int a = p.by_split(it);
+  x.split = it - a * p.splits;
+  const int b = p.by_tile(a);
+  x.i0 = (a - b * p.m_tiles) * 8 * NQ;
+  x.r = p.by_head(b);
+  x.h = b - x.r * p.kv_heads;
+  x.nq = min(8 * NQ, p.m - x.i0);
   x.len = min(max(len, 0), p.max_len);
-  x.nb = (x.len + KB - 1) / KB;
-  const int nbt = x.nb + (p.nodes + KB - 1) / KB;
-  const int per = (nbt + p.splits - 1) / p.splits;
+  const int nbt = (x.len + p.nodes + KB - 1) / KB;
+  const int per = p.splits == 1 ? nbt : (nbt + p.splits - 1) / p.splits;
   const int lo = min(x.split * per, nbt);
   x.b = lo + w;
   x.b_end = min(lo + per, nbt);
@@ -161,64 +178,92 @@ __device__ __forceinline__ MmaItem open_item(const AttendParams& p, long long it
   if (x.b >= x.b_end) x.b = x.b_end = -1;
   return x;
 }
+__device__ __forceinline__ int item_row(const AttendParams& p, int it) { return p.by_head(p.by_tile(p.by_split(it))); }
 
-template <bool BF, int DP, int MT>
-__global__ void __launch_bounds__(kMmThreads) attend_mma_kernel(const AttendParams p) {
-  using S = MmaShape<DP, MT>;
-  constexpr int KB = S::KB, NS = S::NS, ROW = S::ROW, NT = KB / 8, DT = BF ? DT_BF16 : DT_F16;
+template <bool BF, int DP, int NQ>
+__global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
+    attend_mma_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                      const AttendParams p) {
+  using S = MmaShape<DP, NQ>;
+  constexpr int KB = S::KB, NS = S::NS, KT = KB / 16, DT = BF ? DT_BF16 : DT_F16;
+  constexpr int CPR = DP / 8, RPI = 32 / CPR;  // 16-byte vectors of a row; rows per copy instruction
   extern __shared__ unsigned char mm_raw[];
-  __shared__ float wm[kMmWarps][16 * MT], wl[kMmWarps][16 * MT];
+  __shared__ float wm[kMmWarps][8 * NQ], wl[kMmWarps][8 * NQ];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const MmaSmem sm = mma_smem<DP, MT>(p.m, p.nodes);
-  unsigned char* mine = mm_raw + warp * sm.total;
+  const int W = p.warps, wi = W == 1 ? 0 : warp, sets = W == 1 ? NS : 1;
+  const MmaSmem sm = mma_smem<DP, NQ>(p.m, p.nodes, W);
+  const uint32_t raw = smem_addr(mm_raw), rings = (raw + 1023u) & ~1023u;  // the swizzle's period
+  const uint32_t ring = rings + warp * NS * S::STAGE;
+  unsigned char* mine = mm_raw + (rings - raw) + kMmWarps * NS * S::STAGE + warp * sm.total;
   const uint32_t base = smem_addr(mine);
-  TreeSeen& tree = *reinterpret_cast<TreeSeen*>(mine + sm.tree);
-  const int np = (p.nodes + 3) / 4 * 16;
-  const int W = p.warps, wi = W == 1 ? 0 : warp;
-  const int chunks = p.dim / 8;         // 16-byte vectors of a key
-  const int kd = (p.dim + 15) / 16;     // k steps of the first product
-  const long long stride = W == 1 ? (long long)gridDim.x * kMmWarps : gridDim.x;
-  const long long first = W == 1 ? (long long)blockIdx.x * kMmWarps + warp : blockIdx.x;
+  const TreeSeen tree = tree_at(mine + sm.tree, p.nodes);
+  const int chunks = p.dim / 8;
+  const int kd = (p.dim + 15) / 16;  // 16-element steps of a head
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(base + sm.bars + 8 * i, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  // of a block in panels of 64 elements: byte offset of 16-byte vector c of row r
+  auto at = [&](int r, int c) { return (uint32_t)((c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
+  const int items = (int)p.items;
+  const int stride = W == 1 ? (int)gridDim.x * kMmWarps : (int)gridDim.x;
+  const int first = W == 1 ? (int)blockIdx.x * kMmWarps + warp : (int)blockIdx.x;
 
   // ---- the ring's filling side: item `fi` (its length loaded one item ahead), block `fx.b`
-  long long fi = first;
-  int f_seq = 0, f_slot = 0;
+  const int fc = lane % CPR, fr = lane / CPR;  // this lane's vector of a row, and its row of a copy
+  const bool fcv = fc < chunks;
+  const int fsz = fcv ? 16 : 0, fo = fcv ? fc * 16 : 0;
+  int fi = first, f_seq = 0, f_slot = 0;
   bool f_new = true;
   MmaItem fx{};
-  int f_len = fi < p.items ? __ldg(p.len + item_row<DP, MT>(p, fi)) : 0;
+  int f_len = fi < items ? __ldg(p.len + item_row(p, fi)) : 0;
+  bool timed_out = false;
   auto fill = [&]() {
-    if (fi < p.items) {
+    if (fi < items && !timed_out) {
       if (f_new) {
-        fx = open_item<DP, MT>(p, fi, f_len, wi);
-        const long long nx = fi + stride;
-        if (nx < p.items) f_len = __ldg(p.len + item_row<DP, MT>(p, nx));
+        fx = open_item<KB, NQ>(p, fi, f_len, wi);
+        if (fi + stride < items) f_len = __ldg(p.len + item_row(p, fi + stride));
         const uint32_t qd = base + sm.q + f_seq * sm.q_one;
-        for (int e = lane; e < fx.nq * (DP / 8); e += 32) {
-          const int i = e / (DP / 8), c = e % (DP / 8);
-          const unsigned char* src = p.q.data + query_offset(p, p.q, fx.r, fx.h, fx.i0 + i);
-          cp_async16_fill(qd + i * ROW + ((c ^ (i & 7)) << 4), src + (c < chunks ? c * 16 : 0), c < chunks);
-        }
+        for (int i = fr; i < fx.nq; i += RPI)
+          cp_async16_fill(qd + i * sm.q_row + fc * 16, p.q.data + query_offset(p, p.q, fx.r, fx.h, fx.i0 + i) + fo, fsz);
         for (int i = lane; i < p.nodes; i += 32)
-          cp_async4(base + sm.par + f_seq * np + i * 4, p.parent + (long long)fx.r * p.nodes + i);
-        f_seq = f_seq + 1 == NS ? 0 : f_seq + 1;
+          cp_async4(base + sm.par + f_seq * sm.par_one + i * 4, p.parent + (long long)fx.r * p.nodes + i);
+        f_seq = f_seq + 1 == sets ? 0 : f_seq + 1;
         f_new = false;
       }
-      const bool draft = fx.b >= fx.nb;
-      const int n0 = fx.b < 0 ? 0 : (draft ? fx.b - fx.nb : fx.b) * KB;
-      const int n = fx.b < 0 ? 0 : (draft ? p.nodes : fx.len) - n0;  // keys of the block, if below KB
-      const AtView& kv = draft ? p.dkey : p.key;
-      const AtView& vv = draft ? p.dvalue : p.value;
-      const unsigned char* ks = kv.data + (long long)fx.r * kv.row + (long long)fx.h * kv.head + (long long)n0 * kv.pos;
-      const unsigned char* vs = vv.data + (long long)fx.r * vv.row + (long long)fx.h * vv.head + (long long)n0 * vv.pos;
-      const uint32_t kd_ = base + f_slot * S::STAGE, vd_ = kd_ + KB * ROW;
-      constexpr int CPR = DP / 8;
+      const uint32_t kd_ = ring + f_slot * S::STAGE, vd_ = kd_ + S::PANELS * S::PANEL;
+      if (fx.b >= 0 && fx.b * KB + KB <= fx.len) {
+        if (lane == 0) {
+          const uint32_t bar = base + sm.bars + 8 * f_slot;
+          const int h = p.kv_head_one ? 0 : fx.h, r = p.kv_row_one ? 0 : fx.r;
+          // the slot's last contents may have come by the lanes' own copies and stores
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive_expect_tx(bar, S::STAGE);
 #pragma unroll
-      for (int u = 0; u < KB * CPR / 32; ++u) {
-        const int e = u * 32 + lane, row = e / CPR, c = e % CPR;
-        const bool ok = row < n && c < chunks;
-        const uint32_t off = row * ROW + ((c ^ (row & 7)) << 4);
-        cp_async16_fill(kd_ + off, ok ? ks + row * kv.pos + c * 16 : p.q.data, ok);
-        cp_async16_fill(vd_ + off, ok ? vs + row * vv.pos + c * 16 : p.q.data, ok);
+          for (int c = 0; c < S::PANELS; ++c) {
+            tma_load_4d(kd_ + c * S::PANEL, &map_k, c * 64, fx.b * KB, h, r, bar);
+            tma_load_4d(vd_ + c * S::PANEL, &map_v, c * 64, fx.b * KB, h, r, bar);
+          }
+        }
+      } else {  // the row's last block: its drafted tokens, then zeros
+        const int total = fx.b >= 0 ? fx.len + p.nodes : 0;
+        const int j0 = fx.b * KB + fr;
+        const unsigned char* fk = p.key.data + (long long)fx.r * p.key.row + (long long)fx.h * p.key.head + fo;
+        const unsigned char* fv = p.value.data + (long long)fx.r * p.value.row + (long long)fx.h * p.value.head + fo;
+        const unsigned char* dk = p.dkey.data + (long long)fx.r * p.dkey.row + (long long)fx.h * p.dkey.head + fo;
+        const unsigned char* dv = p.dvalue.data + (long long)fx.r * p.dvalue.row + (long long)fx.h * p.dvalue.head + fo;
+        const uint32_t kpos = (uint32_t)p.key.pos, vpos = (uint32_t)p.value.pos;
+#pragma unroll 4
+        for (int u = 0; u < KB / RPI; ++u) {
+          const uint32_t off = at(u * RPI + fr, fc);
+          const int j = j0 + u * RPI;
+          const bool ok = fcv && j < total && j >= 0;
+          const unsigned char* ka = j < fx.len ? fk + (unsigned long long)(uint32_t)j * kpos : dk + (long long)(j - fx.len) * p.dkey.pos;
+          const unsigned char* va = j < fx.len ? fv + (unsigned long long)(uint32_t)j * vpos : dv + (long long)(j - fx.len) * p.dvalue.pos;
+          cp_async16_fill(kd_ + off, ok ? ka : p.q.data, ok ? 16 : 0);
+          cp_async16_fill(vd_ + off, ok ? va : p.q.data, ok ? 16 : 0);
+        }
       }
       if (fx.b >= 0) fx.b += W;
       if (fx.b < 0 || fx.b >= fx.b_end) {
@@ -229,201 +274,205 @@ __global__ void __launch_bounds__(kMmThreads) attend_mma_kernel(const AttendPara
     cp_async_commit();
     f_slot = f_slot + 1 == NS ? 0 : f_slot + 1;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < NS - 1; ++i) fill();
 
   int slot = 0, seq = 0;
-  int c_len = first < p.items ? __ldg(p.len + item_row<DP, MT>(p, first)) : 0;
-  for (long long it = first; it < p.items; it += stride) {
-    MmaItem x = open_item<DP, MT>(p, it, c_len, wi);
+  uint32_t phases = 0;  // bit i: the parity that slot i's barrier completes next
+  int c_len = first < items ? __ldg(p.len + item_row(p, first)) : 0;
+#pragma unroll 1
+  for (int it = first; it < items; it += stride) {
+    MmaItem x = open_item<KB, NQ>(p, it, c_len, wi);
     if (x.len != c_len && lane == 0) atomicOr(p.status, kDevInternal);
-    if (it + stride < p.items) c_len = __ldg(p.len + item_row<DP, MT>(p, it + stride));
+    if (it + stride < items) c_len = __ldg(p.len + item_row(p, it + stride));
     const uint32_t qs = base + sm.q + seq * sm.q_one;
-    uint32_t qf[S::QREG ? DP / 16 : 1][4];
+    uint32_t qf[S::QREG ? NQ : 1][DP / 16][2];
     bool bad_values = false, dead_any = false;
-    unsigned alive = ~0u;  // bit 2 * mt + half: the query sees something
-    float m_run[MT][2], l_run[MT][2], o[MT][DP / 8][4];
+    unsigned alive = ~0u;  // bit 2 * a + e: query 8 a + 2 t + e sees something
+    float m_run[NQ][2], l_run[NQ][2], o[DP / 16][NQ][4];
 #pragma unroll
-    for (int a = 0; a < MT; ++a) {
+    for (int a = 0; a < NQ; ++a) {
       m_run[a][0] = m_run[a][1] = -INFINITY;
       l_run[a][0] = l_run[a][1] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < DP / 8; ++j) o[a][j][0] = o[a][j][1] = o[a][j][2] = o[a][j][3] = 0.0f;
+      for (int j = 0; j < DP / 16; ++j) o[j][a][0] = o[j][a][1] = o[j][a][2] = o[j][a][3] = 0.0f;
     }
     bool open = true;
+#pragma unroll 1
     do {
       cp_async_wait<NS - 2>();
+      if (x.b >= 0 && x.b * KB + KB <= x.len) {
+        // after a wait that ran out nothing is fetched or waited for any more; the loops just end
+        const bool there = timed_out || mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns);
+        timed_out |= !__all_sync(~0u, there);
+        phases ^= 1u << slot;
+      }
       __syncwarp();  // every lane's copies of this stage are there, and all are done with the last one
       if (open) {
         open = false;
         if constexpr (S::QREG) {
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
+          for (int a = 0; a < NQ; ++a)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = g + (e & 1) * 8, c = 2 * kk + (e >> 1);
-              qf[kk][e] = row < x.nq ? lds32(qs + row * ROW + ((c ^ (row & 7)) << 4) + t * 4) : 0u;
-            }
-          }
+            for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int q = a * 8 + g;
+                qf[a][kk][e] = q < x.nq ? lds32(qs + q * sm.q_row + (2 * kk + e) * 16 + t * 4) : 0u;
+              }
         }
         if (p.nodes) {
-          const int* par = reinterpret_cast<const int*>(mine + sm.par + seq * np);
+          const int* par = reinterpret_cast<const int*>(mine + sm.par + seq * sm.par_one);
           if (tree_seen_from(tree, [&](int i) { return par[i]; }, p.nodes, lane, 32, [] { __syncwarp(); }))
             atomicOr(p.status, kDevInternal);
           alive = 0;
 #pragma unroll
-          for (int a = 0; a < 2 * MT; ++a) {
-            const int row = (a >> 1) * 16 + (a & 1) * 8 + g;
-            if (row < x.nq && tree.mask[(x.i0 + row) / p.group]) alive |= 1u << a;
-            dead_any |= row < x.nq && !((alive >> a) & 1u);
+          for (int a = 0; a < 2 * NQ; ++a) {
+            const int q = (a >> 1) * 8 + 2 * t + (a & 1);
+            if (q < x.nq && tree.mask[p.by_group(x.i0 + q)]) alive |= 1u << a;
+            dead_any |= q < x.nq && !((alive >> a) & 1u);
           }
           dead_any = __any_sync(~0u, dead_any);
         }
-        seq = seq + 1 == NS ? 0 : seq + 1;
+        seq = seq + 1 == sets ? 0 : seq + 1;
       }
       fill();
-      const uint32_t ks = base + slot * S::STAGE, vs = ks + KB * ROW;
-      const bool draft = x.b >= x.nb;
-      const int n0 = x.b < 0 ? 0 : (draft ? x.b - x.nb : x.b) * KB;
-      const int n = x.b < 0 ? 0 : (draft ? p.nodes : x.len) - n0;
+      const uint32_t ks = ring + slot * S::STAGE, vs = ks + S::PANELS * S::PANEL;
+      const int n0 = max(x.b, 0) * KB;
+      const int total = x.b < 0 ? 0 : x.len + p.nodes;
 
-      // S = Q K^T
-      float s[MT][NT][4];
+      // S^T = K Q^T
+      float s[KT][NQ][4];
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+      for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) s[a][j][0] = s[a][j][1] = s[a][j][2] = s[a][j][3] = 0.0f;
-      const int lr = (lane & 7) + ((lane >> 4) << 3), lc = (lane >> 3) & 1;  // K: key within 16, 16-byte half
+        for (int a = 0; a < NQ; ++a) s[k][a][0] = s[k][a][1] = s[k][a][2] = s[k][a][3] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        if (kk < kd) {
-          uint32_t qa[MT][4];
+        if (DP == 64 || kk < kd) {
+          uint32_t qb[NQ][2];
           if constexpr (S::QREG) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qa[0][e] = qf[kk][e];
+            for (int a = 0; a < NQ; ++a) {
+              qb[a][0] = qf[a][kk][0];
+              qb[a][1] = qf[a][kk][1];
+            }
           } else {
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-              const int row = a * 16 + (lane & 15), c = 2 * kk + (lane >> 4);
-              ldsm4(qa[a], qs + row * ROW + ((c ^ (row & 7)) << 4));
+            for (int a = 0; a < NQ; a += 2) {
+              uint32_t f[4];
+              const int q = a * 8 + (lane & 7) + (lane >> 4) * 8, c = 2 * kk + ((lane >> 3) & 1);
+              ldsm4(f, qs + q * sm.q_row + c * 16);
+              qb[a][0] = f[0];
+              qb[a][1] = f[1];
+              qb[a + 1][0] = f[2];
+              qb[a + 1][1] = f[3];
             }
           }
 #pragma unroll
-          for (int j = 0; j < NT; j += 2) {
-            uint32_t b[4];
-            const int row = j * 8 + lr, c = 2 * kk + lc;
-            ldsm4(b, ks + row * ROW + ((c ^ (row & 7)) << 4));
+          for (int k = 0; k < KT; ++k) {
+            uint32_t f[4];
+            const int row = k * 16 + (lane & 15), c = 2 * kk + (lane >> 4);
+            ldsm4(f, ks + at(row, c));
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-              mma16816<BF>(s[a][j], qa[a], b[0], b[1]);
-              mma16816<BF>(s[a][j + 1], qa[a], b[2], b[3]);
-            }
+            for (int a = 0; a < NQ; ++a) mma16816<BF>(s[k][a], f, qb[a][0], qb[a][1]);
           }
         }
       }
 
+      const bool edge = x.b < 0 || n0 + KB > x.len;
       // values that some queries must not meet: infinite and NaN ones of the drafted tokens are
       // taken out and added back at the end to the queries that see them
-      if (draft && p.nodes > 1) {
+      if (edge && p.nodes > 1) {
         bool hit = false;
-        for (int e = lane; e < min(n, KB) * (DP / 8); e += 32) {
-          const uint32_t at = vs + e * 16;
-          uint4 v = lds128(at);
-          bool h = false;
-          v.x = finite2<BF>(v.x, &h);
-          v.y = finite2<BF>(v.y, &h);
-          v.z = finite2<BF>(v.z, &h);
-          v.w = finite2<BF>(v.w, &h);
-          if (h) sts128(at, v);
-          hit |= h;
+        const int from = max(x.len - n0, 0), upto = min(total - n0, KB);
+        for (int e = from * CPR + lane; e < upto * CPR; e += 32) {
+          const uint32_t a = vs + at(e / CPR, e % CPR);
+          uint4 v = lds128(a);
+          bool bad = false;
+          v.x = finite2<BF>(v.x, &bad);
+          v.y = finite2<BF>(v.y, &bad);
+          v.z = finite2<BF>(v.z, &bad);
+          v.w = finite2<BF>(v.w, &bad);
+          if (bad) sts128(a, v);
+          hit |= bad;
         }
         bad_values |= __any_sync(~0u, hit);
         __syncwarp();
       }
 
-      const bool edge = draft || n < KB || dead_any;
+      uint32_t pb[KT][NQ][2];
 #pragma unroll
-      for (int a = 0; a < MT; ++a) {
+      for (int a = 0; a < NQ; ++a) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int k = 0; k < KT; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[a][j][e] *= p.scale_log2;
-        if (edge) {
+          for (int e = 0; e < 4; ++e) s[k][a][e] *= p.scale_log2;
+        if (edge || dead_any) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = a * 16 + half * 8 + g;
-            unsigned see = ((alive >> (2 * a + half)) & 1u) ? ~0u : 0u;
-            if (draft && see && row < x.nq) see = (unsigned)(tree.mask[(x.i0 + row) / p.group] >> n0);
+          for (int e = 0; e < 2; ++e) {
+            const bool live = (alive >> (2 * a + e)) & 1u;
+            const int q = a * 8 + 2 * t + e;
+            const unsigned long long see = edge && p.nodes && live && q < x.nq ? tree.mask[p.by_group(x.i0 + q)] : 0ull;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int k = 0; k < KT; ++k)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = j * 8 + 2 * t + e;
-                if (key >= n || !((see >> key) & 1u)) s[a][j][2 * half + e] = -INFINITY;
+              for (int hf = 0; hf < 2; ++hf) {
+                const int j = n0 + k * 16 + hf * 8 + g;
+                const bool ok = live && j < total && (j < x.len || ((see >> (j - x.len)) & 1ull));
+                if (!ok) s[k][a][2 * hf + e] = -INFINITY;
               }
           }
         }
-        float bm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          bm[0] = fmaxf(bm[0], fmaxf(s[a][j][0], s[a][j][1]));
-          bm[1] = fmaxf(bm[1], fmaxf(s[a][j][2], s[a][j][3]));
-        }
+        float sub[2], fct[2];
         bool moved = false;
-        float fct[2], sub[2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          bm[half] = fmaxf(bm[half], __shfl_xor_sync(~0u, bm[half], 1));
-          bm[half] = fmaxf(bm[half], __shfl_xor_sync(~0u, bm[half], 2));
-          const float mn = fmaxf(m_run[a][half], bm[half]);
-          moved |= mn > m_run[a][half];
-          sub[half] = mn == -INFINITY ? 0.0f : mn;
-          fct[half] = fast_exp2(m_run[a][half] - sub[half]);
-          m_run[a][half] = mn;
+        for (int e = 0; e < 2; ++e) {
+          float bm = fmaxf(s[0][a][e], s[0][a][2 + e]);
+#pragma unroll
+          for (int k = 1; k < KT; ++k) bm = fmaxf(bm, fmaxf(s[k][a][e], s[k][a][2 + e]));
+          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 4));
+          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 8));
+          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 16));
+          const float mn = fmaxf(m_run[a][e], bm);
+          moved |= mn > m_run[a][e];
+          sub[e] = mn == -INFINITY ? 0.0f : mn;
+          fct[e] = fast_exp2(m_run[a][e] - sub[e]);
+          m_run[a][e] = mn;
         }
         if (__any_sync(~0u, moved)) {
+          l_run[a][0] *= fct[0];
+          l_run[a][1] *= fct[1];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) l_run[a][half] *= fct[half];
-#pragma unroll
-          for (int j = 0; j < DP / 8; ++j) {
-            o[a][j][0] *= fct[0];
-            o[a][j][1] *= fct[0];
-            o[a][j][2] *= fct[1];
-            o[a][j][3] *= fct[1];
+          for (int j = 0; j < DP / 16; ++j) {
+            o[j][a][0] *= fct[0];
+            o[j][a][1] *= fct[1];
+            o[j][a][2] *= fct[0];
+            o[j][a][3] *= fct[1];
           }
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int k = 0; k < KT; ++k) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[a][j][e] = fast_exp2(s[a][j][e] - sub[e >> 1]);
-          l_run[a][0] += s[a][j][0] + s[a][j][1];
-          l_run[a][1] += s[a][j][2] + s[a][j][3];
+          for (int e = 0; e < 4; ++e) s[k][a][e] = fast_exp2(s[k][a][e] - sub[e & 1]);
+          l_run[a][0] += s[k][a][0] + s[k][a][2];
+          l_run[a][1] += s[k][a][1] + s[k][a][3];
+          pb[k][a][0] = transpose8(pack2<BF>(s[k][a][0], s[k][a][1]));
+          pb[k][a][1] = transpose8(pack2<BF>(s[k][a][2], s[k][a][3]));
         }
       }
 
-      // O += P V
+      // O^T += V^T P^T
 #pragma unroll
-      for (int k2 = 0; k2 < KB / 16; ++k2) {
-        uint32_t pa[MT][4];
+      for (int j = 0; j < DP / 16; ++j) {
+        if (DP == 64 || j < kd) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          pa[a][0] = pack2<BF>(s[a][2 * k2][0], s[a][2 * k2][1]);
-          pa[a][1] = pack2<BF>(s[a][2 * k2][2], s[a][2 * k2][3]);
-          pa[a][2] = pack2<BF>(s[a][2 * k2 + 1][0], s[a][2 * k2 + 1][1]);
-          pa[a][3] = pack2<BF>(s[a][2 * k2 + 1][2], s[a][2 * k2 + 1][3]);
-        }
-        const int row = k2 * 16 + (lane & 15);
+          for (int k = 0; k < KT; ++k) {
+            uint32_t f[4];
+            const int row = k * 16 + (lane & 7) + (lane >> 4) * 8, c = 2 * j + ((lane >> 3) & 1);
+            ldsm4_trans(f, vs + at(row, c));
 #pragma unroll
-        for (int j = 0; j < DP / 8; j += 2) {
-          if (j < 2 * kd) {
-            uint32_t b[4];
-            const int c = j + (lane >> 4);
-            ldsm4_trans(b, vs + row * ROW + ((c ^ (row & 7)) << 4));
-#pragma unroll
-            for (int a = 0; a < MT; ++a) {
-              mma16816<BF>(o[a][j], pa[a], b[0], b[1]);
-              mma16816<BF>(o[a][j + 1], pa[a], b[2], b[3]);
-            }
+            for (int a = 0; a < NQ; ++a) mma16816<BF>(o[j][a], f, pb[k][a][0], pb[k][a][1]);
           }
         }
       }
@@ -432,110 +481,122 @@ __global__ void __launch_bounds__(kMmThreads) attend_mma_kernel(const AttendPara
     } while (x.b >= 0 && x.b < x.b_end);
 
     if (bad_values) {  // rare: the infinite and NaN values of the drafted tokens
-      const AtView& vv = p.dvalue;
-      const unsigned char* dv = vv.data + (long long)x.r * vv.row + (long long)x.h * vv.head;
+      const unsigned char* dv = p.dvalue.data + (long long)x.r * p.dvalue.row + (long long)x.h * p.dvalue.head;
+      for (int nd = 0; nd < p.nodes; ++nd)
 #pragma unroll
-      for (int a = 0; a < 2 * MT; ++a) {
-        const int row = (a >> 1) * 16 + (a & 1) * 8 + g;
-        const unsigned long long see = row < x.nq ? tree.mask[(x.i0 + row) / p.group] : 0ull;
-        for (int nd = 0; nd < p.nodes; ++nd) {
-          if (!((see >> nd) & 1ull)) continue;
+        for (int a = 0; a < 2 * NQ; ++a) {
+          const int q = (a >> 1) * 8 + 2 * t + (a & 1);
+          if (q >= x.nq || !((tree.mask[p.by_group(x.i0 + q)] >> nd) & 1ull)) continue;
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
+          for (int j = 0; j < DP / 16; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d = j * 8 + 2 * t + e;
-              const float v = d < p.dim ? load_elem<DT>(dv + nd * vv.pos + d * 2) : 0.0f;
-              if (!isfinite(v)) o[a >> 1][j][2 * (a & 1) + e] += v;
+            for (int hf = 0; hf < 2; ++hf) {
+              const int d = j * 16 + hf * 8 + g;
+              const float v = d < p.dim ? load_elem<DT>(dv + nd * p.dvalue.pos + d * 2) : 0.0f;
+              if (!isfinite(v)) o[j][a >> 1][2 * hf + (a & 1)] += v;
             }
         }
-      }
+      __syncwarp();
     }
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int a = 0; a < NQ; ++a)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        l_run[a][half] += __shfl_xor_sync(~0u, l_run[a][half], 1);
-        l_run[a][half] += __shfl_xor_sync(~0u, l_run[a][half], 2);
+      for (int e = 0; e < 2; ++e) {
+        l_run[a][e] += __shfl_xor_sync(~0u, l_run[a][e], 4);
+        l_run[a][e] += __shfl_xor_sync(~0u, l_run[a][e], 8);
+        l_run[a][e] += __shfl_xor_sync(~0u, l_run[a][e], 16);
       }
-    const long long prow = (((long long)x.r * p.kv_heads + x.h) * p.m + x.i0) * p.splits + x.split;
     if (W == 1) {  // never split
 #pragma unroll
-      for (int a = 0; a < 2 * MT; ++a) {
-        const int row = (a >> 1) * 16 + (a & 1) * 8 + g;
-        if (row < x.nq) {
-          const float l = l_run[a >> 1][a & 1];
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          unsigned char* out = p.out.data + query_offset(p, p.out, x.r, x.h, x.i0 + row) + t * 4;
+      for (int a = 0; a < NQ; ++a) {
+        if (a * 8 >= x.nq) break;
+        const int q = a * 8 + g;  // the query whose elements this lane stores after the transpose
+        unsigned char* out = p.out.data + query_offset(p, p.out, x.r, x.h, x.i0 + min(q, x.nq - 1)) + t * 4;
+        const bool z0 = l_run[a][0] == 0.0f, z1 = l_run[a][1] == 0.0f;
+        const float i0 = z0 ? 0.0f : 1.0f / l_run[a][0], i1 = z1 ? 0.0f : 1.0f / l_run[a][1];
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
-            if (j < chunks) {
-              const float o0 = l == 0.0f ? 0.0f : o[a >> 1][j][2 * (a & 1)] * inv;
-              const float o1 = l == 0.0f ? 0.0f : o[a >> 1][j][2 * (a & 1) + 1] * inv;
-              *reinterpret_cast<uint32_t*>(out + j * 16) = pack2<BF>(o0, o1);
-            }
+        for (int j = 0; j < DP / 16; ++j) {
+          if (j >= kd) break;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float y0 = z0 ? 0.0f : o[j][a][2 * hf] * i0, y1 = z1 ? 0.0f : o[j][a][2 * hf + 1] * i1;
+            const uint32_t y = transpose8(pack2<BF>(y0, y1));
+            if (q < x.nq && 2 * j + hf < chunks) *reinterpret_cast<uint32_t*>(out + j * 32 + hf * 16) = y;
+          }
         }
       }
     } else {
       // the four warps' results, added in their order
-      constexpr int PITCH = DP + 8;
+      constexpr int PITCH = DP + 4;
       cp_async_wait<0>();
       __syncthreads();
-      float* acc = reinterpret_cast<float*>(mm_raw);
+      float* acc = reinterpret_cast<float*>(mm_raw + (rings - raw));
 #pragma unroll
-      for (int a = 0; a < 2 * MT; ++a) {
-        const int row = (a >> 1) * 16 + (a & 1) * 8 + g;
-        if (t == 0) {
-          wm[warp][row] = m_run[a >> 1][a & 1];
-          wl[warp][row] = l_run[a >> 1][a & 1];
-        }
-        if (row < x.nq) {
+      for (int a = 0; a < NQ; ++a)
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j)
-            *reinterpret_cast<float2*>(acc + (warp * 16 * MT + row) * PITCH + j * 8 + 2 * t) =
-                make_float2(o[a >> 1][j][2 * (a & 1)], o[a >> 1][j][2 * (a & 1) + 1]);
+        for (int e = 0; e < 2; ++e) {
+          const int q = a * 8 + 2 * t + e;
+          if (g == 0) {
+            wm[warp][q] = m_run[a][e];
+            wl[warp][q] = l_run[a][e];
+          }
+          if (q < x.nq) {
+#pragma unroll
+            for (int j = 0; j < DP / 16; ++j) {
+              acc[(warp * 8 * NQ + q) * PITCH + j * 16 + g] = o[j][a][e];
+              acc[(warp * 8 * NQ + q) * PITCH + j * 16 + 8 + g] = o[j][a][2 + e];
+            }
+          }
         }
-      }
       __syncthreads();
       const int half_dim = p.dim / 2;
+      const long long prow = (((long long)x.r * p.kv_heads + x.h) * p.m + x.i0) * p.splits + x.split;
       for (int e = threadIdx.x; e < x.nq * half_dim; e += kMmThreads) {
-        const int row = e / half_dim, d = (e - row * half_dim) * 2;
-        float M = wm[0][row];
+        const int q = e / half_dim, d = (e - q * half_dim) * 2;
+        float M = wm[0][q];
 #pragma unroll
-        for (int w = 1; w < kMmWarps; ++w) M = fmaxf(M, wm[w][row]);
+        for (int w = 1; w < kMmWarps; ++w) M = fmaxf(M, wm[w][q]);
         const float sub = M == -INFINITY ? 0.0f : M;
         float L = 0.0f, o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
         for (int w = 0; w < kMmWarps; ++w) {
-          const float l = wl[w][row], f = fast_exp2(wm[w][row] - sub);
+          const float l = wl[w][q], f = fast_exp2(wm[w][q] - sub);
           L = fmaf(f, l, L);
-          const float2 v = *reinterpret_cast<const float2*>(acc + (w * 16 * MT + row) * PITCH + d);
+          const float2 v = *reinterpret_cast<const float2*>(acc + (w * 8 * NQ + q) * PITCH + d);
           o0 = add_part(o0, f, v.x, l);
           o1 = add_part(o1, f, v.y, l);
         }
         if (p.splits == 1) {
           const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          *reinterpret_cast<uint32_t*>(p.out.data + query_offset(p, p.out, x.r, x.h, x.i0 + row) + d * 2) =
+          *reinterpret_cast<uint32_t*>(p.out.data + query_offset(p, p.out, x.r, x.h, x.i0 + q) + d * 2) =
               pack2<BF>(L == 0.0f ? 0.0f : o0 * inv, L == 0.0f ? 0.0f : o1 * inv);
         } else {
-          const long long pr = prow + (long long)row * p.splits;
+          const long long pr = prow + (long long)q * p.splits;
           *reinterpret_cast<float2*>(p.part_o + pr * p.dim + d) = make_float2(o0, o1);
           if (d == 0) p.part_ml[pr] = make_float2(M, L);
         }
       }
     }
   }
+  if (timed_out && lane == 0) atomicOr(p.status, kDevTimeout);
+  if (timed_out) {  // every copy lands before the CTA may exit
+    for (int i = 0; i < NS; ++i) mbar_wait_bounded(base + sm.bars + 8 * i, ((phases >> i) & 1u) ^ 1u, kMmDrainNs);
+  }
   cp_async_wait<0>();
 }
 
-template <bool BF, int DP, int MT>
-cudaError_t run_mma(const AttendParams& p, cudaStream_t stream) {
+template <bool BF, int DP, int NQ>
+cudaError_t run_mma(const AttendParams& p, int dtype, cudaStream_t stream) {
+  using S = MmaShape<DP, NQ>;
   static std::atomic<uint64_t> allowed{0};
-  const int most = kMmWarps * mma_smem<DP, MT>(16 * MT, kAtMaxNodes).total;
-  const int bytes = kMmWarps * mma_smem<DP, MT>(p.m, p.nodes).total;
-  auto kernel = attend_mma_kernel<BF, DP, MT>;
+  const int most = mma_smem_bytes<DP, NQ>(8 * NQ, kAtMaxNodes, 1);
+  const int bytes = mma_smem_bytes<DP, NQ>(p.m, p.nodes, p.warps);
+  auto kernel = attend_mma_kernel<BF, DP, NQ>;
   cudaError_t e = allow_shared(kernel, most, allowed);
   if (e != cudaSuccess) return e;
+  // without a row of a whole block there is nothing for TMA to read
+  CUtensorMap maps[2] = {};
+  if (p.max_len >= S::KB && !encode_keys(maps, p, dtype, S::KB)) return cudaErrorInvalidValue;
   long long grid = p.items;
   if (p.warps == 1) {
     int occ = 1;
@@ -544,24 +605,33 @@ cudaError_t run_mma(const AttendParams& p, cudaStream_t stream) {
     const long long need = (p.items + kMmWarps - 1) / kMmWarps, fit = (long long)kAtSms * (occ > 0 ? occ : 1);
     grid = need < fit ? need : fit;
   }
-  kernel<<<(unsigned)grid, kMmThreads, bytes, stream>>>(p);
+  kernel<<<(unsigned)grid, kMmThreads, bytes, stream>>>(maps[0], maps[1], p);
   return cudaGetLastError();
 }
 
+template <bool BF, int DP>
+cudaError_t run_mma_queries(const AttendParams& p, int dtype, cudaStream_t stream) {
+  const int q = attend_mma_queries(p.dim, p.m);
+  if (q == 8) return run_mma<BF, DP, 1>(p, dtype, stream);
+  if constexpr (DP <= 128) {
+    if (q == 32) return run_mma<BF, DP, 4>(p, dtype, stream);
+  }
+  return run_mma<BF, DP, 2>(p, dtype, stream);
+}
+
 template <bool BF>
-cudaError_t run_mma_dim(const AttendParams& p, cudaStream_t stream) {
-  const bool two = attend_mma_queries(p.dim, p.m) == 32;
-  if (p.dim <= 64) return two ? run_mma<BF, 64, 2>(p, stream) : run_mma<BF, 64, 1>(p, stream);
-  if (p.dim <= 128) return two ? run_mma<BF, 128, 2>(p, stream) : run_mma<BF, 128, 1>(p, stream);
-  return run_mma<BF, 256, 1>(p, stream);
+cudaError_t run_mma_dim(const AttendParams& p, int dtype, cudaStream_t stream) {
+  if (p.dim <= 64) return run_mma_queries<BF, 64>(p, dtype, stream);
+  if (p.dim <= 128) return run_mma_queries<BF, 128>(p, dtype, stream);
+  return run_mma_queries<BF, 256>(p, dtype, stream);
 }
 
 }  // namespace
 
-int attend_mma_queries(int dim, int m) { return m > 16 && dim <= 128 ? 32 : 16; }
+int attend_mma_queries(int dim, int m) { return m <= 8 ? 8 : m <= 16 || dim > 128 ? 16 : 32; }
 
 cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t stream) {
-  return dtype == DT_BF16 ? run_mma_dim<true>(p, stream) : run_mma_dim<false>(p, stream);
+  return dtype == DT_BF16 ? run_mma_dim<true>(p, dtype, stream) : run_mma_dim<false>(p, dtype, stream);
 }
 
 }  // namespace lsb

@@ -68,19 +68,16 @@ template <int DT, int MQ, int ND>
 __global__ void __launch_bounds__(kSiThreads) attend_simt_kernel(const AttendParams p) {
   constexpr int B = Traits<DT>::kBytes;
   extern __shared__ float4 si_smem[];
-  __shared__ TreeSeen tree;
+  __shared__ unsigned long long tree_raw[kAtMaxNodes * 12 / 8];
+  const TreeSeen tree = tree_at(tree_raw, kAtMaxNodes);
   __shared__ float wm[kSiWarps][MQ], wl[kSiWarps][MQ];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pitch = simt_pitch(p.dim);
   float* qs = reinterpret_cast<float*>(si_smem);
   float* ks = qs + MQ * pitch + warp * 32 * pitch;
 
-  long long it = blockIdx.x;
-  const int split = (int)(it % p.splits);
-  it /= p.splits;
-  const int i0 = (int)(it % p.m_tiles) * MQ;
-  it /= p.m_tiles;
-  const int h = (int)(it % p.kv_heads), r = (int)(it / p.kv_heads);
+  const int it = (int)blockIdx.x, ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
+  const int i0 = (ia - ib * p.m_tiles) * MQ, r = p.by_head(ib), h = ib - r * p.kv_heads;
   const int nq = min(MQ, p.m - i0);
   const int len = row_keys(p, r, tid == 0);
 
@@ -100,7 +97,7 @@ __global__ void __launch_bounds__(kSiThreads) attend_simt_kernel(const AttendPar
   const int b_lo = min(split * per, nbt), b_hi = min(b_lo + per, nbt);
   bool alive[MQ];
 #pragma unroll
-  for (int j = 0; j < MQ; ++j) alive[j] = j < nq && (!p.nodes || tree.mask[(i0 + j) / p.group] != 0);
+  for (int j = 0; j < MQ; ++j) alive[j] = j < nq && (!p.nodes || tree.mask[p.by_group(i0 + j)] != 0);
 
   float mx[MQ], sum[MQ], o[MQ][ND];
 #pragma unroll
@@ -146,7 +143,7 @@ __global__ void __launch_bounds__(kSiThreads) attend_simt_kernel(const AttendPar
     float pr[MQ];
 #pragma unroll
     for (int j = 0; j < MQ; ++j) {
-      seen[j] = draft && alive[j] ? (unsigned)(tree.mask[(i0 + j) / p.group] >> n0) : (alive[j] ? ~0u : 0u);
+      seen[j] = draft && alive[j] ? (unsigned)(tree.mask[p.by_group(i0 + j)] >> n0) : (alive[j] ? ~0u : 0u);
       const bool ok = lane < n && ((seen[j] >> lane) & 1u);
       const float t = ok ? s[j] * p.scale_log2 : -INFINITY;
       float bm = t;
@@ -230,8 +227,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
   const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const long long problems = (long long)p.rows * p.kv_heads;
   if (w >= problems * p.m) return;
-  const long long pb = w / p.m;
-  const int i = (int)(w - pb * p.m), h = (int)(pb % p.kv_heads), r = (int)(pb / p.kv_heads);
+  const int pb = (int)(w / p.m), i = (int)(w - (long long)pb * p.m), r = p.by_head(pb), h = pb - r * p.kv_heads;
   const float2* ml = p.part_ml + w * p.splits;
   const float* po = p.part_o + w * p.splits * p.dim;
   float M = -INFINITY;

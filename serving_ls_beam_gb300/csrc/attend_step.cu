@@ -87,28 +87,24 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
 template <int DT, int LPK, int MQ>
 __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendParams p) {
   constexpr int E = Traits<DT>::kVec, ES = Traits<DT>::kBytes, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
-  __shared__ TreeSeen trees[kAsWarps];
+  __shared__ unsigned long long trees[kAsWarps][kAtMaxNodes * 12 / 8];
   __shared__ float wm[kAsWarps][MQ], wl[kAsWarps][MQ];
   __shared__ float acc[kAsWarps][MQ][LPK * E + 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPK, gk = lane / LPK;
   const int W = p.warps, wi = W == 1 ? 0 : warp;
   const bool cv = c < p.dim / E;  // this lane holds a part of the vectors
   const int my_u = (lane & 1) << 2 | (lane & 2) | (lane >> 2 & 1);
-  TreeSeen& tree = trees[warp];
-  const long long stride = W == 1 ? (long long)gridDim.x * kAsWarps : gridDim.x;
-  long long it = W == 1 ? (long long)blockIdx.x * kAsWarps + warp : blockIdx.x;
-  const long long per_row = (long long)p.splits * p.m_tiles * p.kv_heads;
-  int next_len = it < p.items ? __ldg(p.len + it / per_row) : 0;
-  for (; it < p.items; it += stride) {
-    const int r = (int)(it / per_row);
-    int e = (int)(it - r * per_row);
-    const int split = e % p.splits;
-    e /= p.splits;
-    const int i0 = (e % p.m_tiles) * MQ, h = e / p.m_tiles;
+  const TreeSeen tree = tree_at(trees[warp], kAtMaxNodes);
+  const int items = (int)p.items, stride = W == 1 ? (int)gridDim.x * kAsWarps : (int)gridDim.x;
+  int it = W == 1 ? (int)blockIdx.x * kAsWarps + warp : (int)blockIdx.x;
+  int next_len = it < items ? __ldg(p.len + p.by_head(p.by_tile(p.by_split(it)))) : 0;
+  for (; it < items; it += stride) {
+    const int ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
+    const int i0 = (ia - ib * p.m_tiles) * MQ, r = p.by_head(ib), h = ib - r * p.kv_heads;
     const int nq = min(MQ, p.m - i0);
     const int len = min(max(next_len, 0), p.max_len);
     if (len != next_len && lane == 0) atomicOr(p.status, kDevInternal);
-    if (it + stride < p.items) next_len = __ldg(p.len + (it + stride) / per_row);
+    if (it + stride < items) next_len = __ldg(p.len + p.by_head(p.by_tile(p.by_split(it + stride))));
     const int total = len + p.nodes, nbt = (total + KB - 1) / KB, per = (nbt + p.splits - 1) / p.splits;
     const int lo = min(split * per, nbt), hi = min(lo + per, nbt);
     int b = lo + wi;
@@ -117,26 +113,26 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
     const unsigned char* vb = p.value.data + (long long)r * p.value.row + (long long)h * p.value.head + c * 16;
     const unsigned char* dkb = p.dkey.data + (long long)r * p.dkey.row + (long long)h * p.dkey.head + c * 16;
     const unsigned char* dvb = p.dvalue.data + (long long)r * p.dvalue.row + (long long)h * p.dvalue.head + c * 16;
-    auto fetch = [&](uint4(&d)[U], int blk, const unsigned char* cache, long long pos, const unsigned char* draft,
+    auto fetch = [&](uint4(&d)[U], int blk, const unsigned char* cache, uint32_t pos, const unsigned char* draft,
                      long long dpos) {
       const int j0 = blk * KB + gk;
       if (blk * KB + KB <= len) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          d[u] = cv ? load_stream(cache + (long long)(j0 + u * KPL) * pos) : make_uint4(0u, 0u, 0u, 0u);
+          d[u] = cv ? load_stream(cache + (unsigned long long)(uint32_t)(j0 + u * KPL) * pos) : make_uint4(0u, 0u, 0u, 0u);
       } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int j = j0 + u * KPL;
-          const unsigned char* at = j < len ? cache + (long long)j * pos : draft + (long long)(j - len) * dpos;
+          const unsigned char* at = j < len ? cache + (unsigned long long)(uint32_t)j * pos : draft + (long long)(j - len) * dpos;
           d[u] = cv && j < total && blk < hi ? load_stream(at) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
     };
     uint4 kr[U], vr[U];
     if (b < hi) {
-      fetch(kr, b, kb, p.key.pos, dkb, p.dkey.pos);
-      fetch(vr, b, vb, p.value.pos, dvb, p.dvalue.pos);
+      fetch(kr, b, kb, (uint32_t)p.key.pos, dkb, p.dkey.pos);
+      fetch(vr, b, vb, (uint32_t)p.value.pos, dvb, p.dvalue.pos);
     }
     float q[MQ][E];
 #pragma unroll
@@ -155,7 +151,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
       alive = 0;
 #pragma unroll
       for (int j = 0; j < MQ; ++j)
-        if (j < nq && tree.mask[(i0 + j) / p.group]) alive |= 1u << j;
+        if (j < nq && tree.mask[p.by_group(i0 + j)]) alive |= 1u << j;
     }
     float m[MQ], l[MQ], o[MQ][E];
 #pragma unroll
@@ -179,7 +175,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
           part[j][u] = a.x + a.y;
         }
       }
-      if (b + W < hi) fetch(kr, b + W, kb, p.key.pos, dkb, p.dkey.pos);
+      if (b + W < hi) fetch(kr, b + W, kb, (uint32_t)p.key.pos, dkb, p.dkey.pos);
       const int key = b * KB + my_u * KPL + gk;  // this lane's key
       const bool edge = b * KB + KB > len;
       float w[MQ];
@@ -188,7 +184,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
         float s = reduce8<LPK>(part[j], lane);
         bool sees = (alive >> j) & 1u;
         if (edge) {
-          if (key >= len) sees = sees && key < total && (tree.mask[(i0 + min(j, nq - 1)) / p.group] >> (key - len) & 1ull);
+          if (key >= len) sees = sees && key < total && (tree.mask[p.by_group(i0 + min(j, nq - 1))] >> (key - len) & 1ull);
         }
         s = sees ? s : -INFINITY;
         float bm = s;
@@ -226,7 +222,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
           }
         }
       }
-      if (b + W < hi) fetch(vr, b + W, vb, p.value.pos, dvb, p.dvalue.pos);
+      if (b + W < hi) fetch(vr, b + W, vb, (uint32_t)p.value.pos, dvb, p.dvalue.pos);
     }
     // over the lane groups
 #pragma unroll

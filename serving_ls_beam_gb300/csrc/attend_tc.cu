@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   using S = TcShape<DP>;
   constexpr int NST = S::NST, DT = BF ? DT_BF16 : DT_F16;
   extern __shared__ unsigned char ta_raw[];
-  __shared__ TreeSeen tree;
+  __shared__ unsigned long long tree_raw[kAtMaxNodes * 12 / 8];
+  const TreeSeen tree = tree_at(tree_raw, kAtMaxNodes);
   __shared__ float2 join_ml[kTaM];
   const uint32_t raw = smem_addr(ta_raw), base = (raw + 1023u) & ~1023u;
   unsigned char* gbase = ta_raw + (base - raw);
@@ -128,12 +129,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   volatile int* bad_values = reinterpret_cast<volatile int*>(gbase + S::WORDS + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long it = blockIdx.x;
-  const int split = (int)(it % p.splits);
-  it /= p.splits;
-  const int i0 = (int)(it % p.m_tiles) * (2 * kTaM);
-  it /= p.m_tiles;
-  const int h = (int)(it % p.kv_heads), r = (int)(it / p.kv_heads);
+  const int it = (int)blockIdx.x, ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
+  const int i0 = (ia - ib * p.m_tiles) * (2 * kTaM), r = p.by_head(ib), h = ib - r * p.kv_heads;
   const int nq = min(2 * kTaM, p.m - i0);
   const bool wide = nq > kTaM;  // two tiles of queries; otherwise the slots share one
   const int len = row_keys(p, r, tid == 0);
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int qi = i0 + (wide ? slot * kTaM : 0) + row;
     const bool mine = row < qn;
     const bool warp_live = quarter * 32 < qn;
-    const unsigned long long sees = mine && p.nodes ? tree.mask[qi / p.group] : 0ull;
+    const unsigned long long sees = mine && p.nodes ? tree.mask[p.by_group(qi)] : 0ull;
     const bool alive = mine && (!p.nodes || sees != 0);
     const bool dead_any = __any_sync(~0u, !alive);
     const int njobs = slot ? jobs1 : jobs0;

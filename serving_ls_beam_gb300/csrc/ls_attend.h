@@ -10,12 +10,23 @@
 #include <atomic>
 
 #include "ls_beam.h"
+#include "ls_internal.h"
 
 namespace lsb {
 
 constexpr int kAtMaxDim = 256;   // largest head size
 constexpr int kAtMaxNodes = LS_MAX_NODES;
 constexpr int kAtSms = 152;
+
+// Division of 0 <= n < 2^31 by a number known on the host (Granlund and Montgomery, 1994).
+struct AtDivisor {
+  uint32_t magic;
+  int shift;
+  void set(int d) { make_divisor((uint32_t)d, &magic, &shift); }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, magic) + (uint32_t)n) >> shift); }
+#endif
+};
 
 // A tensor [row, pos, head, head_dim] by its byte strides (head_dim contiguous).
 struct AtView {
@@ -43,10 +54,12 @@ struct AttendParams {
   float* part_o;          // [problem, m, split, dim] f32
   float2* part_ml;        // [problem, m, split]: maximum (log2 units) and sum
   long long items;        // rows * kv_heads * m_tiles * splits
+  // item = ((row * kv_heads + head) * m_tiles + tile) * splits + split; query = token * group + head
+  AtDivisor by_split, by_tile, by_head, by_group, by_q_len;
   long long spin_limit_ns;
-  // attend_tc.cu: scale_log2 is its absolute value and the sign goes into the queries; a key
-  // tensor shared by all rows or heads (stride 0) has one row or head in its tensor map
-  int negate, kv_row_one, kv_head_one;
+  int negate;             // attend_tc.cu: scale_log2 is its absolute value, the sign goes into the queries
+  // keys shared by all rows or heads (stride 0): their tensor maps have one row or head
+  int kv_row_one, kv_head_one;
 };
 
 // Partial results may take this many (query, split) rows of dim + 2 floats: the plan keeps
@@ -111,8 +124,12 @@ struct AttendDebug {
   int kernel, warps, splits;
 };
 AttendDebug attend_debug();
+bool maps_describe(const AttendParams& p);  // encode_keys can succeed
 // Tensor map of a 16-bit tensor [row, head, pos, dim] by byte strides, in boxes of 64 elements by
 // `box` positions (one swizzle row of 128 bytes each); reads past an extent return zeros.
+// The tensor maps of the keys and the values in boxes of `box` keys; false where a map cannot
+// describe them.
+bool encode_keys(CUtensorMap* maps, const AttendParams& p, int dtype, int box);
 bool encode_attend(CUtensorMap* map, const AtView& v, int dtype, int dim, int pos, int heads, int rows, int box);
 ls_status report_cuda(cudaError_t e);
 

@@ -8,11 +8,18 @@
 
 namespace lsb {
 
-// What the nodes of one row's tree see, in shared memory.
+// What the nodes of one row's tree see, in shared memory (tree_bytes of it, 8-byte aligned).
 struct TreeSeen {
-  unsigned long long mask[kAtMaxNodes];  // bit j: the node sees node j (0: an empty place)
-  int up[kAtMaxNodes];
+  unsigned long long* mask;  // bit j: the node sees node j (0: an empty place)
+  int* up;
 };
+__host__ __device__ inline int tree_bytes(int nodes) { return nodes * 12; }
+__device__ __forceinline__ TreeSeen tree_at(void* shared, int nodes) {
+  TreeSeen t;
+  t.mask = static_cast<unsigned long long*>(shared);
+  t.up = reinterpret_cast<int*>(t.mask + nodes);
+  return t;
+}
 
 // Fills t for a tree of `nodes` nodes with `n` threads (thread `tid`); `sync` orders those
 // threads' shared memory.  Pointer doubling: after round r a node's mask holds its 2^r nearest
@@ -20,7 +27,7 @@ struct TreeSeen {
 // place, one whose parent is not before it is invalid (returned true) and treated the same,
 // and so are the nodes under either.
 template <class Parent, class Sync>
-__device__ __forceinline__ bool tree_seen_from(TreeSeen& t, Parent parent, int nodes, int tid, int n, Sync sync) {
+__device__ __forceinline__ bool tree_seen_from(const TreeSeen& t, Parent parent, int nodes, int tid, int n, Sync sync) {
   bool bad = false;
   for (int i = tid; i < nodes; i += n) {
     const int p = parent(i);
@@ -59,7 +66,7 @@ __device__ __forceinline__ bool tree_seen_from(TreeSeen& t, Parent parent, int n
 }
 
 template <class Sync>
-__device__ __forceinline__ bool tree_seen(TreeSeen& t, const int32_t* parent, int nodes, int tid, int n, Sync sync) {
+__device__ __forceinline__ bool tree_seen(const TreeSeen& t, const int32_t* parent, int nodes, int tid, int n, Sync sync) {
   return tree_seen_from(t, [&](int i) { return __ldg(parent + i); }, nodes, tid, n, sync);
 }
 
@@ -80,8 +87,8 @@ __device__ __forceinline__ int row_keys(const AttendParams& p, int r, bool repor
 
 // Query i of problem (r, h).
 __device__ __forceinline__ long long query_offset(const AttendParams& p, const AtView& v, int r, int h, int i) {
-  const int t = i / p.group, g = i - t * p.group;
-  const int b = t / p.q_len, pos = t - b * p.q_len;
+  const int t = p.by_group(i), g = i - t * p.group;
+  const int b = p.by_q_len(t), pos = t - b * p.q_len;
   return ((long long)r * p.beams + b) * v.row + (long long)pos * v.pos + (long long)(h * p.group + g) * v.head;
 }
 
