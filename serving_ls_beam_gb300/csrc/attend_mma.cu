@@ -36,10 +36,6 @@ constexpr int kMmWarps = 4;
 constexpr int kMmThreads = kMmWarps * 32;
 constexpr long long kMmDrainNs = 2000000000LL;
 
-// 16 bytes to shared memory, n of them read (16 or 0) and the rest zeros
-__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }

@@ -49,7 +49,7 @@ struct TcShape {
   static constexpr int NST = DP == 64 ? 4 : 2;                 // stages of either ring
   static constexpr uint32_t TILE = PANELS * kTaPanel;          // 128 vectors of DP elements
   static constexpr uint32_t Q = 0, K = 2 * TILE, V = K + NST * TILE, BAR = V + NST * TILE;
-  static constexpr int NBAR = 4 * NST + 1 + 2 + 2 + 2 + 1;     // full / empty x K / V, q, s, p, o, done
+  static constexpr int NBAR = 4 * NST + 1 + 2 + 4 + 2 + 1;     // full / empty x K / V, q, s, p x halves, o, done
   static constexpr uint32_t WORDS = BAR + 8 * NBAR;            // tensor-memory address, abort flag, value flag
   static constexpr uint32_t BYTES = WORDS + 16 + 1024;         // + alignment of the tiles
 };
@@ -78,6 +78,11 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void softmax_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -88,16 +93,22 @@ struct Waits {
   long long limit;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (mbar_test_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-      if (mbar_try_wait(bar, parity, 20000u)) return true;
-      if (*abort) return false;
-      if ((long long)(global_timer_ns() - t0) >= limit) {
-        *abort = 1;
-        atomicOr(status, kDevTimeout);
-        return false;
+    if (limit <= 0) return give_up();
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+      if (mbar_test_wait(bar, parity)) return true;
+      if ((n & 255u) == 0) {  // the timer and the flag are slow to read
+        if (*abort) return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if ((long long)(now - t0) >= limit) return give_up();
       }
     }
+  }
+  __device__ __forceinline__ bool give_up() const {
+    *abort = 1;
+    atomicOr(status, kDevTimeout);
+    return false;
   }
 };
 
@@ -121,19 +132,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   auto vempty = [&](int s) { return bars + 8u * (3 * NST + s); };
   const uint32_t qfull = bars + 8u * (4 * NST);
   auto sfull = [&](int s) { return bars + 8u * (4 * NST + 1 + s); };
-  auto pfull = [&](int s) { return bars + 8u * (4 * NST + 3 + s); };
-  auto ofull = [&](int s) { return bars + 8u * (4 * NST + 5 + s); };
-  const uint32_t done = bars + 8u * (4 * NST + 7);
+  auto pfull = [&](int s, int half) { return bars + 8u * (4 * NST + 3 + 2 * s + half); };  // 64 keys each
+  auto ofull = [&](int s) { return bars + 8u * (4 * NST + 7 + s); };
+  const uint32_t done = bars + 8u * (4 * NST + 9);
   volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(gbase + S::WORDS);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + S::WORDS + 4);
   volatile int* bad_values = reinterpret_cast<volatile int*>(gbase + S::WORDS + 8);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const int it = (int)blockIdx.x, ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
   const int i0 = (ia - ib * p.m_tiles) * (2 * kTaM), r = p.by_head(ib), h = ib - r * p.kv_heads;
   const int nq = min(2 * kTaM, p.m - i0);
   const bool wide = nq > kTaM;  // two tiles of queries; otherwise the slots share one
-  const int len = row_keys(p, r, tid == 0);
+  const int len = __shfl_sync(~0u, row_keys(p, r, tid == 0), 0);  // one value, known to be one
   const int nb = (len + kTaN - 1) / kTaN, nbt = nb + (p.nodes ? 1 : 0);
   const int per = (nbt + p.splits - 1) / p.splits;
   const int t_lo = min(split * per, nbt), nt = min(per, nbt - t_lo);  // this CTA's tiles
@@ -152,7 +163,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     mbar_init(qfull, 8);
     for (int s = 0; s < 2; ++s) {
       mbar_init(sfull(s), 1);
-      mbar_init(pfull(s), 4);
+      mbar_init(pfull(s, 0), 4);
+      mbar_init(pfull(s, 1), 4);
       mbar_init(ofull(s), 1);
     }
     mbar_init(done, 1);
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_at;
+  const uint32_t tmem = __shfl_sync(~0u, *tmem_at, 0);
   const Waits wait{abort, p.status, p.spin_limit_ns};
 
   if (warp == 0) {
@@ -211,39 +223,60 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && nt > 0) {
+    if (nt > 0) {
       // ---------------------------------------------------------------- products
+      // The whole warp walks the tiles, so that the compiler sees one path and keeps the operands
+      // of the products in uniform registers; one elected lane issues them.  (With one lane alone
+      // in the loop each product took some 90 cycles to issue, twice what it takes to run.)
       constexpr uint32_t ab = BF ? 1u : 0u;
       constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
       constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
       const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
+      const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K), v0 = desc_mn(base + S::V);
       bool ok = wait(qfull, 0);
       auto scores = [&](int s, int i) {
         const int t = tile_of(s, i), st = t % NST;
-        if (!(ok = ok && wait(kfull(st), (uint32_t)(t / NST) & 1u))) return;
+        if (!(ok = ok && __all_sync(~0u, wait(kfull(st), (uint32_t)(t / NST) & 1u)))) return;
         tc_fence_after();
-        const uint64_t a = desc_k(base + S::Q + (wide ? s : 0) * S::TILE), b = desc_k(base + S::K + st * S::TILE);
+        if (elect_one()) {
+          const uint64_t a = q0 + (wide ? s : 0) * (S::TILE >> 4), b = k0 + st * (S::TILE >> 4);
+          const uint32_t d = tmem + s * kTaN;
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k)
-          if (k < kd) {
+          for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
             const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
-            umma_f16(tmem + s * kTaN, a + off, b + off, id_s, k != 0);
+            umma_f16(d, a + off, b + off, id_s, k != 0);
           }
-        umma_commit(sfull(s));
-        if (!wide || s == 1) umma_commit(kempty(st));
+          umma_commit(sfull(s));
+          if (!wide || s == 1) umma_commit(kempty(st));
+        }
+        __syncwarp();
       };
       auto values = [&](int s, int i, bool last) {
         const int t = tile_of(s, i), st = t % NST;
-        if (!(ok = ok && wait(pfull(s), (uint32_t)i & 1u) && wait(vfull(st), (uint32_t)(t / NST) & 1u))) return;
-        tc_fence_after();
-        const uint64_t b = desc_mn(base + S::V + st * S::TILE);
+        if (!(ok = ok && __all_sync(~0u, wait(vfull(st), (uint32_t)(t / NST) & 1u)))) return;
         const int steps = (keys_of(t) + 15) / 16;
+        const uint64_t b = v0 + st * (S::TILE >> 4);
+        const uint32_t d = tmem + kTaO + s * kTaM, a = tmem + s * kTaN;
 #pragma unroll
-        for (int k = 0; k < kTaN / 16; ++k)
-          if (k < steps)
-            umma_f16_ts(tmem + kTaO + s * kTaM, tmem + s * kTaN + 8u * k, b + (uint64_t)k * (2048 >> 4), id_o, (i | k) != 0);
-        if (!wide || s == 1) umma_commit(vempty(st));
-        if (last) umma_commit(ofull(s));
+        for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
+          if (!(ok = ok && __all_sync(~0u, wait(pfull(s, half), (uint32_t)i & 1u)))) return;
+          tc_fence_after();
+          if (elect_one()) {
+            if (steps >= 4 * half + 4) {
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                umma_f16_ts(d, a + 8u * k, b + (uint64_t)k * (2048 >> 4), id_o, (i | k) != 0);
+            } else {
+              for (int k = 4 * half; k < steps; ++k)
+                umma_f16_ts(d, a + 8u * k, b + (uint64_t)k * (2048 >> 4), id_o, (i | k) != 0);
+            }
+            if (half == 1) {
+              if (!wide || s == 1) umma_commit(vempty(st));
+              if (last) umma_commit(ofull(s));
+            }
+          }
+          __syncwarp();
+        }
       };
       scores(0, 0);
       if (ok && jobs1 > 0) scores(1, 0);
@@ -255,7 +288,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (ok && i + 1 < jobs1) scores(1, i + 1);
         }
       }
-      umma_commit(done);
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
       mbar_wait_bounded(done, 0u, kTaDrainNs);
     }
     __syncwarp();
@@ -273,22 +307,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     bool ok = true;
     if (nt > 0) {
       // the slot's queries into shared memory (half of them each when the slots share a tile)
-      const uint32_t flip = p.negate ? 0x80008000u : 0u;
+      // by asynchronous copies, all under way at once
       const int rows = wide ? kTaM : kTaM / 2, r0 = wide ? 0 : slot * (kTaM / 2);
-      const uint32_t q_s = S::Q + (wide ? slot : 0) * S::TILE;
-#pragma unroll 4
+      const uint32_t q_s = base + S::Q + (wide ? slot : 0) * S::TILE;
       for (int e = wg; e < rows * (DP / 8); e += 128) {
         const int qr = r0 + e / (DP / 8), c = e % (DP / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (qr < qn && c * 8 < p.dim) {
-          const unsigned char* src = p.q.data + query_offset(p, p.q, r, h, i0 + (wide ? slot * kTaM : 0) + qr);
-          v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
+        const bool there = qr < qn && c * 8 < p.dim;
+        const unsigned char* src = there ? p.q.data + query_offset(p, p.q, r, h, i0 + (wide ? slot * kTaM : 0) + qr) + c * 16 : p.q.data;
+        cp_async16_fill(q_s + (c >> 3) * kTaPanel + qr * 128 + (((c & 7) ^ (qr & 7)) << 4), src, there ? 16 : 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (p.negate) {  // a negative scale: the queries' signs, each thread the vectors it copied
+        for (int e = wg; e < rows * (DP / 8); e += 128) {
+          const int qr = r0 + e / (DP / 8), c = e % (DP / 8);
+          uint4* v = reinterpret_cast<uint4*>(gbase + (q_s - base) + (c >> 3) * kTaPanel + qr * 128 + (((c & 7) ^ (qr & 7)) << 4));
+          *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
         }
-        *reinterpret_cast<uint4*>(gbase + q_s + (c >> 3) * kTaPanel + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = v;
       }
       fence_async_shared();
       __syncwarp();
@@ -298,6 +333,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + kTaO + slot * kTaM;
     float m_run = -INFINITY, l_run = 0.0f;
     const float c = p.scale_log2;  // not negative: a negative scale is in Q's sign
+    // the weights of half a tile (and the fixed-up values) are there for the products
+    auto hand_over = [&](int half) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull(slot, half));
+    };
     for (int i = 0; i < njobs; ++i) {
       const int t = tile_of(slot, i), n = keys_of(t);
       const bool draft = t_lo + t >= nb;
@@ -306,86 +347,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         break;
       }
       tc_fence_after();
-      __syncwarp();
-      if (warp_live) {
-        uint32_t s[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k * 32 < n) {
-            tmem_ld32_issue(ts + k * 32, s[k]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[k][j] = 0xff800000u;
-          }
-        }
-        tmem_wait_ld();
-        if (n < kTaN || dead_any || draft) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
-            if (!alive) see = 0u;
-            const int left = n - 32 * k;
-            if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[k][j] = (see >> j) & 1u ? s[k][j] : 0xff800000u;
-          }
-        }
-        float m4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a = __uint_as_float(s[k][0]), b = __uint_as_float(s[k][1]);
-#pragma unroll
-          for (int j = 2; j < 32; j += 2) {
-            a = fmaxf(a, __uint_as_float(s[k][j]));
-            b = fmaxf(b, __uint_as_float(s[k][j + 1]));
-          }
-          m4[k] = fmaxf(a, b);
-        }
-        const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-        const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
-        if (__any_sync(~0u, grow)) {
-          const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;
-          const float f = fast_exp2(m_run - sub);
-          m_run = to_m;
-          l_run *= f;
-          if (i > 0) {
-#pragma unroll 1
-            for (int k = 0; k < kd * 16; k += 32) {
-              uint32_t o[32];
-              tmem_ld32_issue(to + k, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(to + k, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float sub = m_run == -INFINITY ? 0.0f : m_run;
-        const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
-        float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k * 32 < n) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 x = make_float2(__uint_as_float(s[k][2 * j]), __uint_as_float(s[k][2 * j + 1]));
-              float2 e = __ffma2_rn(x, c2, b2);
-              e.x = fast_exp2(e.x);
-              e.y = fast_exp2(e.y);
-              if (j & 1)
-                l1 = __fadd2_rn(l1, e);
-              else
-                l0 = __fadd2_rn(l0, e);
-              w[j] = pack_pair<BF>(e.x, e.y);
-            }
-            tmem_st16(ts + k * 16, w);
-          }
-        }
-        l_run += (l0.x + l1.x) + (l0.y + l1.y);
-        tmem_wait_st();
-      }
+      // (only after the scores' wait: it says that the ring's slot has been through its last tile)
       // values of the tile's last 16 keys that lie past the row's end, and infinite and NaN
       // values of drafted tokens, must not meet weights of 0: they are made zero (the latter
       // are added back at the end to the queries that see them)
@@ -418,9 +380,85 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         fence_async_shared();
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pfull(slot));
+      if (warp_live) {
+        uint32_t s[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
+        tmem_wait_ld();
+        if (n < kTaN || dead_any || draft) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
+            if (!alive) see = 0u;
+            const int left = n - 32 * k;
+            if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[k][j] = (see >> j) & 1u ? s[k][j] : 0xff800000u;
+          }
+        }
+        float m4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a = max3(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]), __uint_as_float(s[k][2]));
+          float b = max3(__uint_as_float(s[k][3]), __uint_as_float(s[k][4]), __uint_as_float(s[k][5]));
+#pragma unroll
+          for (int j = 6; j < 30; j += 4) {
+            a = max3(a, __uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1]));
+            b = max3(b, __uint_as_float(s[k][j + 2]), __uint_as_float(s[k][j + 3]));
+          }
+          m4[k] = max3(a, b, fmaxf(__uint_as_float(s[k][30]), __uint_as_float(s[k][31])));
+        }
+        const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+        const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
+        if (__any_sync(~0u, grow)) {
+          const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;
+          const float f = fast_exp2(m_run - sub);
+          m_run = to_m;
+          l_run *= f;
+          if (i > 0) {
+#pragma unroll 1
+            for (int k = 0; k < kd * 16; k += 32) {
+              uint32_t o[32];
+              tmem_ld32_issue(to + k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(to + k, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float sub = m_run == -INFINITY ? 0.0f : m_run;
+        const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
+        float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = make_float2(__uint_as_float(s[k][2 * j]), __uint_as_float(s[k][2 * j + 1]));
+            float2 e = __ffma2_rn(x, c2, b2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            if (j & 1)
+              l1 = __fadd2_rn(l1, e);
+            else
+              l0 = __fadd2_rn(l0, e);
+            w[j] = pack_pair<BF>(e.x, e.y);
+          }
+          tmem_st16(ts + k * 16, w);
+          if (k == 1) {
+            tmem_wait_st();
+            hand_over(0);
+          }
+        }
+        l_run += (l0.x + l1.x) + (l0.y + l1.y);
+        tmem_wait_st();
+      } else {
+        hand_over(0);
+      }
+      hand_over(1);
     }
     if (ok && njobs > 0) ok = __all_sync(~0u, wait(ofull(slot), 0u));
     if (!wide && nt > 0) {
@@ -463,7 +501,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const AtView& vv = p.dvalue;
       const unsigned char* dv = vv.data + (long long)r * vv.row + (long long)h * vv.head;
       const long long pr = ((((long long)r * p.kv_heads + h) * p.m + qi) * p.splits) + split;
-      unsigned char* out = p.out.data + (mine ? query_offset(p, p.out, r, h, qi) : 0);
+      // a tile of output rows: in the key ring, which no product reads any more once slot 0's last
+      // one has ended (all scores were issued before it); joined slots, whose sums lie there, use
+      // the value ring
+      unsigned char* stage = gbase + (wide ? S::K + slot * S::TILE : S::V);
       if (mine && p.splits > 1) p.part_ml[pr] = make_float2(m_run, l_run);
 #pragma unroll 1
       for (int k = 0; k < p.dim; k += 32) {
@@ -492,17 +533,29 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
-          if (mine && k + j < p.dim) {
-            if (p.splits > 1) {
+          if (p.splits > 1) {
+            if (mine && k + j < p.dim) {
               float4* dst = reinterpret_cast<float4*>(p.part_o + pr * p.dim + k + j);
               dst[0] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
               dst[1] = make_float4(x[j + 4], x[j + 5], x[j + 6], x[j + 7]);
-            } else {
-              *reinterpret_cast<uint4*>(out + (k + j) * 2) =
+            }
+          } else {
+            const int v = (k + j) / 8;
+            if (v < DP / 8)
+              *reinterpret_cast<uint4*>(stage + row * (DP * 2) + ((v ^ (row & 7)) << 4)) =
                   make_uint4(pack_pair<BF>(x[j], x[j + 1]), pack_pair<BF>(x[j + 2], x[j + 3]),
                              pack_pair<BF>(x[j + 4], x[j + 5]), pack_pair<BF>(x[j + 6], x[j + 7]));
-            }
           }
+        }
+      }
+      if (p.splits == 1) {  // whole rows at a time, the warp's own 32
+        __syncwarp();
+        const int vecs = p.dim / 8;
+        for (int e = lane; e < 32 * (DP / 8); e += 32) {
+          const int rr = quarter * 32 + e / (DP / 8), v = e % (DP / 8);
+          if (rr < qn && v < vecs)
+            *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + (wide ? slot * kTaM : 0) + rr) + v * 16) =
+                *reinterpret_cast<const uint4*>(stage + rr * (DP * 2) + ((v ^ (rr & 7)) << 4));
         }
       }
     }
