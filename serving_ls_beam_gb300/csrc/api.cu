@@ -60,7 +60,7 @@ struct Debug {
 
 // LS_BEAM_DEBUG: comma-separated "exact", "ipplain", "iptma", "ipwords", "ipstatic", "steprefresh", "chunk", "strips",
 // "fused", "nofused", "cluster", "nocluster", "spin=<ns>", "vpl=<4|8|16>", "stages=<2..8>", "parts=<n>", "ipw=<words>",
-// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atstep", "atwarps=<1|4>", "atsplits=<n>".
+// "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atwarps=<1|4>", "atsplits=<n>".
 Debug read_debug() {
   Debug d;
   const char* env = std::getenv("LS_BEAM_DEBUG");
@@ -92,7 +92,6 @@ Debug read_debug() {
     else if (!std::strcmp(tok, "nocheck")) d.check_ptrs = false;
     else if (!std::strcmp(tok, "atsimt")) d.attend.kernel = kAtForceSimt;
     else if (!std::strcmp(tok, "atmma")) d.attend.kernel = kAtForceMma;
-    else if (!std::strcmp(tok, "atstep")) d.attend.kernel = kAtForceStep;
     else if (!std::strcmp(tok, "attc")) d.attend.kernel = kAtForceTc;
     else if (!std::strncmp(tok, "atwarps=", 8)) d.attend.warps = std::atoi(tok + 8) == 1 ? 1 : 4;
     else if (!std::strncmp(tok, "atsplits=", 9)) d.attend.splits = std::atoi(tok + 9);
@@ -417,6 +416,26 @@ bool pointers_reachable(const void* const* ptrs, int n) {
 long long wait_limit_ns() { return read_debug().spin_ns; }
 
 AttendDebug attend_debug() { return read_debug().attend; }
+
+bool encode_queries(CUtensorMap* map, const AttendParams& p, int dtype, int queries) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn || queries % p.group) return false;
+  // tokens run over the beams of a row: one stride where a beam's queries end where the next begin
+  if (p.beams > 1 && p.q_len > 1 && p.q.row != p.q_len * p.q.pos) return false;
+  const long long token = p.q_len > 1 ? p.q.pos : p.q.row;
+  const cuuint64_t dims[5] = {(cuuint64_t)p.dim, (cuuint64_t)p.group, (cuuint64_t)p.tokens, (cuuint64_t)p.kv_heads,
+                              (cuuint64_t)p.rows};
+  const cuuint64_t line = (cuuint64_t)((p.dim * 2 + 15) / 16 * 16);
+  auto stride = [&](long long bytes, int extent) { return extent > 1 ? (cuuint64_t)bytes : line; };
+  const cuuint64_t strides[4] = {stride(p.q.head, p.group), stride(token, p.tokens), stride(p.q.head * p.group, p.kv_heads),
+                                 stride(p.q.row * p.beams, p.rows)};
+  for (cuuint64_t s : strides)
+    if (s == 0 || s >= 1ull << 40) return false;
+  const cuuint32_t boxes[5] = {64, (cuuint32_t)p.group, (cuuint32_t)(queries / p.group), 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, dtype == LS_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, p.q.data,
+            dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool encode_attend(CUtensorMap* map, const AtView& v, int dtype, int dim, int pos, int heads, int rows, int box) {
   const EncodeTiledFn fn = encode_tiled_fn();

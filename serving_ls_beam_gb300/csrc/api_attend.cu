@@ -61,12 +61,14 @@ bool vectors16(const AtView& v) {
   return ((reinterpret_cast<uintptr_t>(v.data) | (uint64_t)v.row | (uint64_t)v.pos | (uint64_t)v.head) & 15) == 0;
 }
 
-// The tensor-core kernel's tensor maps: key, value and the drafted ones (copies of the key's
-// where there are none).  False where a map cannot describe the tensors.
-bool encode_maps(CUtensorMap (&maps)[4], const AttendParams& p, int dtype) {
+// The tensor-core kernel's tensor maps: key, value, the drafted ones and the queries (copies of the
+// key's where there are none).  False where a map cannot describe the tensors.
+bool encode_maps(CUtensorMap (&maps)[5], AttendParams& p, int dtype) {
   if (!encode_keys(maps, p, dtype, kAtTcBox)) return false;
   maps[2] = maps[0];
   maps[3] = maps[1];
+  maps[4] = maps[0];
+  p.q_tma = !p.negate && encode_queries(&maps[4], p, dtype, kAtTcQueries / 2);
   if (!p.nodes) return true;
   for (const AtView& v : {p.dkey, p.dvalue})
     if ((p.rows > 1 && v.row == 0) || (p.kv_heads > 1 && v.head == 0) || (p.nodes > 1 && v.pos == 0)) return false;
@@ -90,20 +92,19 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   const bool tensor = lines && dtype != LS_DTYPE_F32;
   p.kv_row_one = p.rows > 1 && p.key.row == 0;
   p.kv_head_one = p.kv_heads > 1 && p.key.head == 0;
-  CUtensorMap maps[4];
+  p.negate = p.scale_log2 < 0.0f;
+  CUtensorMap maps[5];
   const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
                   (dbg.kernel ? dbg.kernel == kAtForceTc : p.m > 32) && encode_maps(maps, p, dtype);
-  const bool step = !tc && lines && p.dim * es <= 512 &&
-                    (dbg.kernel ? dbg.kernel == kAtForceStep : dtype == LS_DTYPE_F32);
-  const bool mma = tensor && !tc && !step && dbg.kernel != kAtForceSimt && maps_describe(p);
+  const bool step = lines && dtype == LS_DTYPE_F32 && p.dim <= kAtStepDim && dbg.kernel != kAtForceSimt;
+  const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt && maps_describe(p);
   const int mq = tc     ? kAtTcQueries
-                 : step ? attend_step_queries(dtype, p.m)
+                 : step ? attend_step_queries(p.m)
                  : mma  ? attend_mma_queries(p.dim, p.m)
                         : attend_simt_queries(dtype, p.m);
   p.m_tiles = (p.m + mq - 1) / mq;
   const long long whole = base * p.m_tiles;
   if (tc) {
-    p.negate = p.scale_log2 < 0.0f;
     // a scale of 0 as 2^-100: masked scores stay -inf, and every weight still is exactly 1
     p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
@@ -121,7 +122,7 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.by_group.set(p.group);
   p.by_q_len.set(p.q_len);
   cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
-                  : step ? launch_attend_step(p, dtype, stream)
+                  : step ? launch_attend_step(p, stream)
                   : mma ? launch_attend_mma(p, dtype, stream)
                         : launch_attend_simt(p, dtype, stream);
   if (e == cudaSuccess && p.splits > 1) e = launch_attend_join(p, dtype, stream);

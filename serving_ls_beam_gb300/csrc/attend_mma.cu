@@ -90,21 +90,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// The two 16-bit values of w, zero where they are infinite or NaN; *hit is set for those.
-template <bool BF>
-__device__ __forceinline__ uint32_t finite2(uint32_t w, bool* hit) {
-  constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
-  if ((w & E) == E) {
-    w &= 0xffff0000u;
-    *hit = true;
-  }
-  if ((w & (E << 16)) == E << 16) {
-    w &= 0x0000ffffu;
-    *hit = true;
-  }
-  return w;
-}
-
 // The 8 x 8 matrix of 16-bit values whose row g lane (g, t) holds two of, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -385,13 +370,10 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         for (int e = from * CPR + lane; e < upto * CPR; e += 32) {
           const uint32_t a = vs + at(e / CPR, e % CPR);
           uint4 v = lds128(a);
-          bool bad = false;
-          v.x = finite2<BF>(v.x, &bad);
-          v.y = finite2<BF>(v.y, &bad);
-          v.z = finite2<BF>(v.z, &bad);
-          v.w = finite2<BF>(v.w, &bad);
-          if (bad) sts128(a, v);
-          hit |= bad;
+          if (clear_non_finite<BF>(v)) {
+            sts128(a, v);
+            hit = true;
+          }
         }
         bad_values |= __any_sync(~0u, hit);
         __syncwarp();
@@ -523,7 +505,8 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
       }
     } else {
       // the four warps' results, added in their order
-      constexpr int PITCH = DP + 4;
+      constexpr int PITCH = DP;
+      static_assert(8 * NQ * PITCH * 4 <= NS * S::STAGE, "within the rings: the barriers lie behind them");
       cp_async_wait<0>();
       __syncthreads();
       float* acc = reinterpret_cast<float*>(mm_raw + (rings - raw));

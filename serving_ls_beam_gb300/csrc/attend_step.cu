@@ -1,7 +1,5 @@
-// Attention of one to a few queries over a row's keys, for every type: the single-token step,
-// the beams of a sentence, fp32 models.  With at most four queries (eight in f32) per key the
-// products are too thin for the matrix instructions (15 of 16 operand rows would be empty), and
-// what counts is how many bytes are under way and how few instructions a key takes.
+// Attention over a row's keys in f32, one to eight queries at a time, on the CUDA cores.  What
+// counts is how many bytes are under way and how few instructions a key takes.
 //
 //   s_n = (scale q) . k_n,  o = sum_n 2^(s_n - max) v_n / sum_n 2^(s_n - max)
 //
@@ -35,26 +33,8 @@ __device__ __forceinline__ uint4 load_stream(const unsigned char* p) {
   return d;
 }
 
-template <int DT>
-__device__ __forceinline__ uint4 pack_vec(const float (&x)[Traits<DT>::kVec]) {
-  uint4 d;
-  if constexpr (DT == DT_F32) {
-    d = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == DT_F16) {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    d = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return d;
+__device__ __forceinline__ uint4 pack_vec(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
 // The 8 values of each lane summed over the lanes that differ in bits 0 to 2 (and up to LPK):
@@ -84,9 +64,9 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
   return c;
 }
 
-template <int DT, int LPK, int MQ>
+template <int LPK, int MQ>
 __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendParams p) {
-  constexpr int E = Traits<DT>::kVec, ES = Traits<DT>::kBytes, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
+  constexpr int DT = DT_F32, E = 4, ES = 4, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
   __shared__ unsigned long long trees[kAsWarps][kAtMaxNodes * 12 / 8];
   __shared__ float wm[kAsWarps][MQ], wl[kAsWarps][MQ];
   __shared__ float acc[kAsWarps][MQ][LPK * E + 4];
@@ -244,7 +224,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
           const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
 #pragma unroll
           for (int x = 0; x < E; ++x) y[x] = l[j] == 0.0f ? 0.0f : o[j][x] * inv;
-          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + c * 16) = pack_vec<DT>(y);
+          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + c * 16) = pack_vec(y);
         }
       }
     } else {
@@ -281,7 +261,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
           const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
           for (int x = 0; x < E; ++x) y[x] = L == 0.0f ? 0.0f : y[x] * inv;
-          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + x0 * ES) = pack_vec<DT>(y);
+          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + x0 * ES) = pack_vec(y);
         } else {
           const long long row = (((long long)r * p.kv_heads + h) * p.m + i0 + j) * p.splits + split;
 #pragma unroll
@@ -294,7 +274,7 @@ __global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendPar
   }
 }
 
-template <int DT, int LPK, int MQ>
+template <int LPK, int MQ>
 cudaError_t run_step(const AttendParams& p, cudaStream_t stream) {
   long long grid = p.items;
   if (p.warps == 1) {
@@ -302,45 +282,34 @@ cudaError_t run_step(const AttendParams& p, cudaStream_t stream) {
     if (occ == 0) {
       int n = 0;
       const cudaError_t e =
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attend_step_kernel<DT, LPK, MQ>, kAsThreads, 0);
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attend_step_kernel<LPK, MQ>, kAsThreads, 0);
       if (e != cudaSuccess) return e;
       occ = n > 0 ? n : 1;
     }
     const long long need = (p.items + kAsWarps - 1) / kAsWarps, fit = (long long)kAtSms * occ;
     grid = need < fit ? need : fit;
   }
-  attend_step_kernel<DT, LPK, MQ><<<(unsigned)grid, kAsThreads, 0, stream>>>(p);
+  attend_step_kernel<LPK, MQ><<<(unsigned)grid, kAsThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int DT, int LPK>
+template <int LPK>
 cudaError_t run_step_queries(const AttendParams& p, cudaStream_t stream) {
-  switch (attend_step_queries(DT, p.m)) {
-    case 1: return run_step<DT, LPK, 1>(p, stream);
-    case 2: return run_step<DT, LPK, 2>(p, stream);
-    case 4: return run_step<DT, LPK, 4>(p, stream);
-    default: break;
+  switch (attend_step_queries(p.m)) {
+    case 1: return run_step<LPK, 1>(p, stream);
+    case 2: return run_step<LPK, 2>(p, stream);
+    case 4: return run_step<LPK, 4>(p, stream);
+    default: return run_step<LPK, 8>(p, stream);
   }
-  if constexpr (DT == DT_F32) return run_step<DT, LPK, 8>(p, stream);
-  return cudaErrorInvalidValue;
-}
-
-template <int DT>
-cudaError_t run_step_dim(const AttendParams& p, cudaStream_t stream) {
-  const int chunks = p.dim / Traits<DT>::kVec;
-  if (chunks <= 8) return run_step_queries<DT, 8>(p, stream);
-  if (chunks <= 16) return run_step_queries<DT, 16>(p, stream);
-  return run_step_queries<DT, 32>(p, stream);
 }
 
 }  // namespace
 
-int attend_step_queries(int dtype, int m) { return m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 || dtype != DT_F32 ? 4 : 8; }
+int attend_step_queries(int m) { return m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 ? 4 : 8; }
 
-cudaError_t launch_attend_step(const AttendParams& p, int dtype, cudaStream_t stream) {
-  if (dtype == DT_F32) return run_step_dim<DT_F32>(p, stream);
-  if (dtype == DT_F16) return run_step_dim<DT_F16>(p, stream);
-  return run_step_dim<DT_BF16>(p, stream);
+cudaError_t launch_attend_step(const AttendParams& p, cudaStream_t stream) {
+  if (p.dim <= 32) return run_step_queries<8>(p, stream);
+  return p.dim <= 64 ? run_step_queries<16>(p, stream) : run_step_queries<32>(p, stream);
 }
 
 }  // namespace lsb

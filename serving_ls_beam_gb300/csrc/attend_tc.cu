@@ -1,23 +1,32 @@
 // Attention of many queries over a row's keys (f16 / bf16, head size up to 128) on the 5th
 // generation tensor cores: forced prefixes and scored targets of a cross attention, trees of
-// drafts whose nodes share their key heads.
+// drafts whose nodes share their key heads, long rows.
 //
 //   S = Q K^T,  P = exp2(c S - max),  O = O * correction + P V,  out = O / sum P
 //
 // with the running maximum and sum of the softmax (Milakov and Gimelshein, 2018).  One CTA per
-// SM, ten warps, tiles of 128 keys:
-//   warp 0     TMA producer: two rings of swizzled key and value tiles (64-element panels of
-//              128-byte rows); a tile's second 64 keys are not fetched when the row ends before;
-//   warp 1     owns the 512 tensor-memory columns; one lane issues S = Q K^T (Q and K from
-//              shared memory, M 128, N 128) and O += P V (P from tensor memory, V read as the
-//              transposed operand from the same [key][element] tile);
-//   warps 2-5, 6-9  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
+// SM takes item after item (up to 256 queries of one problem and one part of its keys), in tiles
+// of 128 keys; twelve warps, one of them idle:
+//   warp 8     TMA producer: two rings of swizzled key and value tiles (64-element panels of
+//              128-byte rows; a tile's second 64 keys are not fetched when the row ends before)
+//              and the queries, where their layout lets TMA read them in order;
+//   warp 9     owns the 512 tensor-memory columns and issues S = Q K^T (Q and K from shared
+//              memory, M 128, N 128) and O += P V (P from tensor memory, V read as the
+//              transposed operand from the same [key][element] tile).  The whole warp walks the
+//              jobs, so that the compiler sees one path and keeps the operands in uniform
+//              registers; an elected lane issues;
+//   warps 0-3, 4-7  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
 //              memory), reads its 128 scores, and writes its weights over them as 16-bit
-//              values (rounded to the tensors' type; sums are of the unrounded f32 weights).
-// While one slot's softmax runs, the tensor cores work for the other.  With more than 128
-// queries the slots are two tiles of queries over the same key tiles (each tile is fetched once
-// for 256 queries); with fewer they are the even and the odd key tiles of the same queries,
-// joined through shared memory at the end.
+//              values (rounded to the tensors' type; sums are of the unrounded f32 weights),
+//              handing each half to the products as it is written;
+//   warp 10    the queries by asynchronous copies where TMA cannot read them.
+// Jobs (a key tile of one slot) alternate between the slots, so that the tensor cores work for
+// one slot while the other's softmax runs.  With more than 128 queries the slots are two tiles of
+// queries over the same key tiles (each fetched once for 256 queries); with fewer they are the
+// even and the odd key tiles of the same queries, joined at the end: both warpgroups read both
+// accumulators and each writes half of the columns.  The score buffers (two for head sizes above
+// 64, three otherwise, what 512 columns hold) let scores run ahead of the values, also into the
+// next item.
 //
 // The accumulator is rescaled only when a query's maximum has grown by more than 2^8 since the
 // last time: until then its weights are at most 2^8 instead of 1, which f32 sums and the 16-bit
@@ -34,12 +43,11 @@
 namespace lsb {
 namespace {
 
-constexpr int kTaThreads = 320;
+constexpr int kTaThreads = 384;
 constexpr int kTaM = 128;   // queries of a slot
 constexpr int kTaN = 128;   // keys of a tile
 constexpr uint32_t kTaPanel = 128 * 128;  // 128 rows of 64 16-bit elements
 constexpr uint32_t kTaCols = 512;
-constexpr uint32_t kTaO = 256;            // tensor-memory columns: S of the slots at 0 and 128, O from here
 constexpr long long kTaDrainNs = 2000000000LL;
 constexpr float kTaLazy = 8.0f;           // growth of the maximum (log2) that is let pass
 
@@ -47,9 +55,15 @@ template <int DP>
 struct TcShape {
   static constexpr int PANELS = DP / 64;
   static constexpr int NST = DP == 64 ? 4 : 2;                 // stages of either ring
+  static constexpr int NSB = DP == 64 ? 3 : 2;                 // score buffers
+  static constexpr int NQB = DP == 64 ? 2 : 1;                 // pairs of query tiles
   static constexpr uint32_t TILE = PANELS * kTaPanel;          // 128 vectors of DP elements
-  static constexpr uint32_t Q = 0, K = 2 * TILE, V = K + NST * TILE, BAR = V + NST * TILE;
-  static constexpr int NBAR = 4 * NST + 1 + 2 + 4 + 2 + 1;     // full / empty x K / V, q, s, p x halves, o, done
+  static constexpr uint32_t Q = 0, K = 2 * NQB * TILE, V = K + NST * TILE, BAR = V + NST * TILE;
+  static constexpr uint32_t O = NSB * kTaN;                    // tensor-memory column of slot 0's sums
+  // barriers: full / empty of K and V, of the queries, scores, weights x halves, sums x slots, sums read, join, done
+  static constexpr int B_KF = 0, B_KE = NST, B_VF = 2 * NST, B_VE = 3 * NST, B_QF = 4 * NST, B_QE = B_QF + NQB,
+                       B_S = B_QE + NQB, B_P = B_S + NSB, B_O = B_P + 2 * NSB, B_OE = B_O + 2, B_J = B_OE + 1,
+                       B_DONE = B_J + 1, NBAR = B_DONE + 1;
   static constexpr uint32_t WORDS = BAR + 8 * NBAR;            // tensor-memory address, abort flag, value flag
   static constexpr uint32_t BYTES = WORDS + 16 + 1024;         // + alignment of the tiles
 };
@@ -84,7 +98,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void softmax_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Waits of this kernel: bounded, and given up when another role gave up.
 struct Waits {
@@ -112,457 +125,551 @@ struct Waits {
   }
 };
 
+// One item: the queries i0 .. i0 + nq of problem (r, h) and tiles t_lo .. t_lo + nt of its keys
+// (tile nb: the drafted tokens), in `jobs` jobs: job j belongs to slot j & 1.
+struct TcItem {
+  int r, h, i0, nq, split, len, nb, t_lo, nt, jobs;
+  bool wide;  // two tiles of queries; otherwise the slots share one
+  __device__ __forceinline__ int tile(int j) const { return wide ? j >> 1 : j; }
+  __device__ __forceinline__ bool draft(int t) const { return t_lo + t >= nb; }
+  __device__ __forceinline__ int keys(int t, int nodes) const { return draft(t) ? nodes : min(kTaN, len - (t_lo + t) * kTaN); }
+};
+__device__ __forceinline__ int tc_row(const AttendParams& p, int it) { return p.by_head(p.by_tile(p.by_split(it))); }
+__device__ __forceinline__ TcItem tc_item(const AttendParams& p, int it, int len) {
+  TcItem x;
+  const int a = p.by_split(it), b = p.by_tile(a);
+  x.split = it - a * p.splits;
+  x.i0 = (a - b * p.m_tiles) * (2 * kTaM);
+  x.r = p.by_head(b);
+  x.h = b - x.r * p.kv_heads;
+  x.nq = min(2 * kTaM, p.m - x.i0);
+  x.wide = x.nq > kTaM;
+  x.len = min(max(len, 0), p.max_len);
+  x.nb = (x.len + kTaN - 1) / kTaN;
+  const int nbt = x.nb + (p.nodes ? 1 : 0), per = p.splits == 1 ? nbt : (nbt + p.splits - 1) / p.splits;
+  x.t_lo = min(x.split * per, nbt);
+  x.nt = min(per, nbt - x.t_lo);
+  x.jobs = x.wide ? 2 * x.nt : x.nt;
+  return x;
+}
+
+// A walk over this CTA's items that have tiles: the next length is loaded while an item is worked on.
+struct TcWalk {
+  int it, next_len;
+  int active;   // items with tiles before this one
+  int job, tile;  // jobs and tiles before this item's
+  TcItem x;
+  bool valid;
+  __device__ __forceinline__ void load(const AttendParams& p, int i) {
+    // the shuffle tells the compiler that the value is one for the warp
+    next_len = __shfl_sync(~0u, i < (int)p.items ? __ldg(p.len + tc_row(p, i)) : 0, 0);
+  }
+  __device__ __forceinline__ void find(const AttendParams& p) {
+    for (; it < (int)p.items; it += gridDim.x) {
+      x = tc_item(p, it, next_len);
+      load(p, it + gridDim.x);
+      if (x.nt > 0) {
+        valid = true;
+        return;
+      }
+    }
+    valid = false;
+  }
+  __device__ __forceinline__ void begin(const AttendParams& p) {
+    it = blockIdx.x;
+    active = job = tile = 0;
+    load(p, it);
+    find(p);
+  }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    ++active;
+    job += x.jobs;
+    tile += x.nt;
+    it += gridDim.x;
+    find(p);
+  }
+};
+
 template <bool BF, int DP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
-                     const AttendParams p) {
+                     const __grid_constant__ CUtensorMap map_q, const AttendParams p) {
   using S = TcShape<DP>;
-  constexpr int NST = S::NST, DT = BF ? DT_BF16 : DT_F16;
+  constexpr int NST = S::NST, NSB = S::NSB, NQB = S::NQB, DT = BF ? DT_BF16 : DT_F16;
   extern __shared__ unsigned char ta_raw[];
-  __shared__ unsigned long long tree_raw[kAtMaxNodes * 12 / 8];
-  const TreeSeen tree = tree_at(tree_raw, kAtMaxNodes);
-  __shared__ float2 join_ml[kTaM];
+  __shared__ unsigned long long trees[8][kAtMaxNodes * 12 / 8];
+  __shared__ float2 join_ml[2][2][kTaM];
   const uint32_t raw = smem_addr(ta_raw), base = (raw + 1023u) & ~1023u;
   unsigned char* gbase = ta_raw + (base - raw);
-  const uint32_t bars = base + S::BAR;
-  auto kfull = [&](int s) { return bars + 8u * s; };
-  auto kempty = [&](int s) { return bars + 8u * (NST + s); };
-  auto vfull = [&](int s) { return bars + 8u * (2 * NST + s); };
-  auto vempty = [&](int s) { return bars + 8u * (3 * NST + s); };
-  const uint32_t qfull = bars + 8u * (4 * NST);
-  auto sfull = [&](int s) { return bars + 8u * (4 * NST + 1 + s); };
-  auto pfull = [&](int s, int half) { return bars + 8u * (4 * NST + 3 + 2 * s + half); };  // 64 keys each
-  auto ofull = [&](int s) { return bars + 8u * (4 * NST + 7 + s); };
-  const uint32_t done = bars + 8u * (4 * NST + 9);
+  auto bar = [&](int i) { return base + S::BAR + 8u * (uint32_t)i; };
   volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(gbase + S::WORDS);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + S::WORDS + 4);
+  // [2] item + 1, by turns: one slot's softmax may be an item ahead of the other's
   volatile int* bad_values = reinterpret_cast<volatile int*>(gbase + S::WORDS + 8);
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  const int it = (int)blockIdx.x, ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
-  const int i0 = (ia - ib * p.m_tiles) * (2 * kTaM), r = p.by_head(ib), h = ib - r * p.kv_heads;
-  const int nq = min(2 * kTaM, p.m - i0);
-  const bool wide = nq > kTaM;  // two tiles of queries; otherwise the slots share one
-  const int len = __shfl_sync(~0u, row_keys(p, r, tid == 0), 0);  // one value, known to be one
-  const int nb = (len + kTaN - 1) / kTaN, nbt = nb + (p.nodes ? 1 : 0);
-  const int per = (nbt + p.splits - 1) / p.splits;
-  const int t_lo = min(split * per, nbt), nt = min(per, nbt - t_lo);  // this CTA's tiles
-  const int jobs0 = wide ? nt : (nt + 1) / 2, jobs1 = wide ? nt : nt / 2;
-  auto tile_of = [&](int s, int i) { return wide ? i : 2 * i + s; };
-  auto keys_of = [&](int t) { return t_lo + t < nb ? min(kTaN, len - (t_lo + t) * kTaN) : p.nodes; };
   const int kd = (p.dim + 15) / 16;
-
   if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(kfull(s), 1);
-      mbar_init(kempty(s), 1);
-      mbar_init(vfull(s), 1);
-      mbar_init(vempty(s), 1);
+    for (int i = 0; i < S::NBAR; ++i) {
+      const bool weights = i >= S::B_P && i < S::B_O;  // one arrival per warp of the slot's softmax
+      const bool all = i == S::B_OE || i == S::B_J;    // one per softmax warp
+      mbar_init(bar(i), weights ? 4 : all ? 8 : 1);
     }
-    mbar_init(qfull, 8);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(sfull(s), 1);
-      mbar_init(pfull(s, 0), 4);
-      mbar_init(pfull(s, 1), 4);
-      mbar_init(ofull(s), 1);
-    }
-    mbar_init(done, 1);
     *abort = 0;
-    *bad_values = 0;
+    bad_values[0] = bad_values[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 1) {
+  if (warp == 9) {
     __syncwarp();
     tmem_alloc(base + S::WORDS, kTaCols);
     tmem_relinquish();
-  }
-  if (p.nodes) {
-    if (tree_seen(tree, p.parent + (long long)r * p.nodes, p.nodes, tid, kTaThreads, [] { __syncthreads(); }))
-      atomicOr(p.status, kDevInternal);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, *tmem_at, 0);
   const Waits wait{abort, p.status, p.spin_limit_ns};
+  auto wait_all = [&](int i, int phase) { return (bool)__all_sync(~0u, wait(bar(i), (uint32_t)phase & 1u)); };
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- producer
-      int kn = 0, vn = 0;
-      bool ok = true;
-      auto load = [&](int t, uint32_t ring, uint32_t full, uint32_t empty, const CUtensorMap* map, const CUtensorMap* dmap,
-                      int* count) {
-        const int st = t % NST;
-        if (t >= NST && !wait(empty, (uint32_t)(t / NST - 1) & 1u)) {
-          ok = false;
-          return;
-        }
-        const bool draft = t_lo + t >= nb;
-        const int halves = draft || keys_of(t) <= 64 ? 1 : 2;
-        mbar_arrive_expect_tx(full, (uint32_t)(halves * S::PANELS) * (kTaPanel / 2));
-        for (int c = 0; c < S::PANELS; ++c)
-          for (int hf = 0; hf < halves; ++hf) {
-            const uint32_t dst = ring + st * S::TILE + c * kTaPanel + hf * (kTaPanel / 2);
-            if (draft)
-              tma_load_4d(dst, dmap, c * 64, 0, h, r, full);
-            else
-              tma_load_4d(dst, map, c * 64, (t_lo + t) * kTaN + hf * 64, p.kv_head_one ? 0 : h, p.kv_row_one ? 0 : r, full);
-          }
-        *count = t + 1;
-      };
-      for (int t = -1; t < nt && ok; ++t) {
-        if (t + 1 < nt) load(t + 1, base + S::K, kfull((t + 1) % NST), kempty((t + 1) % NST), &map_k, &map_dk, &kn);
-        if (t >= 0 && ok) load(t, base + S::V, vfull(t % NST), vempty(t % NST), &map_v, &map_dv, &vn);
+  // the softmax threads hold 128 scores each: they get the registers that the other warps do not
+  // need (2 * 128 * 208 + 128 * 88 = 384 * 168, the launch's)
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------------------------------------------------------- softmax
+    const int slot = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane, wg = tid - slot * 128;
+    const TreeSeen tree = tree_at(trees[warp], kAtMaxNodes);
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t to = lanes + S::O + slot * DP, other_o = lanes + S::O + (slot ^ 1) * DP;
+    const float c = p.scale_log2;  // not negative: a negative scale is in Q's sign
+    int next_len = blockIdx.x < p.items ? __ldg(p.len + tc_row(p, blockIdx.x)) : 0;
+    int jobs_before = 0, tiles_before = 0, joins = 0;
+    int sums[2] = {0, 0};  // products of either slot in the items before
+    bool ok = true;
+    int turn = 1;
+    for (int it = blockIdx.x; it < (int)p.items && ok; it += gridDim.x) {
+      turn ^= 1;
+      const TcItem x = tc_item(p, it, next_len);
+      if (x.len != next_len && tid == 0) atomicOr(p.status, kDevInternal);
+      if (it + gridDim.x < p.items) next_len = __ldg(p.len + tc_row(p, it + gridDim.x));
+      const int qn = x.wide ? min(kTaM, x.nq - slot * kTaM) : x.nq;  // queries of the slot
+      const int qi = x.i0 + (x.wide ? slot * kTaM : 0) + row;
+      const bool mine = row < qn, warp_live = quarter * 32 < qn;
+      unsigned long long sees = 0ull;
+      if (p.nodes) {
+        __syncwarp();
+        if (tree_seen(tree, p.parent + (long long)x.r * p.nodes, p.nodes, lane, 32, [] { __syncwarp(); }))
+          atomicOr(p.status, kDevInternal);
+        if (mine) sees = tree.mask[p.by_group(qi)];
       }
-      if (*abort) {  // every copy issued lands before the CTA may exit
-        for (int t = max(0, kn - NST); t < kn; ++t) mbar_wait_bounded(kfull(t % NST), (uint32_t)(t / NST) & 1u, kTaDrainNs);
-        for (int t = max(0, vn - NST); t < vn; ++t) mbar_wait_bounded(vfull(t % NST), (uint32_t)(t / NST) & 1u, kTaDrainNs);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (nt > 0) {
-      // ---------------------------------------------------------------- products
-      // The whole warp walks the tiles, so that the compiler sees one path and keeps the operands
-      // of the products in uniform registers; one elected lane issues them.  (With one lane alone
-      // in the loop each product took some 90 cycles to issue, twice what it takes to run.)
-      constexpr uint32_t ab = BF ? 1u : 0u;
-      constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
-      constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
-      const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
-      const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K), v0 = desc_mn(base + S::V);
-      bool ok = wait(qfull, 0);
-      auto scores = [&](int s, int i) {
-        const int t = tile_of(s, i), st = t % NST;
-        if (!(ok = ok && __all_sync(~0u, wait(kfull(st), (uint32_t)(t / NST) & 1u)))) return;
+      const bool alive = mine && (!p.nodes || sees != 0);
+      const bool dead_any = __any_sync(~0u, !alive);
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int j = slot; j < x.jobs; j += 2) {
+        const int t = x.tile(j), n = x.keys(t, p.nodes), b = (jobs_before + j) % NSB;
+        const uint32_t ts = lanes + b * kTaN;
+        const bool draft = x.draft(t);
+        // the weights of half a tile (and the fixed-up values) are there for the products
+        auto hand_over = [&](int half) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(S::B_P + 2 * b + half));
+        };
+        if (!(ok = wait_all(S::B_S + b, (jobs_before + j) / NSB))) break;
         tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = q0 + (wide ? s : 0) * (S::TILE >> 4), b = k0 + st * (S::TILE >> 4);
-          const uint32_t d = tmem + s * kTaN;
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
-            const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
-            umma_f16(d, a + off, b + off, id_s, k != 0);
+        // (only after the scores' wait: it says that the ring's slot has been through its last tile)
+        // values of the tile's last 16 keys that lie past the row's end, and infinite and NaN
+        // values of drafted tokens, must not meet weights of 0: they are made zero (the latter
+        // are added back at the end to the queries that see them)
+        if ((n & 15 || (draft && p.nodes > 1)) && (!x.wide || slot == 0)) {
+          const int g = tiles_before + t;
+          if (!(ok = wait_all(S::B_VF + g % NST, g / NST))) break;
+          unsigned char* v = gbase + S::V + (g % NST) * S::TILE;
+          const int fill = (16 - (n & 15)) & 15;
+          for (int e = wg; e < fill * (DP / 8); e += 128) {
+            const int key = n + e / (DP / 8), xx = e % (DP / 8);
+            *reinterpret_cast<uint4*>(v + (xx >> 3) * kTaPanel + key * 128 + (xx & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
-          umma_commit(sfull(s));
-          if (!wide || s == 1) umma_commit(kempty(st));
+          if (draft && p.nodes > 1) {
+            for (int e = wg; e < n * (DP / 8); e += 128) {
+              const int key = e / (DP / 8), xx = e % (DP / 8);
+              uint4* at = reinterpret_cast<uint4*>(v + (xx >> 3) * kTaPanel + key * 128 + (xx & 7) * 16);
+              uint4 d = *at;
+              if (clear_non_finite<BF>(d)) {
+                *at = d;
+                bad_values[turn] = it + 1;
+              }
+            }
+          }
+          fence_async_shared();
         }
         __syncwarp();
-      };
-      auto values = [&](int s, int i, bool last) {
-        const int t = tile_of(s, i), st = t % NST;
-        if (!(ok = ok && __all_sync(~0u, wait(vfull(st), (uint32_t)(t / NST) & 1u)))) return;
-        const int steps = (keys_of(t) + 15) / 16;
-        const uint64_t b = v0 + st * (S::TILE >> 4);
-        const uint32_t d = tmem + kTaO + s * kTaM, a = tmem + s * kTaN;
+        if (warp_live) {
+          uint32_t s[4][32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
-          if (!(ok = ok && __all_sync(~0u, wait(pfull(s, half), (uint32_t)i & 1u)))) return;
-          tc_fence_after();
-          if (elect_one()) {
-            if (steps >= 4 * half + 4) {
+          for (int k = 0; k < 4; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
+          tmem_wait_ld(s[0]);
 #pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                umma_f16_ts(d, a + 8u * k, b + (uint64_t)k * (2048 >> 4), id_o, (i | k) != 0);
-            } else {
-              for (int k = 4 * half; k < steps; ++k)
-                umma_f16_ts(d, a + 8u * k, b + (uint64_t)k * (2048 >> 4), id_o, (i | k) != 0);
-            }
-            if (half == 1) {
-              if (!wide || s == 1) umma_commit(vempty(st));
-              if (last) umma_commit(ofull(s));
+          for (int k = 1; k < 4; ++k) tmem_after_wait(s[k]);
+          if (n < kTaN || dead_any || draft) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
+              if (!alive) see = 0u;
+              const int left = n - 32 * k;
+              if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[k][i] = (see >> i) & 1u ? s[k][i] : 0xff800000u;
             }
           }
-          __syncwarp();
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float a = max3(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]), __uint_as_float(s[k][2]));
+            float bb = max3(__uint_as_float(s[k][3]), __uint_as_float(s[k][4]), __uint_as_float(s[k][5]));
+#pragma unroll
+            for (int i = 6; i < 30; i += 4) {
+              a = max3(a, __uint_as_float(s[k][i]), __uint_as_float(s[k][i + 1]));
+              bb = max3(bb, __uint_as_float(s[k][i + 2]), __uint_as_float(s[k][i + 3]));
+            }
+            m4[k] = max3(a, bb, fmaxf(__uint_as_float(s[k][30]), __uint_as_float(s[k][31])));
+          }
+          const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+          const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
+          if (__any_sync(~0u, grow)) {
+            const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;
+            const float f = fast_exp2(m_run - sub);
+            m_run = to_m;
+            l_run *= f;
+            if (j >= 2) {
+              // the slot's product before this one has to end first (with three score buffers it may
+              // still run); a slot's products complete its barrier one phase each
+              if (!(ok = wait_all(S::B_O + slot, sums[slot] + (j >> 1) - 1))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < kd * 16; k += 32) {
+                uint32_t o[32];
+                tmem_ld32_issue(to + k, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + k, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float sub = m_run == -INFINITY ? 0.0f : m_run;
+          const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
+          float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t wt[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = make_float2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1]));
+              float2 e = __ffma2_rn(y, c2, b2);
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
+              if (i & 1)
+                l1 = __fadd2_rn(l1, e);
+              else
+                l0 = __fadd2_rn(l0, e);
+              wt[i] = pack_pair<BF>(e.x, e.y);
+            }
+            tmem_st16(ts + k * 16, wt);
+            if (k == 1) {
+              tmem_wait_st();
+              hand_over(0);
+            }
+          }
+          l_run += (l0.x + l1.x) + (l0.y + l1.y);
+          tmem_wait_st();
+        } else {
+          hand_over(0);
         }
-      };
-      scores(0, 0);
-      if (ok && jobs1 > 0) scores(1, 0);
-      for (int i = 0; i < jobs0 && ok; ++i) {
-        values(0, i, i + 1 == jobs0);
-        if (ok && i + 1 < jobs0) scores(0, i + 1);
-        if (i < jobs1) {
-          if (ok) values(1, i, i + 1 == jobs1);
-          if (ok && i + 1 < jobs1) scores(1, i + 1);
+        // A parity tells neighbouring phases apart, no more: the slot's last product is waited for
+        // before the weights that let the next one complete (it has ended by now, as a rule).
+        if (j >= 2 && !(ok = wait_all(S::B_O + slot, sums[slot] + (j >> 1) - 1))) break;
+        hand_over(1);
+      }
+      // the slot's sums (when the slots share the queries, both slots')
+      if (ok && x.jobs > slot) {
+        ok = wait_all(S::B_O + slot, sums[slot] + (x.jobs - slot + 1) / 2 - 1);
+      }
+      // an item of one job: slot 1 keeps pace with it (it says below that the sums are read)
+      if (ok && x.jobs == 1 && slot == 1) ok = wait_all(S::B_O, sums[0]);
+      const bool joined = !x.wide && x.jobs > 1;
+      float f = 1.0f, f_other = 0.0f;
+      if (joined && ok) {
+        ok = wait_all(S::B_O + (slot ^ 1), sums[slot ^ 1] + (x.jobs - (slot ^ 1) + 1) / 2 - 1);
+        join_ml[joins & 1][slot][row] = make_float2(m_run, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::B_J));
+        ok = ok && wait_all(S::B_J, joins);
+        if (ok) {
+          const float2 o = join_ml[joins & 1][slot ^ 1][row];
+          const float M = fmaxf(m_run, o.x), sub = M == -INFINITY ? 0.0f : M;
+          f = fast_exp2(m_run - sub);
+          f_other = fast_exp2(o.x - sub);
+          l_run = f * l_run + f_other * o.y;
+          m_run = M;
+        }
+        ++joins;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      if (warp_live && (x.wide || joined || slot == 0)) {
+        const bool zero = l_run == 0.0f;
+        if (p.splits == 1) {
+          const float inv = zero ? 0.0f : 1.0f / l_run;
+          f *= inv;
+          f_other *= inv;
+        }
+        const bool has_bad = bad_values[turn] == it + 1;
+        const bool rare = has_bad || __any_sync(~0u, zero);
+        const unsigned char* dv = p.dvalue.data + (long long)x.r * p.dvalue.row + (long long)x.h * p.dvalue.head;
+        const long long pr = (((long long)x.r * p.kv_heads + x.h) * p.m + qi) * p.splits + x.split;
+        unsigned char* out = p.out.data + (mine ? query_offset(p, p.out, x.r, x.h, qi) : 0);
+        if (mine && p.splits > 1 && (!joined || slot == 0)) p.part_ml[pr] = make_float2(m_run, l_run);
+#pragma unroll 1
+        for (int k = joined ? 32 * slot : 0; k < p.dim; k += joined ? 64 : 32) {
+          uint32_t o[32];
+          __syncwarp();  // the loads are warp-wide
+          if (x.nt > 0) {
+            tmem_ld32_issue(to + k, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          float y[32];
+          if (joined) {
+            uint32_t o2[32];
+            tmem_ld32_issue(other_o + k, o2);
+            tmem_wait_ld(o);
+            tmem_after_wait(o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(o2[i]), f_other, __uint_as_float(o[i]) * f);
+          } else {
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(o[i]) * f;
+          }
+          if (rare) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = zero ? 0.0f : y[i];
+            if (has_bad)
+              for (int nd = 0; nd < p.nodes; ++nd)
+                if ((sees >> nd) & 1ull)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (k + i < p.dim) {
+                      const float v = load_elem<DT>(dv + nd * p.dvalue.pos + (k + i) * 2);
+                      if (!isfinite(v)) y[i] += v;
+                    }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (mine && k + i < p.dim) {
+              if (p.splits > 1) {
+                float4* dst = reinterpret_cast<float4*>(p.part_o + pr * p.dim + k + i);
+                dst[0] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                dst[1] = make_float4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
+              } else {
+                *reinterpret_cast<uint4*>(out + (k + i) * 2) =
+                    make_uint4(pack_pair<BF>(y[i], y[i + 1]), pack_pair<BF>(y[i + 2], y[i + 3]),
+                               pack_pair<BF>(y[i + 4], y[i + 5]), pack_pair<BF>(y[i + 6], y[i + 7]));
+              }
+            }
+          }
         }
       }
-      if (elect_one()) umma_commit(done);
       __syncwarp();
-      mbar_wait_bounded(done, 0u, kTaDrainNs);
+      if (x.nt > 0) {
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(bar(S::B_OE));
+        jobs_before += x.jobs;
+        tiles_before += x.nt;
+        sums[0] += (x.jobs + 1) / 2;
+        sums[1] += x.jobs / 2;
+      }
     }
-    __syncwarp();
   } else {
-    // ---------------------------------------------------------------- softmax
-    const int slot = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane, wg = tid - 64 - slot * 128;
-    const int qn = wide ? min(kTaM, nq - slot * kTaM) : nq;  // queries of the slot
-    const int qi = i0 + (wide ? slot * kTaM : 0) + row;
-    const bool mine = row < qn;
-    const bool warp_live = quarter * 32 < qn;
-    const unsigned long long sees = mine && p.nodes ? tree.mask[p.by_group(qi)] : 0ull;
-    const bool alive = mine && (!p.nodes || sees != 0);
-    const bool dead_any = __any_sync(~0u, !alive);
-    const int njobs = slot ? jobs1 : jobs0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
+    // ---------------------------------------------------------------- producer
+    TcWalk w;
+    w.begin(p);
     bool ok = true;
-    if (nt > 0) {
-      // the slot's queries into shared memory (half of them each when the slots share a tile)
-      // by asynchronous copies, all under way at once
-      const int rows = wide ? kTaM : kTaM / 2, r0 = wide ? 0 : slot * (kTaM / 2);
-      const uint32_t q_s = base + S::Q + (wide ? slot : 0) * S::TILE;
-      for (int e = wg; e < rows * (DP / 8); e += 128) {
-        const int qr = r0 + e / (DP / 8), c = e % (DP / 8);
-        const bool there = qr < qn && c * 8 < p.dim;
-        const unsigned char* src = there ? p.q.data + query_offset(p, p.q, r, h, i0 + (wide ? slot * kTaM : 0) + qr) + c * 16 : p.q.data;
-        cp_async16_fill(q_s + (c >> 3) * kTaPanel + qr * 128 + (((c & 7) ^ (qr & 7)) << 4), src, there ? 16 : 0);
+    int kn = 0, vn = 0, qn = 0;  // tiles and query sets asked for
+    for (; w.valid && ok; w.next(p)) {
+      const TcItem& x = w.x;
+      auto load = [&](int t, uint32_t ring, int full, int empty, const CUtensorMap* map, const CUtensorMap* dmap, int* count) {
+        const int g = w.tile + t, st = g % NST;
+        if (g >= NST && !(ok = wait_all(empty + st, g / NST - 1))) return;
+        if (elect_one()) {
+          const bool draft = x.draft(t);
+          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : 2;
+          mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (kTaPanel / 2));
+          for (int c = 0; c < S::PANELS; ++c)
+            for (int hf = 0; hf < halves; ++hf) {
+              const uint32_t dst = base + ring + st * S::TILE + c * kTaPanel + hf * (kTaPanel / 2);
+              if (draft)
+                tma_load_4d(dst, dmap, c * 64, 0, x.h, x.r, bar(full + st));
+              else
+                tma_load_4d(dst, map, c * 64, (x.t_lo + t) * kTaN + hf * 64, p.kv_head_one ? 0 : x.h,
+                            p.kv_row_one ? 0 : x.r, bar(full + st));
+            }
+        }
+        __syncwarp();
+        *count = g + 1;
+      };
+      load(0, S::K, S::B_KF, S::B_KE, &map_k, &map_dk, &kn);
+      if (p.q_tma && ok) {
+        const int g = w.active, st = g % NQB;
+        if (g >= NQB) ok = wait_all(S::B_QE + st, g / NQB - 1);
+        if (ok && elect_one()) {
+          const int slots = x.wide ? 2 : 1, token = p.by_group(x.i0);
+          mbar_arrive_expect_tx(bar(S::B_QF + st), (uint32_t)slots * S::TILE);
+          for (int s = 0; s < slots; ++s)
+            for (int c = 0; c < S::PANELS; ++c)
+              tma_load_5d(base + S::Q + (2 * st + s) * S::TILE + c * kTaPanel, &map_q, c * 64, 0, token + s * p.by_group(kTaM),
+                          x.h, x.r, bar(S::B_QF + st));
+        }
+        __syncwarp();
+        if (ok) qn = g + 1;
+      }
+      for (int t = 0; t < x.nt && ok; ++t) {
+        if (t + 1 < x.nt) load(t + 1, S::K, S::B_KF, S::B_KE, &map_k, &map_dk, &kn);
+        if (ok) load(t, S::V, S::B_VF, S::B_VE, &map_v, &map_dv, &vn);
+      }
+    }
+    if (!ok) {  // every copy issued lands before the CTA may exit
+      for (int g = max(0, kn - NST); g < kn; ++g) mbar_wait_bounded(bar(S::B_KF + g % NST), (uint32_t)(g / NST) & 1u, kTaDrainNs);
+      for (int g = max(0, vn - NST); g < vn; ++g) mbar_wait_bounded(bar(S::B_VF + g % NST), (uint32_t)(g / NST) & 1u, kTaDrainNs);
+      for (int g = max(0, qn - NQB); g < qn; ++g) mbar_wait_bounded(bar(S::B_QF + g % NQB), (uint32_t)(g / NQB) & 1u, kTaDrainNs);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t ab = BF ? 1u : 0u;
+    constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
+    constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
+    const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
+    const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K), v0 = desc_mn(base + S::V);
+    bool ok = true;
+    auto scores = [&](const TcWalk& w, int j) {
+      const TcItem& x = w.x;
+      const int t = w.tile + x.tile(j), st = t % NST, b = (w.job + j) % NSB, qs = w.active % NQB, s = j & 1;
+      if (j == 0 && !(ok = wait_all(S::B_QF + qs, w.active / NQB))) return;
+      if (!(ok = wait_all(S::B_KF + st, t / NST))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t a = q0 + (2 * qs + (x.wide ? s : 0)) * (S::TILE >> 4), bd = k0 + st * (S::TILE >> 4);
+        const uint32_t d = tmem + b * kTaN;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
+          const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
+          umma_f16(d, a + off, bd + off, id_s, k != 0);
+        }
+        umma_commit(bar(S::B_S + b));
+        if (!x.wide || s == 1) umma_commit(bar(S::B_KE + st));
+        if (j + 1 == x.jobs) umma_commit(bar(S::B_QE + qs));
+      }
+      __syncwarp();
+    };
+    auto values = [&](const TcWalk& w, int j) {
+      const TcItem& x = w.x;
+      const int t = w.tile + x.tile(j), st = t % NST, b = (w.job + j) % NSB, s = j & 1;
+      // the last item's sums are read before the first product of this one replaces them
+      if (j == 0 && w.active > 0 && !(ok = wait_all(S::B_OE, w.active - 1))) return;
+      if (!(ok = wait_all(S::B_VF + st, t / NST))) return;
+      const int steps = (x.keys(x.tile(j), p.nodes) + 15) / 16;
+      const uint64_t bd = v0 + st * (S::TILE >> 4);
+      const uint32_t d = tmem + S::O + s * DP, a = tmem + b * kTaN;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
+        if (!(ok = wait_all(S::B_P + 2 * b + half, (w.job + j) / NSB))) return;
+        tc_fence_after();
+        if (elect_one()) {
+          if (steps >= 4 * half + 4) {
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+          } else {
+            for (int k = 4 * half; k < steps; ++k)
+              umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+          }
+          if (half == 1) {
+            if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
+            umma_commit(bar(S::B_O + s));
+          }
+        }
+        __syncwarp();
+      }
+    };
+    TcWalk ws, wv;  // scores run NSB jobs ahead of the values
+    ws.begin(p);
+    wv.begin(p);
+    int js = 0, jv = 0;
+    auto step = [&] {
+      if (ws.valid && ok) {
+        scores(ws, js);
+        if (++js == ws.x.jobs) {
+          js = 0;
+          ws.next(p);
+        }
+      }
+    };
+    for (int i = 0; i < NSB; ++i) step();
+    while (wv.valid && ok) {
+      values(wv, jv);
+      if (++jv == wv.x.jobs) {
+        jv = 0;
+        wv.next(p);
+      }
+      step();
+    }
+    if (elect_one()) umma_commit(bar(S::B_DONE));
+    __syncwarp();
+    mbar_wait_bounded(bar(S::B_DONE), 0u, kTaDrainNs);
+  } else if (warp == 10 && !p.q_tma) {
+    // ---------------------------------------------------------------- queries
+    TcWalk w;
+    w.begin(p);
+    bool ok = true;
+    for (; w.valid && ok; w.next(p)) {
+      const TcItem& x = w.x;
+      const int st = w.active % NQB;
+      if (w.active >= NQB && !(ok = wait_all(S::B_QE + st, w.active / NQB - 1))) break;
+      const int rows = x.wide ? 2 * kTaM : kTaM;
+      auto place = [&](int e) {
+        const int qr = e / (DP / 8), ch = e % (DP / 8);
+        return S::Q + (2 * st + (qr >> 7)) * S::TILE + (ch >> 3) * kTaPanel + (qr & 127) * 128 + (((ch & 7) ^ (qr & 7)) << 4);
+      };
+      for (int r0 = 0; r0 < rows; r0 += 32) {  // each lane knows one row's address
+        const long long mine = r0 + lane < x.nq ? query_offset(p, p.q, x.r, x.h, x.i0 + r0 + lane) : 0;
+        for (int e = r0 * (DP / 8) + lane; e < (r0 + 32) * (DP / 8); e += 32) {
+          const int qr = e / (DP / 8), ch = e % (DP / 8);
+          const long long off = __shfl_sync(~0u, mine, qr - r0);
+          const bool there = qr < x.nq && ch * 8 < p.dim;
+          cp_async16_fill(base + place(e), there ? p.q.data + off + ch * 16 : p.q.data, there ? 16 : 0);
+        }
       }
       cp_async_commit();
       cp_async_wait<0>();
-      if (p.negate) {  // a negative scale: the queries' signs, each thread the vectors it copied
-        for (int e = wg; e < rows * (DP / 8); e += 128) {
-          const int qr = r0 + e / (DP / 8), c = e % (DP / 8);
-          uint4* v = reinterpret_cast<uint4*>(gbase + (q_s - base) + (c >> 3) * kTaPanel + qr * 128 + (((c & 7) ^ (qr & 7)) << 4));
+      if (p.negate) {  // a negative scale: the queries' signs, each lane the vectors it copied
+        for (int e = lane; e < rows * (DP / 8); e += 32) {
+          uint4* v = reinterpret_cast<uint4*>(gbase + place(e));
           *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
         }
       }
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
+      if (lane == 0) mbar_arrive(bar(S::B_QF + st));
     }
-    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + slot * kTaN;
-    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + kTaO + slot * kTaM;
-    float m_run = -INFINITY, l_run = 0.0f;
-    const float c = p.scale_log2;  // not negative: a negative scale is in Q's sign
-    // the weights of half a tile (and the fixed-up values) are there for the products
-    auto hand_over = [&](int half) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pfull(slot, half));
-    };
-    for (int i = 0; i < njobs; ++i) {
-      const int t = tile_of(slot, i), n = keys_of(t);
-      const bool draft = t_lo + t >= nb;
-      if (!__all_sync(~0u, wait(sfull(slot), (uint32_t)i & 1u))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // (only after the scores' wait: it says that the ring's slot has been through its last tile)
-      // values of the tile's last 16 keys that lie past the row's end, and infinite and NaN
-      // values of drafted tokens, must not meet weights of 0: they are made zero (the latter
-      // are added back at the end to the queries that see them)
-      if ((n & 15 || (draft && p.nodes > 1)) && (!wide || slot == 0)) {
-        if (!__all_sync(~0u, wait(vfull(t % NST), (uint32_t)(t / NST) & 1u))) {
-          ok = false;
-          break;
-        }
-        unsigned char* v = gbase + S::V + (t % NST) * S::TILE;
-        const int fill = (16 - (n & 15)) & 15;
-        for (int e = wg; e < fill * (DP / 8); e += 128) {
-          const int key = n + e / (DP / 8), x = e % (DP / 8);
-          *reinterpret_cast<uint4*>(v + (x >> 3) * kTaPanel + key * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (draft && p.nodes > 1) {
-          for (int e = wg; e < n * (DP / 8); e += 128) {
-            const int key = e / (DP / 8), x = e % (DP / 8);
-            uint32_t* at = reinterpret_cast<uint32_t*>(v + (x >> 3) * kTaPanel + key * 128 + (x & 7) * 16);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              constexpr uint32_t E = BF ? 0x7f80u : 0x7c00u;
-              const uint32_t w = at[j];
-              const bool lo = (w & E) == E, hi = (w >> 16 & E) == E;
-              if (lo || hi) {
-                at[j] = w & (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-                *bad_values = 1;
-              }
-            }
-          }
-        }
-        fence_async_shared();
-      }
-      __syncwarp();
-      if (warp_live) {
-        uint32_t s[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
-        tmem_wait_ld();
-        if (n < kTaN || dead_any || draft) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
-            if (!alive) see = 0u;
-            const int left = n - 32 * k;
-            if (left < 32) see &= left <= 0 ? 0u : (1u << left) - 1u;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[k][j] = (see >> j) & 1u ? s[k][j] : 0xff800000u;
-          }
-        }
-        float m4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a = max3(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]), __uint_as_float(s[k][2]));
-          float b = max3(__uint_as_float(s[k][3]), __uint_as_float(s[k][4]), __uint_as_float(s[k][5]));
-#pragma unroll
-          for (int j = 6; j < 30; j += 4) {
-            a = max3(a, __uint_as_float(s[k][j]), __uint_as_float(s[k][j + 1]));
-            b = max3(b, __uint_as_float(s[k][j + 2]), __uint_as_float(s[k][j + 3]));
-          }
-          m4[k] = max3(a, b, fmaxf(__uint_as_float(s[k][30]), __uint_as_float(s[k][31])));
-        }
-        const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-        const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
-        if (__any_sync(~0u, grow)) {
-          const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;
-          const float f = fast_exp2(m_run - sub);
-          m_run = to_m;
-          l_run *= f;
-          if (i > 0) {
-#pragma unroll 1
-            for (int k = 0; k < kd * 16; k += 32) {
-              uint32_t o[32];
-              tmem_ld32_issue(to + k, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(to + k, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        const float sub = m_run == -INFINITY ? 0.0f : m_run;
-        const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
-        float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = make_float2(__uint_as_float(s[k][2 * j]), __uint_as_float(s[k][2 * j + 1]));
-            float2 e = __ffma2_rn(x, c2, b2);
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            if (j & 1)
-              l1 = __fadd2_rn(l1, e);
-            else
-              l0 = __fadd2_rn(l0, e);
-            w[j] = pack_pair<BF>(e.x, e.y);
-          }
-          tmem_st16(ts + k * 16, w);
-          if (k == 1) {
-            tmem_wait_st();
-            hand_over(0);
-          }
-        }
-        l_run += (l0.x + l1.x) + (l0.y + l1.y);
-        tmem_wait_st();
-      } else {
-        hand_over(0);
-      }
-      hand_over(1);
-    }
-    if (ok && njobs > 0) ok = __all_sync(~0u, wait(ofull(slot), 0u));
-    if (!wide && nt > 0) {
-      // both slots hold parts of the same queries: slot 1 hands its own over in the key ring
-      // (free: both slots' products have ended)
-      ok = ok && __all_sync(~0u, wait(ofull(0), 0u));
-      float* acc = reinterpret_cast<float*>(gbase + S::K);
-      tc_fence_after();
-      if (slot == 1 && warp_live) {
-        join_ml[row] = make_float2(m_run, l_run);
-        if (ok && jobs1 > 0) {
-#pragma unroll 1
-          for (int k = 0; k < kd * 16; k += 32) {
-            uint32_t o[32];
-            tmem_ld32_issue(to + k, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (k + j < DP) acc[(k + j) * kTaM + row] = __uint_as_float(o[j]);
-          }
-        }
-      }
-      softmax_warps_sync();
-    }
-    tc_fence_after();
-    ok = ok && !*abort;
-    if (ok && warp_live && (wide || slot == 0)) {
-      float f0 = 1.0f, f1 = 0.0f;
-      if (!wide && jobs1 > 0) {
-        const float2 other = join_ml[row];
-        const float M = fmaxf(m_run, other.x), sub = M == -INFINITY ? 0.0f : M;
-        f0 = fast_exp2(m_run - sub);
-        f1 = fast_exp2(other.x - sub);
-        l_run = f0 * l_run + f1 * other.y;
-        m_run = M;
-      }
-      const float inv = p.splits > 1 ? 1.0f : (l_run == 0.0f ? 0.0f : 1.0f / l_run);
-      const bool zero = l_run == 0.0f;
-      const float* acc = reinterpret_cast<const float*>(gbase + S::K);
-      const AtView& vv = p.dvalue;
-      const unsigned char* dv = vv.data + (long long)r * vv.row + (long long)h * vv.head;
-      const long long pr = ((((long long)r * p.kv_heads + h) * p.m + qi) * p.splits) + split;
-      // a tile of output rows: in the key ring, which no product reads any more once slot 0's last
-      // one has ended (all scores were issued before it); joined slots, whose sums lie there, use
-      // the value ring
-      unsigned char* stage = gbase + (wide ? S::K + slot * S::TILE : S::V);
-      if (mine && p.splits > 1) p.part_ml[pr] = make_float2(m_run, l_run);
-#pragma unroll 1
-      for (int k = 0; k < p.dim; k += 32) {
-        uint32_t o[32];
-        __syncwarp();  // the loads are warp-wide
-        if (nt > 0) {
-          tmem_ld32_issue(to + k, o);
-          tmem_wait_ld();
-        }
-        float x[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          x[j] = zero ? 0.0f : __uint_as_float(o[j]) * f0;
-          if (!wide && jobs1 > 0 && f1 != 0.0f && k + j < DP) x[j] = fmaf(f1, acc[(k + j) * kTaM + row], x[j]);
-          x[j] *= inv;
-        }
-        if (*bad_values) {
-          for (int nd = 0; nd < p.nodes; ++nd)
-            if ((sees >> nd) & 1ull)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (k + j < p.dim) {
-                  const float v = load_elem<DT>(dv + nd * vv.pos + (k + j) * 2);
-                  if (!isfinite(v)) x[j] += v;
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          if (p.splits > 1) {
-            if (mine && k + j < p.dim) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + pr * p.dim + k + j);
-              dst[0] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-              dst[1] = make_float4(x[j + 4], x[j + 5], x[j + 6], x[j + 7]);
-            }
-          } else {
-            const int v = (k + j) / 8;
-            if (v < DP / 8)
-              *reinterpret_cast<uint4*>(stage + row * (DP * 2) + ((v ^ (row & 7)) << 4)) =
-                  make_uint4(pack_pair<BF>(x[j], x[j + 1]), pack_pair<BF>(x[j + 2], x[j + 3]),
-                             pack_pair<BF>(x[j + 4], x[j + 5]), pack_pair<BF>(x[j + 6], x[j + 7]));
-          }
-        }
-      }
-      if (p.splits == 1) {  // whole rows at a time, the warp's own 32
-        __syncwarp();
-        const int vecs = p.dim / 8;
-        for (int e = lane; e < 32 * (DP / 8); e += 32) {
-          const int rr = quarter * 32 + e / (DP / 8), v = e % (DP / 8);
-          if (rr < qn && v < vecs)
-            *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + (wide ? slot * kTaM : 0) + rr) + v * 16) =
-                *reinterpret_cast<const uint4*>(stage + rr * (DP * 2) + ((v ^ (rr & 7)) << 4));
-        }
-      }
-    }
-    tc_fence_before();
+  }
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 9) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTaCols);
@@ -570,17 +677,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 template <bool BF, int DP>
-cudaError_t run_tc(const CUtensorMap (&maps)[4], const AttendParams& p, cudaStream_t stream) {
+cudaError_t run_tc(const CUtensorMap (&maps)[5], const AttendParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(attend_tc_kernel<BF, DP>, (int)TcShape<DP>::BYTES, allowed);
   if (e != cudaSuccess) return e;
-  attend_tc_kernel<BF, DP><<<(unsigned)p.items, kTaThreads, TcShape<DP>::BYTES, stream>>>(maps[0], maps[1], maps[2], maps[3], p);
+  const unsigned grid = (unsigned)(p.items < kAtSms ? p.items : kAtSms);
+  attend_tc_kernel<BF, DP><<<grid, kTaThreads, TcShape<DP>::BYTES, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attend_tc(const CUtensorMap (&maps)[4], const AttendParams& p, int dtype, cudaStream_t stream) {
+cudaError_t launch_attend_tc(const CUtensorMap (&maps)[5], const AttendParams& p, int dtype, cudaStream_t stream) {
   if (dtype == DT_BF16) return p.dim <= 64 ? run_tc<true, 64>(maps, p, stream) : run_tc<true, 128>(maps, p, stream);
   return p.dim <= 64 ? run_tc<false, 64>(maps, p, stream) : run_tc<false, 128>(maps, p, stream);
 }

@@ -60,6 +60,7 @@ struct AttendParams {
   int negate;             // attend_tc.cu: scale_log2 is its absolute value, the sign goes into the queries
   // keys shared by all rows or heads (stride 0): their tensor maps have one row or head
   int kv_row_one, kv_head_one;
+  int q_tma;              // attend_tc.cu: the queries' tensor map is there
 };
 
 // Partial results may take this many (query, split) rows of dim + 2 floats: the plan keeps
@@ -102,16 +103,17 @@ inline cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t>&
 
 cudaError_t launch_attend_simt(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_simt_queries(int dtype, int m);  // queries per CTA
-// every stride and address a multiple of 16 bytes, vectors of at most 512 bytes
-cudaError_t launch_attend_step(const AttendParams& p, int dtype, cudaStream_t stream);
-int attend_step_queries(int dtype, int m);  // queries per item
+// f32, every stride and address a multiple of 16 bytes, head size up to kAtStepDim
+constexpr int kAtStepDim = 128;
+cudaError_t launch_attend_step(const AttendParams& p, cudaStream_t stream);
+int attend_step_queries(int m);  // queries per item
 // f16 / bf16, every stride and address a multiple of 16 bytes
 cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_mma_queries(int dim, int m);  // queries per item
 // f16 / bf16, head size up to kAtTcDim, every stride and address a multiple of 16 bytes; maps: key,
-// value, drafted key, drafted value
+// value, drafted key, drafted value, queries
 constexpr int kAtTcDim = 128, kAtTcQueries = 256, kAtTcBox = 64;
-cudaError_t launch_attend_tc(const CUtensorMap (&maps)[4], const AttendParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attend_tc(const CUtensorMap (&maps)[5], const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_attend_join(const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
 
@@ -119,17 +121,20 @@ cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
 bool pointers_reachable(const void* const* ptrs, int n);  // nulls are skipped
 long long wait_limit_ns();
 // LS_BEAM_DEBUG's choice of the attention kernel: 0 = the plan's, else one of these
-constexpr int kAtForceSimt = 1, kAtForceMma = 2, kAtForceTc = 3, kAtForceStep = 4;
+constexpr int kAtForceSimt = 1, kAtForceMma = 2, kAtForceTc = 3;
 struct AttendDebug {
   int kernel, warps, splits;
 };
 AttendDebug attend_debug();
 bool maps_describe(const AttendParams& p);  // encode_keys can succeed
-// Tensor map of a 16-bit tensor [row, head, pos, dim] by byte strides, in boxes of 64 elements by
+// encode_queries: tensor map of the queries [row, key head, token, group, dim] in boxes of 64 elements
+// of `queries` queries in their order; false where one stride per dimension does not describe it.
+// encode_attend: tensor map of a 16-bit tensor [row, head, pos, dim] by byte strides, in boxes of 64 elements by
 // `box` positions (one swizzle row of 128 bytes each); reads past an extent return zeros.
 // The tensor maps of the keys and the values in boxes of `box` keys; false where a map cannot
 // describe them.
 bool encode_keys(CUtensorMap* maps, const AttendParams& p, int dtype, int box);
+bool encode_queries(CUtensorMap* map, const AttendParams& p, int dtype, int queries);
 bool encode_attend(CUtensorMap* map, const AtView& v, int dtype, int dim, int pos, int heads, int rows, int box);
 ls_status report_cuda(cudaError_t e);
 

@@ -70,6 +70,22 @@ __device__ __forceinline__ bool tree_seen(const TreeSeen& t, const int32_t* pare
   return tree_seen_from(t, [&](int i) { return __ldg(parent + i); }, nodes, tid, n, sync);
 }
 
+// The eight 16-bit values of d: infinite and NaN ones become zero; true if there were any.  (An
+// exponent of all ones carries out of its field when one is added to it.)
+template <bool BF>
+__device__ __forceinline__ bool clear_non_finite(uint4& d) {
+  constexpr uint32_t E = BF ? 0x7f807f80u : 0x7c007c00u, U = BF ? 0x00800080u : 0x04000400u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&d);
+  const uint32_t any = ((w[0] & E) + U) | ((w[1] & E) + U) | ((w[2] & E) + U) | ((w[3] & E) + U);
+  if (!(any & 0x80008000u)) return false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((w[i] & E) + U) & 0x80008000u;
+    w[i] &= ~((c & 0x8000u ? 0xffffu : 0u) | (c & 0x80000000u ? 0xffff0000u : 0u));
+  }
+  return true;
+}
+
 // acc + f * x of a part with the sum l: nothing of an empty part, and an infinite or NaN x as
 // it is (f may have underflowed).
 __device__ __forceinline__ float add_part(float acc, float f, float x, float l) {

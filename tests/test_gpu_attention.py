@@ -13,7 +13,7 @@ import serving_ls_beam_gb300 as lsb  # noqa: E402
 
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 KERNELS = [None, "atsimt", "atmma,atwarps=1", "atmma,atwarps=4", "atmma,atwarps=4,atsplits=3",
-           "attc", "attc,atsplits=3", "atstep,atwarps=1", "atstep,atwarps=4,atsplits=3"]
+           "attc", "attc,atsplits=3"]
 
 
 @pytest.fixture(scope="module")
@@ -99,6 +99,69 @@ CROSS = [
 def test_cross(dev, kernel, shape, dtype):
     B, K, T, H, HK, S, D, lens = shape
     check_cross(dev, dtype, B, K, T, H, HK, S, D, lens, seed=S)
+
+
+# more problems than any launch has CTAs, of every kind in turn: no key, one block, one tile and a
+# bit, several; one tile of queries, a tile and a bit, several
+@pytest.mark.parametrize("T,D", [(1, 64), (12, 128), (40, 64), (150, 64), (150, 128), (300, 64)])
+def test_cross_many_problems(dev, kernel, T, D):
+    B, H, S = (120, 8, 300) if T < 100 else (50, 4, 300)
+    g = np.random.default_rng(T + D)
+    dtype = "f16" if T % 4 else "bf16"
+    q = tensor(g, (B, 1, T, H, D), dtype, dev)
+    k, v = tensor(g, (B, H, S, D), dtype, dev), tensor(g, (B, H, S, D), dtype, dev)
+    lens = [[0, 1, 128, 129, 300, 17, 256, 257, 100][b % 9] if b % 5 else int(g.integers(0, S + 1)) for b in range(B)]
+    out = run_cross(q, k, v, lens)
+    pick = sorted({0, T // 2, T - 1, min(T - 1, 127), min(T - 1, 128)})  # a few of the queries, every problem
+    want, bound = ap.cross(f64(q)[:, :, pick], f64(k), f64(v), lens, D ** -0.5, dtype)
+    close(out[:, :, pick], want, bound)
+
+
+@pytest.mark.parametrize("nodes,heads,D", [(1, 8, 64), (10, 8, 128), (33, 8, 64), (64, 16, 128)])
+def test_tree_many_problems(dev, kernel, nodes, heads, D):
+    R, HK, S = 150, 4, 270
+    g = np.random.default_rng(nodes)
+    dtype = "bf16"
+    kinds = ["forest", "chain", "ragged", "empty", "forest"]
+    parent = np.stack([random_parents(g, nodes, kinds[r % 5] if nodes > 1 else "chain") for r in range(R)])
+    q = tensor(g, (R, nodes, heads, D), dtype, dev)
+    ck, cv = tensor(g, (R, HK, S, D), dtype, dev), tensor(g, (R, HK, S, D), dtype, dev)
+    dk, dv = tensor(g, (R, nodes, HK, D), dtype, dev), tensor(g, (R, nodes, HK, D), dtype, dev)
+    for r in range(R):
+        for i in range(nodes):
+            if not ap.branch(parent[r], i):
+                dv[r, i] = float("nan")  # some rows meet values to clear, their neighbours do not
+    lens = [[0, 128, 270, 60, 129][r % 5] if r % 3 else int(g.integers(0, S + 1)) for r in range(R)]
+    out = run_tree(q, ck, cv, lens, dk, dv, parent)
+    pick = sorted({0, nodes // 2, nodes - 1})
+    full_out = f64(out)
+    for r in range(0, R, 2):
+        for i in pick:
+            br = ap.branch(parent[r], i)
+            for h in range(0, heads, 3):
+                kh = h // (heads // HK)
+                if not br:
+                    assert not full_out[r, i, h].any()
+                    continue
+                ks = np.concatenate([f64(ck[r, kh, :lens[r]]), f64(dk[r, br, kh])])
+                vs = np.concatenate([f64(cv[r, kh, :lens[r]]), f64(dv[r, br, kh])])
+                want, bound = ap.one_query(f64(q[r, i, h]), ks, vs, D ** -0.5, dtype)
+                assert (np.abs(full_out[r, i, h] - want) <= bound).all(), (r, i, h)
+
+
+def test_waits_that_run_out_are_reported(dev, monkeypatch):
+    """A wait limit of zero: calls end with the status set (their result is unspecified), and the
+    next call with the ordinary limit is right."""
+    g = np.random.default_rng(4)
+    for T, D in ((1, 64), (200, 64), (200, 128)):
+        q = tensor(g, (2, 1, T, 2, D), "f16", dev)
+        k, v = tensor(g, (2, 2, 500, D), "f16", dev), tensor(g, (2, 2, 500, D), "f16", dev)
+        monkeypatch.setenv("LS_BEAM_DEBUG", "spin=0," + ("attc" if T > 1 else "atmma"))
+        run_cross(q, k, v, [500, 300], status=lsb.LS_ERR_TIMEOUT)
+        monkeypatch.delenv("LS_BEAM_DEBUG")
+        out = run_cross(q, k, v, [500, 300])
+        want, bound = ap.cross(f64(q)[:, :, :2], f64(k), f64(v), [500, 300], D ** -0.5, "f16")
+        close(out[:, :, :2], want, bound)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
