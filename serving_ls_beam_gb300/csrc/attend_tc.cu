@@ -6,20 +6,22 @@
 //
 // with the running maximum and sum of the softmax (Milakov and Gimelshein, 2018).  One CTA per
 // SM takes item after item (up to 256 queries of one problem and one part of its keys), in tiles
-// of 128 keys; twelve warps, one of them idle:
+// of 128 keys; twelve warps:
 //   warp 8     TMA producer: two rings of swizzled key and value tiles (64-element panels of
 //              128-byte rows; a tile's second 64 keys are not fetched when the row ends before)
 //              and the queries, where their layout lets TMA read them in order;
 //   warp 9     owns the 512 tensor-memory columns and issues S = Q K^T (Q and K from shared
-//              memory, M 128, N 128) and O += P V (P from tensor memory, V read as the
-//              transposed operand from the same [key][element] tile).  The whole warp walks the
-//              jobs, so that the compiler sees one path and keeps the operands in uniform
-//              registers; an elected lane issues;
+//              memory, M 128, N 128);
+//   warp 10    issues O += P V (P from tensor memory, V read as the transposed operand from the
+//              same [key][element] tile).  Two warps, because a job's waits, commits and
+//              products take one warp longer to issue than the tensor cores to run.  Each walks
+//              the jobs as a whole, so that the compiler sees one path and keeps the operands in
+//              uniform registers; an elected lane issues;
+//   warp 11    the queries by asynchronous copies where TMA cannot read them;
 //   warps 0-3, 4-7  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
 //              memory), reads its 128 scores, and writes its weights over them as 16-bit
 //              values (rounded to the tensors' type; sums are of the unrounded f32 weights),
-//              handing each half to the products as it is written;
-//   warp 10    the queries by asynchronous copies where TMA cannot read them.
+//              handing each half to the products as it is written.
 // Jobs (a key tile of one slot) alternate between the slots, so that the tensor cores work for
 // one slot while the other's softmax runs.  With more than 128 queries the slots are two tiles of
 // queries over the same key tiles (each fetched once for 256 queries); with fewer they are the
@@ -60,10 +62,11 @@ struct TcShape {
   static constexpr uint32_t TILE = PANELS * kTaPanel;          // 128 vectors of DP elements
   static constexpr uint32_t Q = 0, K = 2 * NQB * TILE, V = K + NST * TILE, BAR = V + NST * TILE;
   static constexpr uint32_t O = NSB * kTaN;                    // tensor-memory column of slot 0's sums
-  // barriers: full / empty of K and V, of the queries, scores, weights x halves, sums x slots, sums read, join, done
+  // barriers: full / empty of K and V and of the queries, scores, score buffer free, weights x
+  // halves, sums x slots, sums read, join, all products issued x 2
   static constexpr int B_KF = 0, B_KE = NST, B_VF = 2 * NST, B_VE = 3 * NST, B_QF = 4 * NST, B_QE = B_QF + NQB,
-                       B_S = B_QE + NQB, B_P = B_S + NSB, B_O = B_P + 2 * NSB, B_OE = B_O + 2, B_J = B_OE + 1,
-                       B_DONE = B_J + 1, NBAR = B_DONE + 1;
+                       B_S = B_QE + NQB, B_SE = B_S + NSB, B_P = B_SE + NSB, B_O = B_P + 2 * NSB, B_OE = B_O + 2, B_J = B_OE + 1,
+                       B_DONE = B_J + 1, NBAR = B_DONE + 2;
   static constexpr uint32_t WORDS = BAR + 8 * NBAR;            // tensor-memory address, abort flag, value flag
   static constexpr uint32_t BYTES = WORDS + 16 + 1024;         // + alignment of the tiles
 };
@@ -109,8 +112,10 @@ struct Waits {
     if (limit <= 0) return give_up();
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
-      if (mbar_test_wait(bar, parity)) return true;
-      if ((n & 255u) == 0) {  // the timer and the flag are slow to read
+      // (a try_wait puts the warp aside for a while; a loop of plain tests would take issue slots
+      // and shared-memory cycles from the softmax warps)
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((n & 15u) == 0) {  // the timer and the flag are slow to read
         if (*abort) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (mine) sees = tree.mask[p.by_group(qi)];
       }
       const bool alive = mine && (!p.nodes || sees != 0);
-      const bool dead_any = __any_sync(~0u, !alive);
+      const bool dead_any = __any_sync(~0u, mine && !alive);  // (lanes without a query may hold anything)
       float m_run = -INFINITY, l_run = 0.0f;
       for (int j = slot; j < x.jobs; j += 2) {
         const int t = x.tile(j), n = x.keys(t, p.nodes), b = (jobs_before + j) % NSB;
@@ -495,6 +500,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr uint32_t ab = BF ? 1u : 0u;  // instruction descriptors of the products
+    constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
+    constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
+    const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
   if (warp == 8) {
     // ---------------------------------------------------------------- producer
     TcWalk w;
@@ -549,89 +558,80 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int g = max(0, qn - NQB); g < qn; ++g) mbar_wait_bounded(bar(S::B_QF + g % NQB), (uint32_t)(g / NQB) & 1u, kTaDrainNs);
     }
   } else if (warp == 9) {
-    // ---------------------------------------------------------------- products
-    constexpr uint32_t ab = BF ? 1u : 0u;
-    constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
-    constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
-    const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
-    const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K), v0 = desc_mn(base + S::V);
+    // ---------------------------------------------------------------- scores
+    const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K);
     bool ok = true;
-    auto scores = [&](const TcWalk& w, int j) {
+    TcWalk w;
+    for (w.begin(p); w.valid && ok; w.next(p)) {
       const TcItem& x = w.x;
-      const int t = w.tile + x.tile(j), st = t % NST, b = (w.job + j) % NSB, qs = w.active % NQB, s = j & 1;
-      if (j == 0 && !(ok = wait_all(S::B_QF + qs, w.active / NQB))) return;
-      if (!(ok = wait_all(S::B_KF + st, t / NST))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t a = q0 + (2 * qs + (x.wide ? s : 0)) * (S::TILE >> 4), bd = k0 + st * (S::TILE >> 4);
-        const uint32_t d = tmem + b * kTaN;
-#pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
-          const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
-          umma_f16(d, a + off, bd + off, id_s, k != 0);
-        }
-        umma_commit(bar(S::B_S + b));
-        if (!x.wide || s == 1) umma_commit(bar(S::B_KE + st));
-        if (j + 1 == x.jobs) umma_commit(bar(S::B_QE + qs));
-      }
-      __syncwarp();
-    };
-    auto values = [&](const TcWalk& w, int j) {
-      const TcItem& x = w.x;
-      const int t = w.tile + x.tile(j), st = t % NST, b = (w.job + j) % NSB, s = j & 1;
-      // the last item's sums are read before the first product of this one replaces them
-      if (j == 0 && w.active > 0 && !(ok = wait_all(S::B_OE, w.active - 1))) return;
-      if (!(ok = wait_all(S::B_VF + st, t / NST))) return;
-      const int steps = (x.keys(x.tile(j), p.nodes) + 15) / 16;
-      const uint64_t bd = v0 + st * (S::TILE >> 4);
-      const uint32_t d = tmem + S::O + s * DP, a = tmem + b * kTaN;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
-        if (!(ok = wait_all(S::B_P + 2 * b + half, (w.job + j) / NSB))) return;
+      const int qs = w.active % NQB;
+      if (!(ok = wait_all(S::B_QF + qs, w.active / NQB))) break;
+      for (int j = 0; j < x.jobs; ++j) {
+        const int g = w.job + j, b = g % NSB, t = w.tile + x.tile(j), st = t % NST, s = j & 1;
+        // the buffer's last weights have been multiplied
+        if (g >= NSB && !(ok = wait_all(S::B_SE + b, g / NSB - 1))) break;
+        if (!(ok = wait_all(S::B_KF + st, t / NST))) break;
         tc_fence_after();
         if (elect_one()) {
-          if (steps >= 4 * half + 4) {
+          const uint64_t a = q0 + (2 * qs + (x.wide ? s : 0)) * (S::TILE >> 4), bd = k0 + st * (S::TILE >> 4);
+          const uint32_t d = tmem + b * kTaN;
 #pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
-          } else {
-            for (int k = 4 * half; k < steps; ++k)
-              umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+          for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
+            const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
+            umma_f16(d, a + off, bd + off, id_s, k != 0);
           }
-          if (half == 1) {
-            if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
-            umma_commit(bar(S::B_O + s));
-          }
+          umma_commit(bar(S::B_S + b));
+          if (!x.wide || s == 1) umma_commit(bar(S::B_KE + st));
+          if (j + 1 == x.jobs) umma_commit(bar(S::B_QE + qs));
         }
         __syncwarp();
       }
-    };
-    TcWalk ws, wv;  // scores run NSB jobs ahead of the values
-    ws.begin(p);
-    wv.begin(p);
-    int js = 0, jv = 0;
-    auto step = [&] {
-      if (ws.valid && ok) {
-        scores(ws, js);
-        if (++js == ws.x.jobs) {
-          js = 0;
-          ws.next(p);
-        }
-      }
-    };
-    for (int i = 0; i < NSB; ++i) step();
-    while (wv.valid && ok) {
-      values(wv, jv);
-      if (++jv == wv.x.jobs) {
-        jv = 0;
-        wv.next(p);
-      }
-      step();
     }
     if (elect_one()) umma_commit(bar(S::B_DONE));
     __syncwarp();
     mbar_wait_bounded(bar(S::B_DONE), 0u, kTaDrainNs);
-  } else if (warp == 10 && !p.q_tma) {
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- values
+    const uint64_t v0 = desc_mn(base + S::V);
+    bool ok = true;
+    TcWalk w;
+    for (w.begin(p); w.valid && ok; w.next(p)) {
+      const TcItem& x = w.x;
+      // the last item's sums are read before the first product of this one replaces them
+      if (w.active > 0 && !(ok = wait_all(S::B_OE, w.active - 1))) break;
+      for (int j = 0; j < x.jobs && ok; ++j) {
+        const int g = w.job + j, b = g % NSB, t = w.tile + x.tile(j), st = t % NST, s = j & 1;
+        if (!(ok = wait_all(S::B_VF + st, t / NST))) break;
+        const int steps = (x.keys(x.tile(j), p.nodes) + 15) / 16;
+        const uint64_t bd = v0 + st * (S::TILE >> 4);
+        const uint32_t d = tmem + S::O + s * DP, a = tmem + b * kTaN;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
+          if (!(ok = wait_all(S::B_P + 2 * b + half, g / NSB))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (steps >= 4 * half + 4) {
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+            } else {
+              for (int k = 4 * half; k < steps; ++k)
+                umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+            }
+            if (half == 1) {
+              umma_commit(bar(S::B_SE + b));
+              umma_commit(bar(S::B_O + s));
+              if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (elect_one()) umma_commit(bar(S::B_DONE + 1));
+    __syncwarp();
+    mbar_wait_bounded(bar(S::B_DONE + 1), 0u, kTaDrainNs);
+  } else if (!p.q_tma) {
     // ---------------------------------------------------------------- queries
     TcWalk w;
     w.begin(p);
