@@ -6,12 +6,12 @@
 //
 // with the running maximum and sum of the softmax (Milakov and Gimelshein, 2018).  One CTA per
 // SM takes item after item (up to 256 queries of one problem and one part of its keys), in tiles
-// of 128 keys; twelve warps:
+// of 128 keys (64 for head sizes above 64); twelve warps:
 //   warp 8     TMA producer: two rings of swizzled key and value tiles (64-element panels of
 //              128-byte rows; a tile's second 64 keys are not fetched when the row ends before)
 //              and the queries, where their layout lets TMA read them in order;
 //   warp 9     owns the 512 tensor-memory columns and issues S = Q K^T (Q and K from shared
-//              memory, M 128, N 128);
+//              memory, M 128, N the tile's keys);
 //   warp 10    issues O += P V (P from tensor memory, V read as the transposed operand from the
 //              same [key][element] tile).  Two warps, because a job's waits, commits and
 //              products take one warp longer to issue than the tensor cores to run.  Each walks
@@ -19,16 +19,15 @@
 //              uniform registers; an elected lane issues;
 //   warp 11    the queries by asynchronous copies where TMA cannot read them;
 //   warps 0-3, 4-7  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
-//              memory), reads its 128 scores, and writes its weights over them as 16-bit
+//              memory), reads its scores of the tile, and writes its weights over them as 16-bit
 //              values (rounded to the tensors' type; sums are of the unrounded f32 weights),
-//              handing each half to the products as it is written.
+//              handing 64 keys at a time to the products.
 // Jobs (a key tile of one slot) alternate between the slots, so that the tensor cores work for
 // one slot while the other's softmax runs.  With more than 128 queries the slots are two tiles of
 // queries over the same key tiles (each fetched once for 256 queries); with fewer they are the
 // even and the odd key tiles of the same queries, joined at the end: both warpgroups read both
-// accumulators and each writes half of the columns.  The score buffers (two for head sizes above
-// 64, three otherwise, what 512 columns hold) let scores run ahead of the values, also into the
-// next item.
+// accumulators and each writes half of the columns.  Three or four score buffers let scores run
+// ahead of the values, also into the next item.
 //
 // The accumulator is rescaled only when a query's maximum has grown by more than 2^8 since the
 // last time: until then its weights are at most 2^8 instead of 1, which f32 sums and the 16-bit
@@ -47,8 +46,7 @@ namespace {
 
 constexpr int kTaThreads = 384;
 constexpr int kTaM = 128;   // queries of a slot
-constexpr int kTaN = 128;   // keys of a tile
-constexpr uint32_t kTaPanel = 128 * 128;  // 128 rows of 64 16-bit elements
+constexpr uint32_t kTaPanel = 128 * 128;  // a panel of queries: 128 rows of 64 16-bit elements
 constexpr uint32_t kTaCols = 512;
 constexpr long long kTaDrainNs = 2000000000LL;
 constexpr float kTaLazy = 8.0f;           // growth of the maximum (log2) that is let pass
@@ -56,12 +54,18 @@ constexpr float kTaLazy = 8.0f;           // growth of the maximum (log2) that i
 template <int DP>
 struct TcShape {
   static constexpr int PANELS = DP / 64;
-  static constexpr int NST = DP == 64 ? 4 : 2;                 // stages of either ring
-  static constexpr int NSB = DP == 64 ? 3 : 2;                 // score buffers
+  // Keys of a tile.  512 columns of tensor memory hold the sums of both slots and the score
+  // buffers: at 128 elements and 128 keys only two, and each job would wait for the products of
+  // the job before; at 64 keys four (measured below).
+  static constexpr int N = DP == 64 ? 128 : 64;
+  static constexpr int NSB = DP == 64 ? 3 : 4;                 // score buffers
+  static constexpr int HALVES = N / 64;                        // weights are handed over 64 keys at a time
+  static constexpr int NST = 4;                                // stages of either ring
   static constexpr int NQB = DP == 64 ? 2 : 1;                 // pairs of query tiles
-  static constexpr uint32_t TILE = PANELS * kTaPanel;          // 128 vectors of DP elements
-  static constexpr uint32_t Q = 0, K = 2 * NQB * TILE, V = K + NST * TILE, BAR = V + NST * TILE;
-  static constexpr uint32_t O = NSB * kTaN;                    // tensor-memory column of slot 0's sums
+  static constexpr uint32_t QT = PANELS * kTaPanel;            // 128 queries of DP elements
+  static constexpr uint32_t PANEL = N * 128, TILE = PANELS * PANEL;  // N keys or values
+  static constexpr uint32_t Q = 0, K = 2 * NQB * QT, V = K + NST * TILE, BAR = V + NST * TILE;
+  static constexpr uint32_t O = NSB * N;                       // tensor-memory column of slot 0's sums
   // barriers: full / empty of K and V and of the queries, scores, score buffer free, weights x
   // halves, sums x slots, sums read, join, all products issued x 2
   static constexpr int B_KF = 0, B_KE = NST, B_VF = 2 * NST, B_VE = 3 * NST, B_QF = 4 * NST, B_QE = B_QF + NQB,
@@ -79,8 +83,8 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
 }
 // MN-major (V as the operand whose rows are head elements): atoms of 64 elements by 8 keys; a
 // panel further for the next 64 elements, 1024 bytes for the next 8 keys.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(kTaPanel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t panel) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
@@ -132,16 +136,18 @@ struct Waits {
 
 // One item: the queries i0 .. i0 + nq of problem (r, h) and tiles t_lo .. t_lo + nt of its keys
 // (tile nb: the drafted tokens), in `jobs` jobs: job j belongs to slot j & 1.
+template <int N>
 struct TcItem {
   int r, h, i0, nq, split, len, nb, t_lo, nt, jobs;
   bool wide;  // two tiles of queries; otherwise the slots share one
   __device__ __forceinline__ int tile(int j) const { return wide ? j >> 1 : j; }
   __device__ __forceinline__ bool draft(int t) const { return t_lo + t >= nb; }
-  __device__ __forceinline__ int keys(int t, int nodes) const { return draft(t) ? nodes : min(kTaN, len - (t_lo + t) * kTaN); }
+  __device__ __forceinline__ int keys(int t, int nodes) const { return draft(t) ? nodes : min(N, len - (t_lo + t) * N); }
 };
 __device__ __forceinline__ int tc_row(const AttendParams& p, int it) { return p.by_head(p.by_tile(p.by_split(it))); }
-__device__ __forceinline__ TcItem tc_item(const AttendParams& p, int it, int len) {
-  TcItem x;
+template <int N>
+__device__ __forceinline__ TcItem<N> tc_item(const AttendParams& p, int it, int len) {
+  TcItem<N> x;
   const int a = p.by_split(it), b = p.by_tile(a);
   x.split = it - a * p.splits;
   x.i0 = (a - b * p.m_tiles) * (2 * kTaM);
@@ -150,7 +156,7 @@ __device__ __forceinline__ TcItem tc_item(const AttendParams& p, int it, int len
   x.nq = min(2 * kTaM, p.m - x.i0);
   x.wide = x.nq > kTaM;
   x.len = min(max(len, 0), p.max_len);
-  x.nb = (x.len + kTaN - 1) / kTaN;
+  x.nb = (x.len + N - 1) / N;
   const int nbt = x.nb + (p.nodes ? 1 : 0), per = p.splits == 1 ? nbt : (nbt + p.splits - 1) / p.splits;
   x.t_lo = min(x.split * per, nbt);
   x.nt = min(per, nbt - x.t_lo);
@@ -159,11 +165,12 @@ __device__ __forceinline__ TcItem tc_item(const AttendParams& p, int it, int len
 }
 
 // A walk over this CTA's items that have tiles: the next length is loaded while an item is worked on.
+template <int N>
 struct TcWalk {
   int it, next_len;
   int active;   // items with tiles before this one
   int job, tile;  // jobs and tiles before this item's
-  TcItem x;
+  TcItem<N> x;
   bool valid;
   __device__ __forceinline__ void load(const AttendParams& p, int i) {
     // the shuffle tells the compiler that the value is one for the warp
@@ -171,7 +178,7 @@ struct TcWalk {
   }
   __device__ __forceinline__ void find(const AttendParams& p) {
     for (; it < (int)p.items; it += gridDim.x) {
-      x = tc_item(p, it, next_len);
+      x = tc_item<N>(p, it, next_len);
       load(p, it + gridDim.x);
       if (x.nt > 0) {
         valid = true;
@@ -201,10 +208,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                      const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
                      const __grid_constant__ CUtensorMap map_q, const AttendParams p) {
   using S = TcShape<DP>;
-  constexpr int NST = S::NST, NSB = S::NSB, NQB = S::NQB, DT = BF ? DT_BF16 : DT_F16;
+  constexpr int NST = S::NST, NSB = S::NSB, NQB = S::NQB, N = S::N, DT = BF ? DT_BF16 : DT_F16;
   extern __shared__ unsigned char ta_raw[];
   __shared__ unsigned long long trees[8][kAtMaxNodes * 12 / 8];
   __shared__ float2 join_ml[2][2][kTaM];
+  __shared__ uint4 stage[8][32 * 4];
   const uint32_t raw = smem_addr(ta_raw), base = (raw + 1023u) & ~1023u;
   unsigned char* gbase = ta_raw + (base - raw);
   auto bar = [&](int i) { return base + S::BAR + 8u * (uint32_t)i; };
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     int turn = 1;
     for (int it = blockIdx.x; it < (int)p.items && ok; it += gridDim.x) {
       turn ^= 1;
-      const TcItem x = tc_item(p, it, next_len);
+      const TcItem<S::N> x = tc_item<S::N>(p, it, next_len);
       if (x.len != next_len && tid == 0) atomicOr(p.status, kDevInternal);
       if (it + gridDim.x < p.items) next_len = __ldg(p.len + tc_row(p, it + gridDim.x));
       const int qn = x.wide ? min(kTaM, x.nq - slot * kTaM) : x.nq;  // queries of the slot
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       float m_run = -INFINITY, l_run = 0.0f;
       for (int j = slot; j < x.jobs; j += 2) {
         const int t = x.tile(j), n = x.keys(t, p.nodes), b = (jobs_before + j) % NSB;
-        const uint32_t ts = lanes + b * kTaN;
+        const uint32_t ts = lanes + b * N;
         const bool draft = x.draft(t);
         // the weights of half a tile (and the fixed-up values) are there for the products
         auto hand_over = [&](int half) {
@@ -293,12 +301,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const int fill = (16 - (n & 15)) & 15;
           for (int e = wg; e < fill * (DP / 8); e += 128) {
             const int key = n + e / (DP / 8), xx = e % (DP / 8);
-            *reinterpret_cast<uint4*>(v + (xx >> 3) * kTaPanel + key * 128 + (xx & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(v + (xx >> 3) * S::PANEL + key * 128 + (xx & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           if (draft && p.nodes > 1) {
             for (int e = wg; e < n * (DP / 8); e += 128) {
               const int key = e / (DP / 8), xx = e % (DP / 8);
-              uint4* at = reinterpret_cast<uint4*>(v + (xx >> 3) * kTaPanel + key * 128 + (xx & 7) * 16);
+              uint4* at = reinterpret_cast<uint4*>(v + (xx >> 3) * S::PANEL + key * 128 + (xx & 7) * 16);
               uint4 d = *at;
               if (clear_non_finite<BF>(d)) {
                 *at = d;
@@ -310,15 +318,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         __syncwarp();
         if (warp_live) {
-          uint32_t s[4][32];
+          uint32_t s[N / 32][32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
+          for (int k = 0; k < N / 32; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
           tmem_wait_ld(s[0]);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) tmem_after_wait(s[k]);
-          if (n < kTaN || dead_any || draft) {
+          for (int k = 1; k < N / 32; ++k) tmem_after_wait(s[k]);
+          if (n < N || dead_any || draft) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < N / 32; ++k) {
               unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
               if (!alive) see = 0u;
               const int left = n - 32 * k;
@@ -327,9 +335,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               for (int i = 0; i < 32; ++i) s[k][i] = (see >> i) & 1u ? s[k][i] : 0xff800000u;
             }
           }
-          float m4[4];
+          float m4[N / 32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < N / 32; ++k) {
             float a = max3(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]), __uint_as_float(s[k][2]));
             float bb = max3(__uint_as_float(s[k][3]), __uint_as_float(s[k][4]), __uint_as_float(s[k][5]));
 #pragma unroll
@@ -339,7 +347,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
             m4[k] = max3(a, bb, fmaxf(__uint_as_float(s[k][30]), __uint_as_float(s[k][31])));
           }
-          const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+          float mn = fmaxf(m4[0], m4[1]);
+          if constexpr (N == 128) mn = fmaxf(mn, fmaxf(m4[2], m4[3]));
+          mn *= c;
           const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
           if (__any_sync(~0u, grow)) {
             const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
           float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < N / 32; ++k) {
             uint32_t wt[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -382,20 +392,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               wt[i] = pack_pair<BF>(e.x, e.y);
             }
             tmem_st16(ts + k * 16, wt);
-            if (k == 1) {
+            if (S::HALVES == 2 && k == 1) {
               tmem_wait_st();
               hand_over(0);
             }
           }
           l_run += (l0.x + l1.x) + (l0.y + l1.y);
           tmem_wait_st();
-        } else {
+        } else if (S::HALVES == 2) {
           hand_over(0);
         }
         // A parity tells neighbouring phases apart, no more: the slot's last product is waited for
         // before the weights that let the next one complete (it has ended by now, as a rule).
         if (j >= 2 && !(ok = wait_all(S::B_O + slot, sums[slot] + (j >> 1) - 1))) break;
-        hand_over(1);
+        hand_over(S::HALVES - 1);
       }
       // the slot's sums (when the slots share the queries, both slots')
       if (ok && x.jobs > slot) {
@@ -434,7 +444,24 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const bool rare = has_bad || __any_sync(~0u, zero);
         const unsigned char* dv = p.dvalue.data + (long long)x.r * p.dvalue.row + (long long)x.h * p.dvalue.head;
         const long long pr = (((long long)x.r * p.kv_heads + x.h) * p.m + qi) * p.splits + x.split;
-        unsigned char* out = p.out.data + (mine ? query_offset(p, p.out, x.r, x.h, qi) : 0);
+        // where this lane's row goes; rows leave through shared memory, 64 bytes of a row by four lanes
+        // (a lane storing its own row would touch 32 lines per instruction)
+        const long long at = p.splits > 1 ? pr * p.dim * 4 : (mine ? query_offset(p, p.out, x.r, x.h, qi) : 0);
+        unsigned char* to_all = p.splits > 1 ? reinterpret_cast<unsigned char*>(p.part_o) : p.out.data;
+        uint4* mystage = stage[warp];
+        auto store_rows = [&](const uint4 (&v)[4], int byte0, int bytes) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mystage[lane * 4 + (i ^ ((lane >> 1) & 3))] = v[i];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + (lane >> 2), ch = lane & 3;
+            const long long off = __shfl_sync(~0u, at, rr);
+            if (quarter * 32 + rr < qn && byte0 + ch * 16 < bytes)
+              *reinterpret_cast<uint4*>(to_all + off + byte0 + ch * 16) = mystage[rr * 4 + (ch ^ ((rr >> 1) & 3))];
+          }
+        };
         if (mine && p.splits > 1 && (!joined || slot == 0)) p.part_ml[pr] = make_float2(m_run, l_run);
 #pragma unroll 1
         for (int k = joined ? 32 * slot : 0; k < p.dim; k += joined ? 64 : 32) {
@@ -472,19 +499,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                       if (!isfinite(v)) y[i] += v;
                     }
           }
+          if (p.splits > 1) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (mine && k + i < p.dim) {
-              if (p.splits > 1) {
-                float4* dst = reinterpret_cast<float4*>(p.part_o + pr * p.dim + k + i);
-                dst[0] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                dst[1] = make_float4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
-              } else {
-                *reinterpret_cast<uint4*>(out + (k + i) * 2) =
-                    make_uint4(pack_pair<BF>(y[i], y[i + 1]), pack_pair<BF>(y[i + 2], y[i + 3]),
-                               pack_pair<BF>(y[i + 4], y[i + 5]), pack_pair<BF>(y[i + 6], y[i + 7]));
-              }
+            for (int hf = 0; hf < 2; ++hf) {
+              uint4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[i] = make_uint4(__float_as_uint(y[hf * 16 + 4 * i]), __float_as_uint(y[hf * 16 + 4 * i + 1]),
+                                  __float_as_uint(y[hf * 16 + 4 * i + 2]), __float_as_uint(y[hf * 16 + 4 * i + 3]));
+              store_rows(v, (k + hf * 16) * 4, p.dim * 4);
             }
+          } else {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = make_uint4(pack_pair<BF>(y[8 * i], y[8 * i + 1]), pack_pair<BF>(y[8 * i + 2], y[8 * i + 3]),
+                                pack_pair<BF>(y[8 * i + 4], y[8 * i + 5]), pack_pair<BF>(y[8 * i + 6], y[8 * i + 7]));
+            store_rows(v, k * 2, p.dim * 2);
           }
         }
       }
@@ -502,30 +533,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr uint32_t ab = BF ? 1u : 0u;  // instruction descriptors of the products
     constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
-    constexpr uint32_t id_s = id0 | ((uint32_t)(kTaN >> 3) << 17);
+    constexpr uint32_t id_s = id0 | ((uint32_t)(S::N >> 3) << 17);
     const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
   if (warp == 8) {
     // ---------------------------------------------------------------- producer
-    TcWalk w;
+    TcWalk<S::N> w;
     w.begin(p);
     bool ok = true;
     int kn = 0, vn = 0, qn = 0;  // tiles and query sets asked for
     for (; w.valid && ok; w.next(p)) {
-      const TcItem& x = w.x;
+      const TcItem<S::N>& x = w.x;
       auto load = [&](int t, uint32_t ring, int full, int empty, const CUtensorMap* map, const CUtensorMap* dmap, int* count) {
         const int g = w.tile + t, st = g % NST;
         if (g >= NST && !(ok = wait_all(empty + st, g / NST - 1))) return;
         if (elect_one()) {
           const bool draft = x.draft(t);
-          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : 2;
-          mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (kTaPanel / 2));
+          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : S::HALVES;
+          mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (64 * 128));
           for (int c = 0; c < S::PANELS; ++c)
             for (int hf = 0; hf < halves; ++hf) {
-              const uint32_t dst = base + ring + st * S::TILE + c * kTaPanel + hf * (kTaPanel / 2);
+              const uint32_t dst = base + ring + st * S::TILE + c * S::PANEL + hf * (64 * 128);
               if (draft)
                 tma_load_4d(dst, dmap, c * 64, 0, x.h, x.r, bar(full + st));
               else
-                tma_load_4d(dst, map, c * 64, (x.t_lo + t) * kTaN + hf * 64, p.kv_head_one ? 0 : x.h,
+                tma_load_4d(dst, map, c * 64, (x.t_lo + t) * N + hf * 64, p.kv_head_one ? 0 : x.h,
                             p.kv_row_one ? 0 : x.r, bar(full + st));
             }
         }
@@ -538,10 +569,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (g >= NQB) ok = wait_all(S::B_QE + st, g / NQB - 1);
         if (ok && elect_one()) {
           const int slots = x.wide ? 2 : 1, token = p.by_group(x.i0);
-          mbar_arrive_expect_tx(bar(S::B_QF + st), (uint32_t)slots * S::TILE);
+          mbar_arrive_expect_tx(bar(S::B_QF + st), (uint32_t)slots * S::QT);
           for (int s = 0; s < slots; ++s)
             for (int c = 0; c < S::PANELS; ++c)
-              tma_load_5d(base + S::Q + (2 * st + s) * S::TILE + c * kTaPanel, &map_q, c * 64, 0, token + s * p.by_group(kTaM),
+              tma_load_5d(base + S::Q + (2 * st + s) * S::QT + c * kTaPanel, &map_q, c * 64, 0, token + s * p.by_group(kTaM),
                           x.h, x.r, bar(S::B_QF + st));
         }
         __syncwarp();
@@ -561,9 +592,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // ---------------------------------------------------------------- scores
     const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K);
     bool ok = true;
-    TcWalk w;
+    TcWalk<S::N> w;
     for (w.begin(p); w.valid && ok; w.next(p)) {
-      const TcItem& x = w.x;
+      const TcItem<S::N>& x = w.x;
       const int qs = w.active % NQB;
       if (!(ok = wait_all(S::B_QF + qs, w.active / NQB))) break;
       for (int j = 0; j < x.jobs; ++j) {
@@ -573,12 +604,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (!(ok = wait_all(S::B_KF + st, t / NST))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t a = q0 + (2 * qs + (x.wide ? s : 0)) * (S::TILE >> 4), bd = k0 + st * (S::TILE >> 4);
-          const uint32_t d = tmem + b * kTaN;
+          const uint64_t a = q0 + (2 * qs + (x.wide ? s : 0)) * (S::QT >> 4), bd = k0 + st * (S::TILE >> 4);
+          const uint32_t d = tmem + b * N;
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {  // elements past the head size are zero
-            const uint32_t off = (uint32_t)(k >> 2) * (kTaPanel >> 4) + 2u * (k & 3);
-            umma_f16(d, a + off, bd + off, id_s, k != 0);
+            const uint32_t in = 2u * (k & 3);
+            umma_f16(d, a + (k >> 2) * (kTaPanel >> 4) + in, bd + (k >> 2) * (S::PANEL >> 4) + in, id_s, k != 0);
           }
           umma_commit(bar(S::B_S + b));
           if (!x.wide || s == 1) umma_commit(bar(S::B_KE + st));
@@ -592,11 +623,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     mbar_wait_bounded(bar(S::B_DONE), 0u, kTaDrainNs);
   } else if (warp == 10) {
     // ---------------------------------------------------------------- values
-    const uint64_t v0 = desc_mn(base + S::V);
+    const uint64_t v0 = desc_mn(base + S::V, S::PANEL);
     bool ok = true;
-    TcWalk w;
+    TcWalk<S::N> w;
     for (w.begin(p); w.valid && ok; w.next(p)) {
-      const TcItem& x = w.x;
+      const TcItem<S::N>& x = w.x;
       // the last item's sums are read before the first product of this one replaces them
       if (w.active > 0 && !(ok = wait_all(S::B_OE, w.active - 1))) break;
       for (int j = 0; j < x.jobs && ok; ++j) {
@@ -604,9 +635,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (!(ok = wait_all(S::B_VF + st, t / NST))) break;
         const int steps = (x.keys(x.tile(j), p.nodes) + 15) / 16;
         const uint64_t bd = v0 + st * (S::TILE >> 4);
-        const uint32_t d = tmem + S::O + s * DP, a = tmem + b * kTaN;
+        const uint32_t d = tmem + S::O + s * DP, a = tmem + b * N;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // the weights of 64 keys at a time, as they are written
+        for (int half = 0; half < S::HALVES; ++half) {  // the weights of 64 keys at a time, as they are written
           if (!(ok = wait_all(S::B_P + 2 * b + half, g / NSB))) break;
           tc_fence_after();
           if (elect_one()) {
@@ -618,7 +649,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               for (int k = 4 * half; k < steps; ++k)
                 umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
             }
-            if (half == 1) {
+            if (half + 1 == S::HALVES) {
               umma_commit(bar(S::B_SE + b));
               umma_commit(bar(S::B_O + s));
               if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
@@ -633,17 +664,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     mbar_wait_bounded(bar(S::B_DONE + 1), 0u, kTaDrainNs);
   } else if (!p.q_tma) {
     // ---------------------------------------------------------------- queries
-    TcWalk w;
+    TcWalk<S::N> w;
     w.begin(p);
     bool ok = true;
     for (; w.valid && ok; w.next(p)) {
-      const TcItem& x = w.x;
+      const TcItem<S::N>& x = w.x;
       const int st = w.active % NQB;
       if (w.active >= NQB && !(ok = wait_all(S::B_QE + st, w.active / NQB - 1))) break;
       const int rows = x.wide ? 2 * kTaM : kTaM;
       auto place = [&](int e) {
         const int qr = e / (DP / 8), ch = e % (DP / 8);
-        return S::Q + (2 * st + (qr >> 7)) * S::TILE + (ch >> 3) * kTaPanel + (qr & 127) * 128 + (((ch & 7) ^ (qr & 7)) << 4);
+        return S::Q + (2 * st + (qr >> 7)) * S::QT + (ch >> 3) * kTaPanel + (qr & 127) * 128 + (((ch & 7) ^ (qr & 7)) << 4);
       };
       for (int r0 = 0; r0 < rows; r0 += 32) {  // each lane knows one row's address
         const long long mine = r0 + lane < x.nq ? query_offset(p, p.q, x.r, x.h, x.i0 + r0 + lane) : 0;
