@@ -68,12 +68,40 @@ bool encode_maps(CUtensorMap (&maps)[5], AttendParams& p, int dtype) {
   maps[2] = maps[0];
   maps[3] = maps[1];
   maps[4] = maps[0];
-  p.q_tma = !p.negate && encode_queries(&maps[4], p, dtype, kAtTcQueries / 2);
+  p.q_tma = !p.negate && encode_queries(&maps[4], p, dtype, kAtTcSlot);
   if (!p.nodes) return true;
   for (const AtView& v : {p.dkey, p.dvalue})
     if ((p.rows > 1 && v.row == 0) || (p.kv_heads > 1 && v.head == 0) || (p.nodes > 1 && v.pos == 0)) return false;
   return encode_attend(&maps[2], p.dkey, dtype, p.dim, p.nodes, p.kv_heads, p.rows, kAtTcBox) &&
          encode_attend(&maps[3], p.dvalue, dtype, p.dim, p.nodes, p.kv_heads, p.rows, kAtTcBox);
+}
+
+// Whether the tcgen05 kernel takes a 16-bit call, from the times of both kernels over queries per
+// key head (1 to 64), row lengths (128 to 6000) and problems (32 to 1500); times in us, warp-level
+// kernel / tcgen05, bf16:
+//   head 128, 32 queries, 1500 problems: 128 keys 81 / 60, 512 keys 151 / 79
+//   head 128, 16 queries, 1500 problems: 256 keys 61 / 64, 512 keys 91 / 77
+//   head 128, 8 queries, 256 problems: 1024 keys 28 / 29, 6000 keys 113 / 104
+//   head 64, 32 queries, 1500 problems: 256 keys 54 / 67, 512 keys 87 / 76
+//   head 64, 40 queries, 3200 problems: 100 keys 95 / 134
+//   head 64, 16 queries: 256 problems, 1024 keys 26 / 24; 1500 problems, 1024 keys 69 / 90
+//   head 64, 8 queries, 256 problems: 6000 keys 60 / 65
+bool tcgen05_pays(const AttendParams& p, long long problems) {
+  const long long keys = (long long)p.max_len + p.nodes;
+  if (p.m <= 8) return false;
+  if (p.dim > 64) return p.m > 16 || keys > 256;
+  if (p.m <= 16) return keys >= 1024 && problems <= 4 * kAtSms;
+  return keys * ((p.m + 31) / 32) > 320;
+}
+
+// Whether a warp takes whole rows in the kernels that stream keys per warp (the other way is four
+// warps to a row or a part of it): many rows, each of a few of a warp's blocks.  In us, one warp /
+// four: 1500 rows of head 64 and 4 queries, 128 keys 15 / 20, 256 20 / 25, 512 32 / 34; of head 128,
+// 128 keys 21 / 28, 256 33 / 36; 256 rows of head 64, 512 keys 18 / 14; f32, 4096 rows of head 64,
+// 128 keys 56 / 67, 512 of head 128 and 2000 keys 363 / 57.
+bool warp_takes_rows(const AttendParams& p, long long items) {
+  const int bytes = (p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256);
+  return items >= 6 * kAtSms && ((long long)p.max_len + p.nodes) * bytes <= 20000;
 }
 
 ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
@@ -95,21 +123,21 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.negate = p.scale_log2 < 0.0f;
   CUtensorMap maps[5];
   const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
-                  (dbg.kernel ? dbg.kernel == kAtForceTc : p.m > 32) && encode_maps(maps, p, dtype);
+                  (dbg.kernel ? dbg.kernel == kAtForceTc : tcgen05_pays(p, base)) && encode_maps(maps, p, dtype);
   const bool step = lines && dtype == LS_DTYPE_F32 && p.dim <= kAtStepDim && dbg.kernel != kAtForceSimt;
   const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt && maps_describe(p);
-  const int mq = tc     ? kAtTcQueries
-                 : step ? attend_step_queries(p.m)
-                 : mma  ? attend_mma_queries(p.dim, p.m)
-                        : attend_simt_queries(dtype, p.m);
-  p.m_tiles = (p.m + mq - 1) / mq;
+  p.m_step = tc     ? 2 * kAtTcSlot
+             : step ? attend_step_queries(p.m)
+             : mma  ? attend_mma_queries(p.dim, p.m)
+                    : attend_simt_queries(dtype, p.m);
+  p.m_tiles = (p.m + p.m_step - 1) / p.m_step;
   const long long whole = base * p.m_tiles;
   if (tc) {
     // a scale of 0 as 2^-100: masked scores stay -inf, and every weight still is exactly 1
     p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
   } else if (mma || step) {
-    p.warps = dbg.warps ? dbg.warps : (whole >= 4 * 2 * kAtSms && p.max_len <= 256 ? 1 : 4);
+    p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole) ? 1 : 4;
     p.splits = p.warps == 1 ? 1 : split_of(p, whole, (mma ? 2 : 4) * kAtSms, mma ? 256 : 128, dbg.splits);
   } else {
     p.splits = split_of(p, whole, 4 * kAtSms, 128, dbg.splits);

@@ -150,10 +150,10 @@ __device__ __forceinline__ TcItem<N> tc_item(const AttendParams& p, int it, int 
   TcItem<N> x;
   const int a = p.by_split(it), b = p.by_tile(a);
   x.split = it - a * p.splits;
-  x.i0 = (a - b * p.m_tiles) * (2 * kTaM);
+  x.i0 = (a - b * p.m_tiles) * p.m_step;
   x.r = p.by_head(b);
   x.h = b - x.r * p.kv_heads;
-  x.nq = min(2 * kTaM, p.m - x.i0);
+  x.nq = min(p.m_step, p.m - x.i0);
   x.wide = x.nq > kTaM;
   x.len = min(max(len, 0), p.max_len);
   x.nb = (x.len + N - 1) / N;

@@ -48,7 +48,8 @@ struct AttendParams {
   int rows, beams, q_len, kv_heads, group, dim, max_len, nodes;
   int tokens;             // beams * q_len
   int m;                  // tokens * group
-  int m_tiles;            // ceil(m / queries per CTA or warp)
+  int m_step;             // queries per item
+  int m_tiles;            // ceil(m / m_step)
   int warps;              // attend_step.cu, attend_mma.cu: warps per item (1 or 4)
   int splits;             // parts of a row's keys (each a CTA's); > 1: partial results
   float* part_o;          // [problem, m, split, dim] f32
@@ -112,7 +113,7 @@ cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t str
 int attend_mma_queries(int dim, int m);  // queries per item
 // f16 / bf16, head size up to kAtTcDim, every stride and address a multiple of 16 bytes; maps: key,
 // value, drafted key, drafted value, queries
-constexpr int kAtTcDim = 128, kAtTcQueries = 256, kAtTcBox = 64;
+constexpr int kAtTcDim = 128, kAtTcSlot = 128, kAtTcBox = 64;  // an item has one or two slots of queries
 cudaError_t launch_attend_tc(const CUtensorMap (&maps)[5], const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_attend_join(const AttendParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream);
