@@ -298,7 +298,7 @@ ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cach
                         move ? cache_value : nullptr, move ? draft_key->data : nullptr, move ? draft_value->data : nullptr};
   if (!pointers_reachable(ptrs, 15)) return LS_ERR_INVALID_ARG;
   const long long head_bytes = (long long)head_dim * es;
-  if (move && (layers > 65535 || (long long)nodes * heads * head_dim > INT_MAX)) return LS_ERR_UNSUPPORTED;
+  if (move && (layers > 65535 || 2ll * nodes * heads * head_dim > 1ll << 30)) return LS_ERR_UNSUPPORTED;
   CommitParams p{};
   if (move) {
     p.cache_key = static_cast<unsigned char*>(cache_key);
@@ -313,6 +313,8 @@ ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cach
                                     p.dvalue.head | p.dvalue_layer | head_bytes);
     p.unit = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
     p.vec_units = (int)(head_bytes / p.unit);
+    p.by_units.set(p.vec_units);
+    p.by_per.set(heads * p.vec_units);
   }
   p.cache_len = cache_len;
   p.parent = parent;

@@ -87,6 +87,7 @@ struct CommitParams {
   int layers, rows, nodes, heads, max_len, eos;
   int vec_units;            // copy units per head vector
   int unit;                 // bytes of a copy unit
+  AtDivisor by_per, by_units;  // by heads * vec_units, by vec_units
 };
 
 // Raises a kernel's dynamic shared-memory limit once per device (`done`: a bit per device).

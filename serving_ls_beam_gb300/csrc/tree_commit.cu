@@ -7,29 +7,49 @@
 // candidates in ascending order, taking each whose parent is the branch's last node so far,
 // walks the branch and takes the first of equal siblings.
 //
-// A CTA has one layer of one row.  Each repeats the walk (a few hundred bytes from L2, a loop
-// over the candidates only), which costs less than a launch for it, and copies its layer's
-// accepted keys and values, 16 bytes per thread where the layout allows.  Nothing of the
-// rejected nodes is read or written.
+// A CTA has one layer of one row, or a part of it where the trees are large and the rows few
+// (branches of very different lengths: the longest would otherwise set the time).  Each repeats
+// the walk (a few hundred bytes from L2, a loop over the candidates only), which costs less than
+// a launch for it, and copies its share of the accepted keys and values, 16 bytes per thread where
+// the layout allows, eight copies under way per thread.  Nothing of the rejected nodes is read
+// or written.
 #include "ls_device.cuh"
 #include "ls_tree.cuh"
 
 namespace lsb {
 namespace {
 
-constexpr int kTcThreads = 128;
+constexpr int kTcThreads = 256;
+constexpr int kTcBatch = 8;  // copies under way per thread
 static_assert(kAtMaxNodes <= 64 && kTcThreads >= kAtMaxNodes, "a thread per node, masks of 64 bits");
 
+// Units [first, first + stride, ..) of the branch's keys, then its values, to the cache.
 template <class U>
-__device__ __forceinline__ void append(unsigned char* cache, const unsigned char* draft, long long node_stride,
-                                       long long head_stride, const int* path, int count, int heads, int units,
-                                       long long slab, int first, int tid) {
-  const int per = heads * units, n = count * per;
-#pragma unroll 4
-  for (int i = tid; i < n; i += kTcThreads) {
-    const int a = i / per, e = i - a * per, h = e / units, u = e - h * units;
-    const U x = __ldg(reinterpret_cast<const U*>(draft + path[a] * node_stride + h * head_stride) + u);
-    reinterpret_cast<U*>(cache + h * slab)[(long long)(first + a) * units + u] = x;
+__device__ __forceinline__ void append(const CommitParams& p, const int* path, int count, int row, int layer, int len,
+                                       int first, int stride) {
+  const int per = p.heads * p.vec_units, half = count * per, n = 2 * half;
+  const long long slab = (long long)p.max_len * p.vec_units;  // in units
+  const long long base = ((long long)layer * p.rows + row) * p.heads * slab + (long long)len * p.vec_units;
+  const unsigned char* dk = p.dkey.data + layer * p.dkey_layer + row * p.dkey.row;
+  const unsigned char* dv = p.dvalue.data + layer * p.dvalue_layer + row * p.dvalue.row;
+  for (int i0 = first; i0 < n; i0 += stride * kTcBatch) {
+    U x[kTcBatch];
+    U* to[kTcBatch];
+#pragma unroll
+    for (int k = 0; k < kTcBatch; ++k) {
+      const int i = i0 + k * stride;
+      to[k] = nullptr;
+      if (i < n) {
+        const bool val = i >= half;
+        const int j = val ? i - half : i, a = p.by_per(j), e = j - a * per, h = p.by_units(e), u = e - h * p.vec_units;
+        const unsigned char* from = val ? dv + path[a] * p.dvalue.pos + h * p.dvalue.head : dk + path[a] * p.dkey.pos + h * p.dkey.head;
+        x[k] = __ldg(reinterpret_cast<const U*>(from) + u);
+        to[k] = reinterpret_cast<U*>(val ? p.cache_value : p.cache_key) + base + h * slab + (long long)a * p.vec_units + u;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTcBatch; ++k)
+      if (to[k]) *to[k] = x[k];
   }
 }
 
@@ -37,7 +57,8 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
   __shared__ int par[kAtMaxNodes], want[kAtMaxNodes], path[kAtMaxNodes];
   __shared__ unsigned fits[kAtMaxNodes / 32];
   __shared__ int s_count;
-  const int r = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x, N = p.nodes;
+  const int r = blockIdx.x, layer = blockIdx.y, part = blockIdx.z, tid = threadIdx.x, N = p.nodes;
+  const bool lead = layer == 0 && part == 0;  // writes the row's results
   const long long at = (long long)r * N;
   int pi = -2, tok = 0;
   if (tid < N) {
@@ -71,7 +92,7 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
       }
     }
     s_count = count;
-    if (layer == 0) {
+    if (lead) {
       const int next = done ? p.eos : count > 0 ? want[path[count - 1]] : __ldg(p.token + at);
       p.out_len[r] = len + count;
       p.out_count[r] = count;
@@ -82,28 +103,25 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
   }
   __syncthreads();
   const int count = s_count;
-  if (layer == 0 && tid < N) p.out_path[at + tid] = tid < count ? path[tid] : -1;
-  if (count == 0) return;
-  const long long slab = (long long)p.max_len * p.vec_units * p.unit;
-  const long long base = ((long long)layer * p.rows + r) * p.heads * slab;
-  const unsigned char* dk = p.dkey.data + layer * p.dkey_layer + r * p.dkey.row;
-  const unsigned char* dv = p.dvalue.data + layer * p.dvalue_layer + r * p.dvalue.row;
-  if (p.unit == 16) {
-    append<uint4>(p.cache_key + base, dk, p.dkey.pos, p.dkey.head, path, count, p.heads, p.vec_units, slab, len, tid);
-    append<uint4>(p.cache_value + base, dv, p.dvalue.pos, p.dvalue.head, path, count, p.heads, p.vec_units, slab, len, tid);
-  } else if (p.unit == 4) {
-    append<uint32_t>(p.cache_key + base, dk, p.dkey.pos, p.dkey.head, path, count, p.heads, p.vec_units, slab, len, tid);
-    append<uint32_t>(p.cache_value + base, dv, p.dvalue.pos, p.dvalue.head, path, count, p.heads, p.vec_units, slab, len, tid);
-  } else {
-    append<uint16_t>(p.cache_key + base, dk, p.dkey.pos, p.dkey.head, path, count, p.heads, p.vec_units, slab, len, tid);
-    append<uint16_t>(p.cache_value + base, dv, p.dvalue.pos, p.dvalue.head, path, count, p.heads, p.vec_units, slab, len, tid);
-  }
+  if (lead && tid < N) p.out_path[at + tid] = tid < count ? path[tid] : -1;
+  if (count == 0 || p.heads == 0) return;
+  const int first = part * kTcThreads + tid, stride = (int)gridDim.z * kTcThreads;
+  if (p.unit == 16)
+    append<uint4>(p, path, count, r, layer, len, first, stride);
+  else if (p.unit == 4)
+    append<uint32_t>(p, path, count, r, layer, len, first, stride);
+  else
+    append<uint16_t>(p, path, count, r, layer, len, first, stride);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream) {
-  tree_commit_kernel<<<dim3((unsigned)p.rows, (unsigned)p.layers), kTcThreads, 0, stream>>>(p);
+  // parts of a (row, layer): one batch per thread at most, within two waves of the GPU
+  const long long units = 2ll * p.nodes * p.heads * p.vec_units, pairs = (long long)p.rows * p.layers;
+  const long long need = (units + kTcThreads * kTcBatch - 1) / (kTcThreads * kTcBatch), room = 2ll * kAtSms * 8 / pairs;
+  const long long parts = need < room ? need : room;
+  tree_commit_kernel<<<dim3((unsigned)p.rows, (unsigned)p.layers, (unsigned)(parts < 1 ? 1 : parts)), kTcThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
