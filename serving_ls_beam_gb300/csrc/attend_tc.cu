@@ -20,8 +20,7 @@
 //   warp 11    the queries by asynchronous copies where TMA cannot read them;
 //   warps 0-3, 4-7  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
 //              memory), reads its scores of the tile, and writes its weights over them as 16-bit
-//              values (rounded to the tensors' type; sums are of the unrounded f32 weights),
-//              handing 64 keys at a time to the products.
+//              values (rounded to the tensors' type; sums are of the unrounded f32 weights).
 // Jobs (a key tile of one slot) alternate between the slots, so that the tensor cores work for
 // one slot while the other's softmax runs.  With more than 128 queries the slots are two tiles of
 // queries over the same key tiles (each fetched once for 256 queries); with fewer they are the
@@ -59,17 +58,16 @@ struct TcShape {
   // the job before; at 64 keys four (measured below).
   static constexpr int N = DP == 64 ? 128 : 64;
   static constexpr int NSB = DP == 64 ? 3 : 4;                 // score buffers
-  static constexpr int HALVES = N / 64;                        // weights are handed over 64 keys at a time
   static constexpr int NST = 4;                                // stages of either ring
   static constexpr int NQB = DP == 64 ? 2 : 1;                 // pairs of query tiles
   static constexpr uint32_t QT = PANELS * kTaPanel;            // 128 queries of DP elements
   static constexpr uint32_t PANEL = N * 128, TILE = PANELS * PANEL;  // N keys or values
   static constexpr uint32_t Q = 0, K = 2 * NQB * QT, V = K + NST * TILE, BAR = V + NST * TILE;
   static constexpr uint32_t O = NSB * N;                       // tensor-memory column of slot 0's sums
-  // barriers: full / empty of K and V and of the queries, scores, score buffer free, weights x
-  // halves, sums x slots, sums read, join, all products issued x 2
+  // barriers: full / empty of K and V and of the queries, scores, score buffer free, weights, sums x
+  // slots, sums read, join, all products issued x 2
   static constexpr int B_KF = 0, B_KE = NST, B_VF = 2 * NST, B_VE = 3 * NST, B_QF = 4 * NST, B_QE = B_QF + NQB,
-                       B_S = B_QE + NQB, B_SE = B_S + NSB, B_P = B_SE + NSB, B_O = B_P + 2 * NSB, B_OE = B_O + 2, B_J = B_OE + 1,
+                       B_S = B_QE + NQB, B_SE = B_S + NSB, B_P = B_SE + NSB, B_O = B_P + NSB, B_OE = B_O + 2, B_J = B_OE + 1,
                        B_DONE = B_J + 1, NBAR = B_DONE + 2;
   static constexpr uint32_t WORDS = BAR + 8 * NBAR;            // tensor-memory address, abort flag, value flag
   static constexpr uint32_t BYTES = WORDS + 16 + 1024;         // + alignment of the tiles
@@ -257,7 +255,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const float c = p.scale_log2;  // not negative: a negative scale is in Q's sign
     int next_len = blockIdx.x < p.items ? __ldg(p.len + tc_row(p, blockIdx.x)) : 0;
     int jobs_before = 0, tiles_before = 0, joins = 0;
-    int sums[2] = {0, 0};  // products of either slot in the items before
+    int sums[2] = {0, 0};  // items before in which the slot had a job
     bool ok = true;
     int turn = 1;
     for (int it = blockIdx.x; it < (int)p.items && ok; it += gridDim.x) {
@@ -282,12 +280,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int t = x.tile(j), n = x.keys(t, p.nodes), b = (jobs_before + j) % NSB;
         const uint32_t ts = lanes + b * N;
         const bool draft = x.draft(t);
-        // the weights of half a tile (and the fixed-up values) are there for the products
-        auto hand_over = [&](int half) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(S::B_P + 2 * b + half));
-        };
         if (!(ok = wait_all(S::B_S + b, (jobs_before + j) / NSB))) break;
         tc_fence_after();
         // (only after the scores' wait: it says that the ring's slot has been through its last tile)
@@ -357,9 +349,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             m_run = to_m;
             l_run *= f;
             if (j >= 2) {
-              // the slot's product before this one has to end first (with three score buffers it may
-              // still run); a slot's products complete its barrier one phase each
-              if (!(ok = wait_all(S::B_O + slot, sums[slot] + (j >> 1) - 1))) break;
+              // the slot's last product has to end first (it may still run): it frees its buffer
+              const int g = jobs_before + j - 2;
+              if (!(ok = wait_all(S::B_SE + g % NSB, g / NSB))) break;
               tc_fence_after();
 #pragma unroll 1
               for (int k = 0; k < kd * 16; k += 32) {
@@ -392,31 +384,24 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               wt[i] = pack_pair<BF>(e.x, e.y);
             }
             tmem_st16(ts + k * 16, wt);
-            if (S::HALVES == 2 && k == 1) {
-              tmem_wait_st();
-              hand_over(0);
-            }
           }
           l_run += (l0.x + l1.x) + (l0.y + l1.y);
           tmem_wait_st();
-        } else if (S::HALVES == 2) {
-          hand_over(0);
         }
-        // A parity tells neighbouring phases apart, no more: the slot's last product is waited for
-        // before the weights that let the next one complete (it has ended by now, as a rule).
-        if (j >= 2 && !(ok = wait_all(S::B_O + slot, sums[slot] + (j >> 1) - 1))) break;
-        hand_over(S::HALVES - 1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::B_P + b));  // the weights, and the fixed-up values
       }
       // the slot's sums (when the slots share the queries, both slots')
       if (ok && x.jobs > slot) {
-        ok = wait_all(S::B_O + slot, sums[slot] + (x.jobs - slot + 1) / 2 - 1);
+        ok = wait_all(S::B_O + slot, sums[slot]);
       }
       // an item of one job: slot 1 keeps pace with it (it says below that the sums are read)
       if (ok && x.jobs == 1 && slot == 1) ok = wait_all(S::B_O, sums[0]);
       const bool joined = !x.wide && x.jobs > 1;
       float f = 1.0f, f_other = 0.0f;
       if (joined && ok) {
-        ok = wait_all(S::B_O + (slot ^ 1), sums[slot ^ 1] + (x.jobs - (slot ^ 1) + 1) / 2 - 1);
+        ok = wait_all(S::B_O + (slot ^ 1), sums[slot ^ 1]);
         join_ml[joins & 1][slot][row] = make_float2(m_run, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::B_J));
@@ -525,8 +510,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (lane == 0) mbar_arrive(bar(S::B_OE));
         jobs_before += x.jobs;
         tiles_before += x.nt;
-        sums[0] += (x.jobs + 1) / 2;
-        sums[1] += x.jobs / 2;
+        ++sums[0];
+        sums[1] += x.jobs > 1;
       }
     }
   } else {
@@ -548,7 +533,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (g >= NST && !(ok = wait_all(empty + st, g / NST - 1))) return;
         if (elect_one()) {
           const bool draft = x.draft(t);
-          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : S::HALVES;
+          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : N / 64;
           mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (64 * 128));
           for (int c = 0; c < S::PANELS; ++c)
             for (int hf = 0; hf < halves; ++hf) {
@@ -636,27 +621,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int steps = (x.keys(x.tile(j), p.nodes) + 15) / 16;
         const uint64_t bd = v0 + st * (S::TILE >> 4);
         const uint32_t d = tmem + S::O + s * DP, a = tmem + b * N;
+        if (!(ok = wait_all(S::B_P + b, g / NSB))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (steps == N / 16) {
 #pragma unroll
-        for (int half = 0; half < S::HALVES; ++half) {  // the weights of 64 keys at a time, as they are written
-          if (!(ok = wait_all(S::B_P + 2 * b + half, g / NSB))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            if (steps >= 4 * half + 4) {
-#pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
-            } else {
-              for (int k = 4 * half; k < steps; ++k)
-                umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
-            }
-            if (half + 1 == S::HALVES) {
-              umma_commit(bar(S::B_SE + b));
-              umma_commit(bar(S::B_O + s));
-              if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
-            }
+            for (int k = 0; k < N / 16; ++k) umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
+          } else {
+            for (int k = 0; k < steps; ++k) umma_f16_ts(d, a + 8u * k, bd + (uint64_t)k * (2048 >> 4), id_o, j >= 2 || k > 0);
           }
-          __syncwarp();
+          umma_commit(bar(S::B_SE + b));
+          if (!x.wide || s == 1) umma_commit(bar(S::B_VE + st));
+          if (j + 2 >= x.jobs) umma_commit(bar(S::B_O + s));  // the slot's last product of the item
         }
+        __syncwarp();
       }
     }
     if (elect_one()) umma_commit(bar(S::B_DONE + 1));
