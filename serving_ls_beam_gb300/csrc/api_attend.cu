@@ -21,13 +21,18 @@ int es_of(ls_dtype d) { return d == LS_DTYPE_F32 ? 4 : 2; }
 bool known(ls_dtype d) { return d == LS_DTYPE_F32 || d == LS_DTYPE_F16 || d == LS_DTYPE_BF16; }
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-// A view's pointer and strides; `written`: dimensions of more than one element need a stride.
-bool view_ok(const ls_view* v, int es, bool written, int rows, int pos, int heads) {
+// A view's pointer, and strides whose largest byte offset 64 bits hold; `written`: dimensions of more
+// than one element need a stride.
+bool view_ok(const ls_view* v, int es, bool written, int layers, int rows, int pos, int heads) {
   if (!v || !v->data || misaligned(v->data, (size_t)es)) return false;
-  const int64_t most = INT64_MAX / 8 / (1ll << 31);
-  for (int64_t s : {v->layer, v->row, v->pos, v->head})
-    if (s < 0 || s > most) return false;
-  if (written && ((rows > 1 && v->row == 0) || (pos > 1 && v->pos == 0) || (heads > 1 && v->head == 0))) return false;
+  const struct {
+    int64_t stride;
+    int extent;
+  } dims[] = {{v->layer, layers}, {v->row, rows}, {v->pos, pos}, {v->head, heads}};
+  for (const auto& d : dims) {
+    if (d.stride < 0 || (written && d.extent > 1 && d.stride == 0)) return false;
+    if (d.stride > (INT64_MAX >> 4) / es / (d.extent > 1 ? d.extent : 1)) return false;
+  }
   return true;
 }
 
@@ -198,8 +203,10 @@ ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view
   const long long m = (long long)k * q_len * (heads / kv_heads);
   if ((long long)batch * k > INT_MAX || m > INT_MAX) return LS_ERR_UNSUPPORTED;
   const int es = es_of(dtype);
-  if (!view_ok(q, es, false, 0, 0, 0) || !view_ok(out, es, true, batch * k, q_len, heads)) return LS_ERR_INVALID_ARG;
-  if (max_src > 0 && (!view_ok(key, es, false, 0, 0, 0) || !view_ok(value, es, false, 0, 0, 0)))
+  if (!view_ok(q, es, false, 1, batch * k, q_len, heads) ||
+      !view_ok(out, es, true, 1, batch * k, q_len, heads)) return LS_ERR_INVALID_ARG;
+  if (max_src > 0 && (!view_ok(key, es, false, 1, batch, max_src, kv_heads) ||
+                      !view_ok(value, es, false, 1, batch, max_src, kv_heads)))
     return LS_ERR_INVALID_ARG;
   if (!src_len || misaligned(src_len, 4) || !workspace || misaligned(workspace, 256) ||
       workspace_bytes < workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim))
@@ -238,10 +245,11 @@ ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls
     return LS_ERR_INVALID_ARG;
   if (rows == 0) return LS_OK;
   const int es = es_of(dtype);
-  if (!view_ok(q, es, false, 0, 0, 0) || !view_ok(out, es, true, rows, nodes, heads) ||
-      !view_ok(draft_key, es, false, 0, 0, 0) || !view_ok(draft_value, es, false, 0, 0, 0))
+  if (!view_ok(q, es, false, 1, rows, nodes, heads) || !view_ok(out, es, true, 1, rows, nodes, heads) ||
+      !view_ok(draft_key, es, false, 1, rows, nodes, kv_heads) || !view_ok(draft_value, es, false, 1, rows, nodes, kv_heads))
     return LS_ERR_INVALID_ARG;
-  if (max_len > 0 && (!view_ok(cache_key, es, false, 0, 0, 0) || !view_ok(cache_value, es, false, 0, 0, 0)))
+  if (max_len > 0 && (!view_ok(cache_key, es, false, 1, rows, max_len, kv_heads) ||
+                      !view_ok(cache_value, es, false, 1, rows, max_len, kv_heads)))
     return LS_ERR_INVALID_ARG;
   if (!cache_len || misaligned(cache_len, 4) || !parent || misaligned(parent, 4) || !workspace ||
       misaligned(workspace, 256) || workspace_bytes < workspace_size(rows, 1, nodes, heads, kv_heads, max_len, head_dim))
@@ -286,8 +294,8 @@ ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cach
   const int es = es_of(dtype);
   const bool move = layers > 0 && heads > 0 && head_dim > 0 && max_len > 0;
   if (move && (!cache_key || !cache_value || cache_key == cache_value || misaligned(cache_key, (size_t)es) ||
-               misaligned(cache_value, (size_t)es) || !view_ok(draft_key, es, false, 0, 0, 0) ||
-               !view_ok(draft_value, es, false, 0, 0, 0)))
+               misaligned(cache_value, (size_t)es) || !view_ok(draft_key, es, false, layers, rows, nodes, heads) ||
+               !view_ok(draft_value, es, false, layers, rows, nodes, heads)))
     return LS_ERR_INVALID_ARG;
   const void* words[] = {cache_len, parent, token, target, out_len, out_path, out_count, out_token};
   for (const void* w : words)

@@ -578,10 +578,11 @@ cudaError_t run_mma(const AttendParams& p, int dtype, cudaStream_t stream) {
   if (p.max_len >= S::KB && !encode_keys(maps, p, dtype, S::KB)) return cudaErrorInvalidValue;
   long long grid = p.items;
   if (p.warps == 1) {
-    int occ = 1;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, kMmThreads, bytes);
+    static std::atomic<uint64_t> known{0};
+    int occ = 0;
+    e = resident_ctas(kernel, kMmThreads, bytes, known, &occ);
     if (e != cudaSuccess) return e;
-    const long long need = (p.items + kMmWarps - 1) / kMmWarps, fit = (long long)kAtSms * (occ > 0 ? occ : 1);
+    const long long need = (p.items + kMmWarps - 1) / kMmWarps, fit = (long long)kAtSms * occ;
     grid = need < fit ? need : fit;
   }
   kernel<<<(unsigned)grid, kMmThreads, bytes, stream>>>(maps[0], maps[1], p);

@@ -12,7 +12,8 @@
 // the block's scores are formed, the values' when its sums are.  The 8 dot products of a lane
 // group are reduced together, each exchange halving the products that a lane still holds (7
 // exchanges instead of 24), which leaves every lane with the score of its own key: one
-// exponential per key, not one per lane.  The drafted tokens follow the row's keys without a gap.
+// exponential per key, not one per lane.  One and two queries keep four CTAs per SM (512 rows of 64
+// positions 47 -> 42 us); with four queries the same cap spills and costs a third.  The drafted tokens follow the row's keys without a gap.
 //
 // A warp takes whole problems in turn (AttendParams::warps 1), or the four warps of a CTA take
 // the blocks of one (part of a) problem in turn and merge through shared memory (4).
@@ -65,7 +66,7 @@ __device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
 }
 
 template <int LPK, int MQ>
-__global__ void __launch_bounds__(kAsThreads) attend_step_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kernel(const AttendParams p) {
   constexpr int DT = DT_F32, E = 4, ES = 4, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
   __shared__ unsigned long long trees[kAsWarps][kAtMaxNodes * 12 / 8];
   __shared__ float wm[kAsWarps][MQ], wl[kAsWarps][MQ];
@@ -278,14 +279,10 @@ template <int LPK, int MQ>
 cudaError_t run_step(const AttendParams& p, cudaStream_t stream) {
   long long grid = p.items;
   if (p.warps == 1) {
-    static int occ = 0;
-    if (occ == 0) {
-      int n = 0;
-      const cudaError_t e =
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attend_step_kernel<LPK, MQ>, kAsThreads, 0);
-      if (e != cudaSuccess) return e;
-      occ = n > 0 ? n : 1;
-    }
+    static std::atomic<uint64_t> known{0};
+    int occ = 0;
+    const cudaError_t e = resident_ctas(attend_step_kernel<LPK, MQ>, kAsThreads, 0, known, &occ);
+    if (e != cudaSuccess) return e;
     const long long need = (p.items + kAsWarps - 1) / kAsWarps, fit = (long long)kAtSms * occ;
     grid = need < fit ? need : fit;
   }

@@ -103,6 +103,23 @@ inline cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t>&
   return e;
 }
 
+// CTAs of a kernel that an SM holds at once (at least 1); `known` keeps the last answer, its shared
+// memory in the upper and the number in the lower half.
+template <class Kernel>
+inline cudaError_t resident_ctas(Kernel kernel, int threads, int bytes, std::atomic<uint64_t>& known, int* ctas) {
+  const uint64_t k = known.load(std::memory_order_relaxed);
+  if ((uint32_t)k != 0 && (k >> 32) == (uint64_t)bytes) {
+    *ctas = (int)(uint32_t)k;
+    return cudaSuccess;
+  }
+  int n = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, bytes);
+  if (e != cudaSuccess) return e;
+  *ctas = n < 1 ? 1 : n;
+  known.store((uint64_t)bytes << 32 | (uint32_t)*ctas, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 cudaError_t launch_attend_simt(const AttendParams& p, int dtype, cudaStream_t stream);
 int attend_simt_queries(int dtype, int m);  // queries per CTA
 // f32, every stride and address a multiple of 16 bytes, head size up to kAtStepDim

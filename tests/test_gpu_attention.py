@@ -386,12 +386,35 @@ def test_same_workspace_and_other_streams(dev, kernel, T):
         assert torch.equal(out, again)  # the same bits every time
 
 
-def test_graph_capture(dev, kernel):
+@pytest.mark.parametrize("T", [1, 20, 150])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_cross_offsets_past_32_bits(dev, kernel, dtype, T):
+    """Keys a megabyte apart and sentences gigabytes apart: byte offsets of more than 2^32 within a
+    row, element offsets of more than 2^31 between rows."""
+    g = np.random.default_rng(T)
+    B, H, S, D = 2, 1, 700, 64
+    es = 4 if dtype == "f32" else 2
+    pos = (1 << 23) // es  # 8 MB from key to key: 5.6 GB a row
+    big = torch.empty(B * S * pos + D, dtype=DT[dtype], device=dev)
+    k = torch.as_strided(big, (B, H, S, D), (S * pos, D, pos, 1))
+    v = torch.as_strided(big, (B, H, S, D), (S * pos, D, pos, 1), 4 * D)
+    k.copy_(tensor(g, (B, H, S, D), dtype, dev))
+    v.copy_(tensor(g, (B, H, S, D), dtype, dev))
+    q = tensor(g, (B, 1, T, H, D), dtype, dev)
+    lens = [700, 601]
+    out = run_cross(q, k, v, lens)
+    pick = sorted({0, T - 1})
+    want, bound = ap.cross(f64(q)[:, :, pick], f64(k), f64(v), lens, D ** -0.5, dtype)
+    close(out[:, :, pick], want, bound)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_graph_capture(dev, kernel, T):
     g = np.random.default_rng(12)
-    q = tensor(g, (1, 2, 1, 4, 64), "f16", dev)
+    q = tensor(g, (1, 2, T, 4, 64), "f16", dev)
     k, v = tensor(g, (1, 2, 900, 64), "f16", dev), tensor(g, (1, 2, 900, 64), "f16", dev)
     lens = torch.full((1,), 900, dtype=torch.int32, device=dev)
-    out, ws = torch.zeros_like(q), workspace(lsb.ls_cross_attention_workspace_size(1, 2, 1, 4, 2, 900, 64), dev)
+    out, ws = torch.zeros_like(q), workspace(lsb.ls_cross_attention_workspace_size(1, 2, T, 4, 2, 900, 64), dev)
     lsb.check(lsb.ls_cross_attention(q, k, v, lens, out, ws))
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
