@@ -7,9 +7,12 @@
 // with the running maximum and sum of the softmax (Milakov and Gimelshein, 2018).  One CTA per
 // SM takes item after item (up to 256 queries of one problem and one part of its keys), in tiles
 // of 128 keys (64 for head sizes above 64); twelve warps:
-//   warp 8     TMA producer: two rings of swizzled key and value tiles (64-element panels of
-//              128-byte rows; a tile's second 64 keys are not fetched when the row ends before)
-//              and the queries, where their layout lets TMA read them in order;
+//   warp 8     loads the keys by TMA into a ring of swizzled tiles (64-element panels of 128-byte
+//              rows; a tile's second 64 keys are not fetched when the row ends before), and the
+//              queries, by TMA where their layout lets it read them in order, else by
+//              asynchronous copies;
+//   warp 11    the values, in a ring of their own so that neither waits for the other, and what
+//              each node of the item's tree sees;
 //   warp 9     owns the 512 tensor-memory columns and issues S = Q K^T (Q and K from shared
 //              memory, M 128, N the tile's keys);
 //   warp 10    issues O += P V (P from tensor memory, V read as the transposed operand from the
@@ -17,7 +20,6 @@
 //              products take one warp longer to issue than the tensor cores to run.  Each walks
 //              the jobs as a whole, so that the compiler sees one path and keeps the operands in
 //              uniform registers; an elected lane issues;
-//   warp 11    the queries by asynchronous copies where TMA cannot read them;
 //   warps 0-3, 4-7  the softmax of slot 0 and slot 1: a thread has one query (one lane of tensor
 //              memory), reads its scores of the tile, and writes its weights over them as 16-bit
 //              values (rounded to the tensors' type; sums are of the unrounded f32 weights).
@@ -34,6 +36,8 @@
 // status word, and the CTA lets its copies and products finish, frees its tensor memory and
 // returns.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"
@@ -65,10 +69,10 @@ struct TcShape {
   static constexpr uint32_t Q = 0, K = 2 * NQB * QT, V = K + NST * TILE, BAR = V + NST * TILE;
   static constexpr uint32_t O = NSB * N;                       // tensor-memory column of slot 0's sums
   // barriers: full / empty of K and V and of the queries, scores, score buffer free, weights, sums x
-  // slots, sums read, join, all products issued x 2
+  // slots, sums read, join, tree there / read x turns, all products issued x 2
   static constexpr int B_KF = 0, B_KE = NST, B_VF = 2 * NST, B_VE = 3 * NST, B_QF = 4 * NST, B_QE = B_QF + NQB,
-                       B_S = B_QE + NQB, B_SE = B_S + NSB, B_P = B_SE + NSB, B_O = B_P + NSB, B_OE = B_O + 2, B_J = B_OE + 1,
-                       B_DONE = B_J + 1, NBAR = B_DONE + 2;
+                       B_S = B_QE + NQB, B_SE = B_S + NSB, B_P = B_SE + NSB, B_O = B_P + NSB, B_OE = B_O + 2, B_J = B_OE + 1, B_T = B_J + 1, B_TE = B_T + 2,
+                       B_DONE = B_TE + 2, NBAR = B_DONE + 2;
   static constexpr uint32_t WORDS = BAR + 8 * NBAR;            // tensor-memory address, abort flag, value flag
   static constexpr uint32_t BYTES = WORDS + 16 + 1024;         // + alignment of the tiles
 };
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   using S = TcShape<DP>;
   constexpr int NST = S::NST, NSB = S::NSB, NQB = S::NQB, N = S::N, DT = BF ? DT_BF16 : DT_F16;
   extern __shared__ unsigned char ta_raw[];
-  __shared__ unsigned long long trees[8][kAtMaxNodes * 12 / 8];
+  __shared__ unsigned long long trees[2][kAtMaxNodes * 12 / 8];  // by turns
   __shared__ float2 join_ml[2][2][kTaM];
   __shared__ uint4 stage[8][32 * 4];
   const uint32_t raw = smem_addr(ta_raw), base = (raw + 1023u) & ~1023u;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < S::NBAR; ++i) {
       const bool weights = i >= S::B_P && i < S::B_O;  // one arrival per warp of the slot's softmax
-      const bool all = i == S::B_OE || i == S::B_J;    // one per softmax warp
+      const bool all = i == S::B_OE || i == S::B_J || (i >= S::B_TE && i < S::B_TE + 2);  // one per softmax warp
       mbar_init(bar(i), weights ? 4 : all ? 8 : 1);
     }
     *abort = 0;
@@ -249,29 +253,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax
     const int slot = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane, wg = tid - slot * 128;
-    const TreeSeen tree = tree_at(trees[warp], kAtMaxNodes);
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t to = lanes + S::O + slot * DP, other_o = lanes + S::O + (slot ^ 1) * DP;
     const float c = p.scale_log2;  // not negative: a negative scale is in Q's sign
     int next_len = blockIdx.x < p.items ? __ldg(p.len + tc_row(p, blockIdx.x)) : 0;
-    int jobs_before = 0, tiles_before = 0, joins = 0;
+    int jobs_before = 0, tiles_before = 0, joins = 0, active = 0;
     int sums[2] = {0, 0};  // items before in which the slot had a job
     bool ok = true;
     int turn = 1;
     for (int it = blockIdx.x; it < (int)p.items && ok; it += gridDim.x) {
       turn ^= 1;
-      const TcItem<S::N> x = tc_item<S::N>(p, it, next_len);
+      const TcItem<N> x = tc_item<N>(p, it, next_len);
       if (x.len != next_len && tid == 0) atomicOr(p.status, kDevInternal);
       if (it + gridDim.x < p.items) next_len = __ldg(p.len + tc_row(p, it + gridDim.x));
       const int qn = x.wide ? min(kTaM, x.nq - slot * kTaM) : x.nq;  // queries of the slot
       const int qi = x.i0 + (x.wide ? slot * kTaM : 0) + row;
       const bool mine = row < qn, warp_live = quarter * 32 < qn;
       unsigned long long sees = 0ull;
-      if (p.nodes) {
+      if (p.nodes && x.nt > 0) {
+        if (!(ok = wait_all(S::B_T + (active & 1), active / 2))) break;
+        if (mine) sees = tree_at(trees[active & 1], kAtMaxNodes).mask[p.by_group(qi)];
         __syncwarp();
-        if (tree_seen(tree, p.parent + (long long)x.r * p.nodes, p.nodes, lane, 32, [] { __syncwarp(); }))
-          atomicOr(p.status, kDevInternal);
-        if (mine) sees = tree.mask[p.by_group(qi)];
+        if (lane == 0) mbar_arrive(bar(S::B_TE + (active & 1)));
       }
       const bool alive = mine && (!p.nodes || sees != 0);
       const bool dead_any = __any_sync(~0u, mine && !alive);  // (lanes without a query may hold anything)
@@ -309,16 +312,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           fence_async_shared();
         }
         __syncwarp();
-        if (warp_live) {
-          uint32_t s[N / 32][32];
+        // the tile's first CH * 32 keys (the others are past the row's end)
+        auto softmax = [&](auto chunks) {
+          constexpr int CH = decltype(chunks)::value;
+          uint32_t s[CH][32];
 #pragma unroll
-          for (int k = 0; k < N / 32; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
+          for (int k = 0; k < CH; ++k) tmem_ld32_issue(ts + k * 32, s[k]);
           tmem_wait_ld(s[0]);
 #pragma unroll
-          for (int k = 1; k < N / 32; ++k) tmem_after_wait(s[k]);
-          if (n < N || dead_any || draft) {
+          for (int k = 1; k < CH; ++k) tmem_after_wait(s[k]);
+          if (CH < N / 32 || n < N || dead_any || draft) {
 #pragma unroll
-            for (int k = 0; k < N / 32; ++k) {
+            for (int k = 0; k < CH; ++k) {
               unsigned see = draft ? (k < 2 ? (unsigned)(sees >> (32 * k)) : 0u) : ~0u;
               if (!alive) see = 0u;
               const int left = n - 32 * k;
@@ -327,9 +332,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               for (int i = 0; i < 32; ++i) s[k][i] = (see >> i) & 1u ? s[k][i] : 0xff800000u;
             }
           }
-          float m4[N / 32];
+          float m4[CH];
 #pragma unroll
-          for (int k = 0; k < N / 32; ++k) {
+          for (int k = 0; k < CH; ++k) {
             float a = max3(__uint_as_float(s[k][0]), __uint_as_float(s[k][1]), __uint_as_float(s[k][2]));
             float bb = max3(__uint_as_float(s[k][3]), __uint_as_float(s[k][4]), __uint_as_float(s[k][5]));
 #pragma unroll
@@ -339,8 +344,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
             m4[k] = max3(a, bb, fmaxf(__uint_as_float(s[k][30]), __uint_as_float(s[k][31])));
           }
-          float mn = fmaxf(m4[0], m4[1]);
-          if constexpr (N == 128) mn = fmaxf(mn, fmaxf(m4[2], m4[3]));
+          float mn = m4[0];
+#pragma unroll
+          for (int k = 1; k < CH; ++k) mn = fmaxf(mn, m4[k]);
           mn *= c;
           const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
           if (__any_sync(~0u, grow)) {
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (j >= 2) {
               // the slot's last product has to end first (it may still run): it frees its buffer
               const int g = jobs_before + j - 2;
-              if (!(ok = wait_all(S::B_SE + g % NSB, g / NSB))) break;
+              if (!wait_all(S::B_SE + g % NSB, g / NSB)) return false;
               tc_fence_after();
 #pragma unroll 1
               for (int k = 0; k < kd * 16; k += 32) {
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const float2 c2 = make_float2(c, c), b2 = make_float2(-sub, -sub);
           float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
 #pragma unroll
-          for (int k = 0; k < N / 32; ++k) {
+          for (int k = 0; k < CH; ++k) {
             uint32_t wt[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -387,6 +393,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
           l_run += (l0.x + l1.x) + (l0.y + l1.y);
           tmem_wait_st();
+          return true;
+        };
+        if (warp_live) {
+          ok = n > N / 2 ? softmax(std::integral_constant<int, N / 32>{}) : softmax(std::integral_constant<int, N / 64>{});
+          if (!ok) break;
         }
         tc_fence_before();
         __syncwarp();
@@ -419,9 +430,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (warp_live && (x.wide || joined || slot == 0)) {
-        const bool zero = l_run == 0.0f;
+        const bool zero = mine && l_run == 0.0f;
         if (p.splits == 1) {
-          const float inv = zero ? 0.0f : 1.0f / l_run;
+          const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
           f *= inv;
           f_other *= inv;
         }
@@ -508,6 +519,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if (x.nt > 0) {
         tc_fence_before();
         if (lane == 0) mbar_arrive(bar(S::B_OE));
+        ++active;
         jobs_before += x.jobs;
         tiles_before += x.nt;
         ++sums[0];
@@ -520,39 +532,47 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     constexpr uint32_t id0 = (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)(kTaM >> 4) << 24);
     constexpr uint32_t id_s = id0 | ((uint32_t)(S::N >> 3) << 17);
     const uint32_t id_o = id0 | (1u << 16) | ((uint32_t)(kd * 2) << 17);  // N = the head size; B is MN-major
-  if (warp == 8) {
-    // ---------------------------------------------------------------- producer
-    TcWalk<S::N> w;
-    w.begin(p);
-    bool ok = true;
-    int kn = 0, vn = 0, qn = 0;  // tiles and query sets asked for
-    for (; w.valid && ok; w.next(p)) {
-      const TcItem<S::N>& x = w.x;
-      auto load = [&](int t, uint32_t ring, int full, int empty, const CUtensorMap* map, const CUtensorMap* dmap, int* count) {
-        const int g = w.tile + t, st = g % NST;
-        if (g >= NST && !(ok = wait_all(empty + st, g / NST - 1))) return;
-        if (elect_one()) {
-          const bool draft = x.draft(t);
-          const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : N / 64;
-          mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (64 * 128));
-          for (int c = 0; c < S::PANELS; ++c)
-            for (int hf = 0; hf < halves; ++hf) {
-              const uint32_t dst = base + ring + st * S::TILE + c * S::PANEL + hf * (64 * 128);
-              if (draft)
-                tma_load_4d(dst, dmap, c * 64, 0, x.h, x.r, bar(full + st));
-              else
-                tma_load_4d(dst, map, c * 64, (x.t_lo + t) * N + hf * 64, p.kv_head_one ? 0 : x.h,
-                            p.kv_row_one ? 0 : x.r, bar(full + st));
-            }
+  // Tile t of a walk's item into a ring (keys or values).
+  auto load = [&](const TcWalk<N>& w, int t, uint32_t ring, int full, int empty, const CUtensorMap* map,
+                  const CUtensorMap* dmap) {
+    const TcItem<N>& x = w.x;
+    const int g = w.tile + t, st = g % NST;
+    if (g >= NST && !wait_all(empty + st, g / NST - 1)) return false;
+    if (elect_one()) {
+      const bool draft = x.draft(t);
+      const int halves = draft || x.keys(t, p.nodes) <= 64 ? 1 : N / 64;
+      mbar_arrive_expect_tx(bar(full + st), (uint32_t)(halves * S::PANELS) * (64 * 128));
+      for (int c = 0; c < S::PANELS; ++c)
+        for (int hf = 0; hf < halves; ++hf) {
+          const uint32_t dst = base + ring + st * S::TILE + c * S::PANEL + hf * (64 * 128);
+          if (draft)
+            tma_load_4d(dst, dmap, c * 64, 0, x.h, x.r, bar(full + st));
+          else
+            tma_load_4d(dst, map, c * 64, (x.t_lo + t) * N + hf * 64, p.kv_head_one ? 0 : x.h, p.kv_row_one ? 0 : x.r,
+                        bar(full + st));
         }
-        __syncwarp();
-        *count = g + 1;
-      };
-      load(0, S::K, S::B_KF, S::B_KE, &map_k, &map_dk, &kn);
-      if (p.q_tma && ok) {
-        const int g = w.active, st = g % NQB;
-        if (g >= NQB) ok = wait_all(S::B_QE + st, g / NQB - 1);
-        if (ok && elect_one()) {
+    }
+    __syncwarp();
+    return true;
+  };
+  // After a wait that ran out: the ring's copies up to number n land before the CTA may exit.
+  auto drain = [&](int n, int slots, int full) {
+    for (int g = max(0, n - slots); g < n; ++g) mbar_wait_bounded(bar(full + g % slots), (uint32_t)(g / slots) & 1u, kTaDrainNs);
+  };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- keys and queries
+    TcWalk<N> w;
+    bool ok = true;
+    int kn = 0, qn = 0;  // tiles and query sets asked for
+    for (w.begin(p); w.valid && ok; w.next(p)) {
+      const TcItem<N>& x = w.x;
+      if (!(ok = load(w, 0, S::K, S::B_KF, S::B_KE, &map_k, &map_dk))) break;
+      kn = w.tile + 1;
+      const int st = w.active % NQB;
+      if (w.active >= NQB && !(ok = wait_all(S::B_QE + st, w.active / NQB - 1))) break;
+      if (p.q_tma) {
+        if (elect_one()) {
           const int slots = x.wide ? 2 : 1, token = p.by_group(x.i0);
           mbar_arrive_expect_tx(bar(S::B_QF + st), (uint32_t)slots * S::QT);
           for (int s = 0; s < slots; ++s)
@@ -561,25 +581,50 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                           x.h, x.r, bar(S::B_QF + st));
         }
         __syncwarp();
-        if (ok) qn = g + 1;
+        qn = w.active + 1;
+      } else {  // by asynchronous copies
+        const int rows = x.wide ? 2 * kTaM : kTaM;
+        auto place = [&](int e) {
+          const int qr = e / (DP / 8), ch = e % (DP / 8);
+          return S::Q + (2 * st + (qr >> 7)) * S::QT + (ch >> 3) * kTaPanel + (qr & 127) * 128 + (((ch & 7) ^ (qr & 7)) << 4);
+        };
+        for (int r0 = 0; r0 < rows; r0 += 32) {  // each lane knows one row's address
+          const long long mine = r0 + lane < x.nq ? query_offset(p, p.q, x.r, x.h, x.i0 + r0 + lane) : 0;
+          for (int e = r0 * (DP / 8) + lane; e < (r0 + 32) * (DP / 8); e += 32) {
+            const int qr = e / (DP / 8), ch = e % (DP / 8);
+            const long long off = __shfl_sync(~0u, mine, qr - r0);
+            const bool there = qr < x.nq && ch * 8 < p.dim;
+            cp_async16_fill(base + place(e), there ? p.q.data + off + ch * 16 : p.q.data, there ? 16 : 0);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        if (p.negate) {  // a negative scale: the queries' signs, each lane the vectors it copied
+          for (int e = lane; e < rows * (DP / 8); e += 32) {
+            uint4* v = reinterpret_cast<uint4*>(gbase + place(e));
+            *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
+          }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::B_QF + st));
       }
-      for (int t = 0; t < x.nt && ok; ++t) {
-        if (t + 1 < x.nt) load(t + 1, S::K, S::B_KF, S::B_KE, &map_k, &map_dk, &kn);
-        if (ok) load(t, S::V, S::B_VF, S::B_VE, &map_v, &map_dv, &vn);
+      for (int t = 1; t < x.nt && ok; ++t) {
+        ok = load(w, t, S::K, S::B_KF, S::B_KE, &map_k, &map_dk);
+        if (ok) kn = w.tile + t + 1;
       }
     }
-    if (!ok) {  // every copy issued lands before the CTA may exit
-      for (int g = max(0, kn - NST); g < kn; ++g) mbar_wait_bounded(bar(S::B_KF + g % NST), (uint32_t)(g / NST) & 1u, kTaDrainNs);
-      for (int g = max(0, vn - NST); g < vn; ++g) mbar_wait_bounded(bar(S::B_VF + g % NST), (uint32_t)(g / NST) & 1u, kTaDrainNs);
-      for (int g = max(0, qn - NQB); g < qn; ++g) mbar_wait_bounded(bar(S::B_QF + g % NQB), (uint32_t)(g / NQB) & 1u, kTaDrainNs);
+    if (!ok) {
+      drain(kn, NST, S::B_KF);
+      drain(qn, NQB, S::B_QF);
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- scores
     const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K);
     bool ok = true;
-    TcWalk<S::N> w;
+    TcWalk<N> w;
     for (w.begin(p); w.valid && ok; w.next(p)) {
-      const TcItem<S::N>& x = w.x;
+      const TcItem<N>& x = w.x;
       const int qs = w.active % NQB;
       if (!(ok = wait_all(S::B_QF + qs, w.active / NQB))) break;
       for (int j = 0; j < x.jobs; ++j) {
@@ -610,9 +655,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // ---------------------------------------------------------------- values
     const uint64_t v0 = desc_mn(base + S::V, S::PANEL);
     bool ok = true;
-    TcWalk<S::N> w;
+    TcWalk<N> w;
     for (w.begin(p); w.valid && ok; w.next(p)) {
-      const TcItem<S::N>& x = w.x;
+      const TcItem<N>& x = w.x;
       // the last item's sums are read before the first product of this one replaces them
       if (w.active > 0 && !(ok = wait_all(S::B_OE, w.active - 1))) break;
       for (int j = 0; j < x.jobs && ok; ++j) {
@@ -640,41 +685,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (elect_one()) umma_commit(bar(S::B_DONE + 1));
     __syncwarp();
     mbar_wait_bounded(bar(S::B_DONE + 1), 0u, kTaDrainNs);
-  } else if (!p.q_tma) {
-    // ---------------------------------------------------------------- queries
-    TcWalk<S::N> w;
-    w.begin(p);
+  } else {
+    // ---------------------------------------------------------------- trees and values
+    TcWalk<N> w;
     bool ok = true;
-    for (; w.valid && ok; w.next(p)) {
-      const TcItem<S::N>& x = w.x;
-      const int st = w.active % NQB;
-      if (w.active >= NQB && !(ok = wait_all(S::B_QE + st, w.active / NQB - 1))) break;
-      const int rows = x.wide ? 2 * kTaM : kTaM;
-      auto place = [&](int e) {
-        const int qr = e / (DP / 8), ch = e % (DP / 8);
-        return S::Q + (2 * st + (qr >> 7)) * S::QT + (ch >> 3) * kTaPanel + (qr & 127) * 128 + (((ch & 7) ^ (qr & 7)) << 4);
-      };
-      for (int r0 = 0; r0 < rows; r0 += 32) {  // each lane knows one row's address
-        const long long mine = r0 + lane < x.nq ? query_offset(p, p.q, x.r, x.h, x.i0 + r0 + lane) : 0;
-        for (int e = r0 * (DP / 8) + lane; e < (r0 + 32) * (DP / 8); e += 32) {
-          const int qr = e / (DP / 8), ch = e % (DP / 8);
-          const long long off = __shfl_sync(~0u, mine, qr - r0);
-          const bool there = qr < x.nq && ch * 8 < p.dim;
-          cp_async16_fill(base + place(e), there ? p.q.data + off + ch * 16 : p.q.data, there ? 16 : 0);
-        }
+    int vn = 0;
+    for (w.begin(p); w.valid && ok; w.next(p)) {
+      const TcItem<N>& x = w.x;
+      if (p.nodes) {
+        const int turn = w.active & 1;
+        if (w.active >= 2 && !(ok = wait_all(S::B_TE + turn, w.active / 2 - 1))) break;
+        if (tree_seen(tree_at(trees[turn], kAtMaxNodes), p.parent + (long long)x.r * p.nodes, p.nodes, lane, 32,
+                      [] { __syncwarp(); }))
+          atomicOr(p.status, kDevInternal);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::B_T + turn));
       }
-      cp_async_commit();
-      cp_async_wait<0>();
-      if (p.negate) {  // a negative scale: the queries' signs, each lane the vectors it copied
-        for (int e = lane; e < rows * (DP / 8); e += 32) {
-          uint4* v = reinterpret_cast<uint4*>(gbase + place(e));
-          *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
-        }
+      for (int t = 0; t < x.nt && ok; ++t) {
+        ok = load(w, t, S::V, S::B_VF, S::B_VE, &map_v, &map_dv);
+        if (ok) vn = w.tile + t + 1;
       }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(S::B_QF + st));
     }
+    if (!ok) drain(vn, NST, S::B_VF);
   }
   }
   __syncthreads();
