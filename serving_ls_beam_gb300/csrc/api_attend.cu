@@ -154,6 +154,7 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.by_head.set(p.kv_heads);
   p.by_group.set(p.group);
   p.by_q_len.set(p.q_len);
+  p.by_m.set(p.m);
   cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
                   : step ? launch_attend_step(p, stream)
                   : mma ? launch_attend_mma(p, dtype, stream)

@@ -218,39 +218,68 @@ __global__ void __launch_bounds__(kSiThreads) attend_simt_kernel(const AttendPar
   }
 }
 
-// The parts of each query joined: a warp per query, lane d the elements d, d + 32, ...
+// The parts of each query joined, a CTA to a query: its warps take the parts in turn, a lane four
+// elements (two of them for head sizes above 128), and add up in the warps' order.  What counts is
+// that all of a query's parts are under way at once: with a warp to a query and the parts one after
+// the other, 19 parts of 512 queries took 21 us instead of 6 (alone, cold).
+constexpr int kJoinWarps = 4;
 template <int DT>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) {
-  constexpr int B = Traits<DT>::kBytes;
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendParams p) {
+  constexpr int B = Traits<DT>::kBytes, VEC = kAtMaxDim / 128;
+  __shared__ float acc[kJoinWarps][kAtMaxDim], sums[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = blockIdx.x, pb = p.by_m(w), i = w - pb * p.m, r = p.by_head(pb), h = pb - r * p.kv_heads;
+  const float2* ml = p.part_ml + (long long)w * p.splits;
+  const float* po = p.part_o + (long long)w * p.splits * p.dim;
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long problems = (long long)p.rows * p.kv_heads;
-  if (w >= problems * p.m) return;
-  const int pb = (int)(w / p.m), i = (int)(w - (long long)pb * p.m), r = p.by_head(pb), h = pb - r * p.kv_heads;
-  const float2* ml = p.part_ml + w * p.splits;
-  const float* po = p.part_o + w * p.splits * p.dim;
   float M = -INFINITY;
   for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, ml[s].x);
 #pragma unroll
   for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
   const float base = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, o[kAtMaxDim / 32];
+  float L = 0.0f, o[VEC][4];
 #pragma unroll
-  for (int c = 0; c < kAtMaxDim / 32; ++c) o[c] = 0.0f;
+  for (int c = 0; c < VEC; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.0f;
+  const bool four = p.dim % 4 == 0;
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = warp; s < p.splits; s += kJoinWarps) {
     const float2 e = ml[s];
     const float f = fast_exp2(e.x - base);
     L = fmaf(f, e.y, L);
 #pragma unroll
-    for (int c = 0; c < kAtMaxDim / 32; ++c)
-      if (c * 32 + lane < p.dim) o[c] = add_part(o[c], f, po[(long long)s * p.dim + c * 32 + lane], e.y);
+    for (int c = 0; c < VEC; ++c) {
+      const int d = c * 128 + lane * 4;
+      const float* at = po + (long long)s * p.dim + d;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (four) {
+        if (d < p.dim) v = *reinterpret_cast<const float4*>(at);
+      } else {
+        if (d < p.dim) v.x = at[0];
+        if (d + 1 < p.dim) v.y = at[1];
+        if (d + 2 < p.dim) v.z = at[2];
+        if (d + 3 < p.dim) v.w = at[3];
+      }
+      o[c][0] = add_part(o[c][0], f, v.x, e.y);
+      o[c][1] = add_part(o[c][1], f, v.y, e.y);
+      o[c][2] = add_part(o[c][2], f, v.z, e.y);
+      o[c][3] = add_part(o[c][3], f, v.w, e.y);
+    }
   }
-  unsigned char* out = p.out.data + query_offset(p, p.out, r, h, i);
 #pragma unroll
-  for (int c = 0; c < kAtMaxDim / 32; ++c)
-    if (c * 32 + lane < p.dim) store_elem<DT>(out + (c * 32 + lane) * B, L == 0.0f ? 0.0f : o[c] / L);
+  for (int c = 0; c < VEC; ++c)
+    *reinterpret_cast<float4*>(&acc[warp][c * 128 + lane * 4]) = make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+  if (lane == 0) sums[warp] = L;
+  __syncthreads();
+  float total = 0.0f;
+#pragma unroll
+  for (int x = 0; x < kJoinWarps; ++x) total += sums[x];
+  unsigned char* out = p.out.data + query_offset(p, p.out, r, h, i);
+  for (int d = threadIdx.x; d < p.dim; d += kJoinWarps * 32) {
+    float y = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) y += acc[x][d];
+    store_elem<DT>(out + d * B, total == 0.0f ? 0.0f : y / total);
+  }
 }
 
 template <int DT, int MQ, int ND>
@@ -291,8 +320,7 @@ cudaError_t launch_attend_simt(const AttendParams& p, int dtype, cudaStream_t st
 }
 
 cudaError_t launch_attend_join(const AttendParams& p, int dtype, cudaStream_t stream) {
-  const long long q = (long long)p.rows * p.kv_heads * p.m;
-  PdlLaunch l(dim3((unsigned)((q + 3) / 4)), dim3(128), 0, stream);
+  PdlLaunch l(dim3((unsigned)(p.rows * p.kv_heads * p.m)), dim3(kJoinWarps * 32), 0, stream);
   if (dtype == DT_F32) return cudaLaunchKernelEx(&l.cfg, attend_join_kernel<DT_F32>, p);
   if (dtype == DT_F16) return cudaLaunchKernelEx(&l.cfg, attend_join_kernel<DT_F16>, p);
   return cudaLaunchKernelEx(&l.cfg, attend_join_kernel<DT_BF16>, p);

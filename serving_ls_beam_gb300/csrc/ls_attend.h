@@ -56,7 +56,7 @@ struct AttendParams {
   float2* part_ml;        // [problem, m, split]: maximum (log2 units) and sum
   long long items;        // rows * kv_heads * m_tiles * splits
   // item = ((row * kv_heads + head) * m_tiles + tile) * splits + split; query = token * group + head
-  AtDivisor by_split, by_tile, by_head, by_group, by_q_len;
+  AtDivisor by_split, by_tile, by_head, by_group, by_q_len, by_m;
   long long spin_limit_ns;
   int negate;             // attend_tc.cu: scale_log2 is its absolute value, the sign goes into the queries
   // keys shared by all rows or heads (stride 0): their tensor maps have one row or head

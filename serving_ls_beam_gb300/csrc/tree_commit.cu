@@ -3,14 +3,13 @@
 //
 // Node 0 holds the token chosen by the step before; node i > 0 guesses the token after its
 // parent.  The model chose target[n] after node n, so a node is confirmed when its parent is
-// and token[i] == target[parent[i]].  Parents come before their children, so one pass over the
-// candidates in ascending order, taking each whose parent is the branch's last node so far,
-// walks the branch and takes the first of equal siblings.
+// and token[i] == target[parent[i]].  All nodes that agree with their parent's choice offer
+// themselves to it at once (the least index wins, which takes the first of equal siblings); the
+// branch then is a chase along the winners from the root, one shared-memory read a node.
 //
 // A CTA has one layer of one row, or a part of it where the trees are large and the rows few
 // (branches of very different lengths: the longest would otherwise set the time).  Each repeats
-// the walk (a few hundred bytes from L2, a loop over the candidates only), which costs less than
-// a launch for it, and copies its share of the accepted keys and values, 16 bytes per thread where
+// the walk (a few hundred bytes from L2 and that chase), which costs less than a launch for it, and copies its share of the accepted keys and values, 16 bytes per thread where
 // the layout allows, eight copies under way per thread.  Nothing of the rejected nodes is read
 // or written.
 #include "ls_device.cuh"
@@ -54,8 +53,7 @@ __device__ __forceinline__ void append(const CommitParams& p, const int* path, i
 }
 
 __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitParams p) {
-  __shared__ int par[kAtMaxNodes], want[kAtMaxNodes], path[kAtMaxNodes];
-  __shared__ unsigned fits[kAtMaxNodes / 32];
+  __shared__ int child[kAtMaxNodes], want[kAtMaxNodes], path[kAtMaxNodes];
   __shared__ int s_count;
   const int r = blockIdx.x, layer = blockIdx.y, part = blockIdx.z, tid = threadIdx.x, N = p.nodes;
   const bool lead = layer == 0 && part == 0;  // writes the row's results
@@ -64,32 +62,20 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
   if (tid < N) {
     pi = __ldg(p.parent + at + tid);
     tok = __ldg(p.token + at + tid);
-    par[tid] = pi;
+    child[tid] = kAtMaxNodes;
     want[tid] = __ldg(p.target + at + tid);
   }
   const int len = __ldg(p.cache_len + r);
   const bool done = p.finished && p.finished[r];
   __syncthreads();
-  const bool ok = tid < N && pi >= 0 && pi < tid && tok == want[pi >= 0 && pi < N ? pi : 0] && tok != p.eos;
-  const unsigned b = __ballot_sync(~0u, ok);
-  if ((tid & 31) == 0 && tid < kAtMaxNodes) fits[tid >> 5] = b;
+  if (tid < N && pi >= 0 && pi < tid && tok == want[pi] && tok != p.eos) atomicMin(&child[pi], tid);
   __syncthreads();
   if (tid == 0) {
     const bool bad_len = len < 0 || len > p.max_len;
     const int room = bad_len ? 0 : p.max_len - len;
     int count = 0;
-    if (!done && par[0] == -1 && room > 0) {
-      path[count++] = 0;
-      int cur = 0;
-      for (int w = 0; w < kAtMaxNodes / 32; ++w) {
-        for (unsigned f = fits[w]; f && count < room; f &= f - 1) {
-          const int i = w * 32 + __ffs(f) - 1;
-          if (par[i] == cur) {
-            path[count++] = i;
-            cur = i;
-          }
-        }
-      }
+    if (!done && pi == -1 && room > 0) {
+      for (int cur = 0; cur < kAtMaxNodes && count < room; cur = child[cur]) path[count++] = cur;
     }
     s_count = count;
     if (lead) {
@@ -98,7 +84,7 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
       p.out_count[r] = count;
       p.out_token[r] = next;
       if (p.out_finished) p.out_finished[r] = done || (count > 0 && next == p.eos);
-      if (p.status && (bad_len || (!done && room == 0) || (!done && par[0] != -1))) atomicOr(p.status, kDevInternal);
+      if (p.status && (bad_len || (!done && room == 0) || (!done && pi != -1))) atomicOr(p.status, kDevInternal);
     }
   }
   __syncthreads();
