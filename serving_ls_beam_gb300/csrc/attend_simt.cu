@@ -11,6 +11,10 @@
 // MQ products of key n with the queries (read as broadcasts); the values are read from global
 // memory, where a warp reads a whole value vector at a time, lane d holding the outputs'
 // elements d, d + 32, ...  The warps' results are merged in shared memory at the end.
+//
+// It is the kernel that takes anything, bound by its shared-memory reads and by the values' latency:
+// the single-token step of 1024 beams of 64 positions takes 423 us here (0.08 of the copy rate), 47
+// in the kernel that such calls go to.
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"
 #include "ls_tree.cuh"

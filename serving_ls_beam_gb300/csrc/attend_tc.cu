@@ -30,6 +30,16 @@
 // accumulators and each writes half of the columns.  Three or four score buffers let scores run
 // ahead of the values, also into the next item.
 //
+// What bounds it:
+// - head size 128: the scores' products, which read 6 KB of shared memory per 64-key instruction
+//   (at its 128 bytes a clock 48 cycles, for 32 of tensor work).  509 queries over up to 2048
+//   states, 32 x 16 heads: 203 us, 1165 TFLOP/s, 0.61 of the measured bf16 rate;
+// - head size 64: the softmax's instructions (two warps a scheduler; per score half a multiply-add,
+//   an exponential, half an addition, half a conversion, half a maximum), then the turn from item
+//   to item.  400 queries over up to 1021 states, 24 x 16 heads: 64 us, 530 TFLOP/s;
+// - few queries over long rows: memory.  64 queries over 131000 positions, 8 heads: 537 MB in 86 us
+//   plus 4 us to join the parts, 0.88 of the measured copy rate.
+//
 // The accumulator is rescaled only when a query's maximum has grown by more than 2^8 since the
 // last time: until then its weights are at most 2^8 instead of 1, which f32 sums and the 16-bit
 // types hold without loss.  Every wait is bounded: one that runs out sets the timeout bit of the
@@ -59,7 +69,8 @@ struct TcShape {
   static constexpr int PANELS = DP / 64;
   // Keys of a tile.  512 columns of tensor memory hold the sums of both slots and the score
   // buffers: at 128 elements and 128 keys only two, and each job would wait for the products of
-  // the job before; at 64 keys four (measured below).
+  // the job before (509 queries over 2048 states: 234 us); at 64 keys four (220 us), although the
+  // scores' products then read the queries from shared memory twice as often.
   static constexpr int N = DP == 64 ? 128 : 64;
   static constexpr int NSB = DP == 64 ? 3 : 4;                 // score buffers
   static constexpr int NST = 4;                                // stages of either ring
