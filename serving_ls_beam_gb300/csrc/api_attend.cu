@@ -137,9 +137,10 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
                     : attend_simt_queries(dtype, p.m);
   p.m_tiles = (p.m + p.m_step - 1) / p.m_step;
   const long long whole = base * p.m_tiles;
+  // The tensor-core kernels take the scale's sign in the queries, and a scale of 0 as 2^-100: masked
+  // scores stay -inf, and every weight still is exactly 1.
+  if (tc || mma) p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
   if (tc) {
-    // a scale of 0 as 2^-100: masked scores stay -inf, and every weight still is exactly 1
-    p.scale_log2 = std::fmax(std::fabs(p.scale_log2), 0x1p-100f);
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
   } else if (mma || step) {
     p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole) ? 1 : 4;

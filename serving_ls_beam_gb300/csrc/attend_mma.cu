@@ -43,6 +43,7 @@ namespace {
 constexpr int kMmWarps = 4;
 constexpr int kMmThreads = kMmWarps * 32;
 constexpr long long kMmDrainNs = 2000000000LL;
+constexpr float kMmLazy = 8.0f;  // growth of the maximum (log2) that is let pass
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -188,13 +189,17 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
   const TreeSeen tree = tree_at(mine + sm.tree, p.nodes);
   const int chunks = p.dim / 8;
   const int kd = (p.dim + 15) / 16;  // 16-element steps of a head
+  const float c = p.scale_log2;      // positive: a negative scale is in Q's sign
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(base + sm.bars + 8 * i, 1);
     fence_barrier_init();
   }
   __syncwarp();
-  // of a block in panels of 64 elements: byte offset of 16-byte vector c of row r
+  // of a block in panels of 64 elements: byte offset of 16-byte vector c of row r.  The products'
+  // operands: a lane's offset for the first 16 elements; later ones differ in two bits of it.
   auto at = [&](int r, int c) { return (uint32_t)((c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
+  const uint32_t k_lane = at(lane & 15, lane >> 4), v_lane = at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+  const uint32_t flip = p.negate ? 0x80008000u : 0u;  // a negative scale: the queries' signs
   const int items = (int)p.items;
   const int stride = W == 1 ? (int)gridDim.x * kMmWarps : (int)gridDim.x;
   const int first = W == 1 ? (int)blockIdx.x * kMmWarps + warp : (int)blockIdx.x;
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
     f_slot = f_slot + 1 == NS ? 0 : f_slot + 1;
   };
 #pragma unroll 1
-  for (int i = 0; i < NS - 1; ++i) fill();
+  for (int i = 0; i < NS; ++i) fill();
 
   int slot = 0, seq = 0;
   uint32_t phases = 0;  // bit i: the parity that slot i's barrier completes next
@@ -289,14 +294,14 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
     bool open = true;
 #pragma unroll 1
     do {
-      cp_async_wait<NS - 2>();
+      cp_async_wait<NS - 1>();
       if (x.b >= 0 && x.b * KB + KB <= x.len) {
         // after a wait that ran out nothing is fetched or waited for any more; the loops just end
         const bool there = timed_out || mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns);
         timed_out |= !__all_sync(~0u, there);
         phases ^= 1u << slot;
       }
-      __syncwarp();  // every lane's copies of this stage are there, and all are done with the last one
+      __syncwarp();  // every lane's copies of this stage are there
       if (open) {
         open = false;
         if constexpr (S::QREG) {
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int q = a * 8 + g;
-                qf[a][kk][e] = q < x.nq ? lds32(qs + q * sm.q_row + (2 * kk + e) * 16 + t * 4) : 0u;
+                qf[a][kk][e] = (q < x.nq ? lds32(qs + q * sm.q_row + (2 * kk + e) * 16 + t * 4) : 0u) ^ flip;
               }
         }
         if (p.nodes) {
@@ -325,7 +330,6 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         }
         seq = seq + 1 == sets ? 0 : seq + 1;
       }
-      fill();
       const uint32_t ks = ring + slot * S::STAGE, vs = ks + S::PANELS * S::PANEL;
       const int n0 = max(x.b, 0) * KB;
       const int total = x.b < 0 ? 0 : x.len + p.nodes;
@@ -352,17 +356,16 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
               uint32_t f[4];
               const int q = a * 8 + (lane & 7) + (lane >> 4) * 8, c = 2 * kk + ((lane >> 3) & 1);
               ldsm4(f, qs + q * sm.q_row + c * 16);
-              qb[a][0] = f[0];
-              qb[a][1] = f[1];
-              qb[a + 1][0] = f[2];
-              qb[a + 1][1] = f[3];
+              qb[a][0] = f[0] ^ flip;
+              qb[a][1] = f[1] ^ flip;
+              qb[a + 1][0] = f[2] ^ flip;
+              qb[a + 1][1] = f[3] ^ flip;
             }
           }
 #pragma unroll
           for (int k = 0; k < KT; ++k) {
             uint32_t f[4];
-            const int row = k * 16 + (lane & 15), c = 2 * kk + (lane >> 4);
-            ldsm4(f, ks + at(row, c));
+            ldsm4(f, ((ks + k_lane) ^ ((kk & 3) << 5)) + (kk >> 2) * S::PANEL + k * 2048);
 #pragma unroll
             for (int a = 0; a < NQ; ++a) mma16816<BF>(s[k][a], f, qb[a][0], qb[a][1]);
           }
@@ -387,14 +390,9 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         __syncwarp();
       }
 
-      uint32_t pb[KT][NQ][2];
+      if (edge || dead_any) {
 #pragma unroll
-      for (int a = 0; a < NQ; ++a) {
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[k][a][e] *= p.scale_log2;
-        if (edge || dead_any) {
+        for (int a = 0; a < NQ; ++a)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool live = (alive >> (2 * a + e)) & 1u;
@@ -409,38 +407,53 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
                 if (!ok) s[k][a][2 * hf + e] = -INFINITY;
               }
           }
-        }
-        float sub[2], fct[2];
-        bool moved = false;
+      }
+      // The maximum is taken over the lanes, and the sums rescaled, only when some lane's own has
+      // grown by more than 2^8: until then weights are at most 2^8 instead of 1, which f32 sums and the
+      // 16-bit types hold without loss.
+      float top[NQ][2];
+      bool grown = false;
+#pragma unroll
+      for (int a = 0; a < NQ; ++a)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float bm = fmaxf(s[0][a][e], s[0][a][2 + e]);
+          top[a][e] = fmaxf(s[0][a][e], s[0][a][2 + e]);
 #pragma unroll
-          for (int k = 1; k < KT; ++k) bm = fmaxf(bm, fmaxf(s[k][a][e], s[k][a][2 + e]));
-          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 4));
-          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 8));
-          bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 16));
-          const float mn = fmaxf(m_run[a][e], bm);
-          moved |= mn > m_run[a][e];
-          sub[e] = mn == -INFINITY ? 0.0f : mn;
-          fct[e] = fast_exp2(m_run[a][e] - sub[e]);
-          m_run[a][e] = mn;
+          for (int k = 1; k < KT; ++k) top[a][e] = fmaxf(top[a][e], fmaxf(s[k][a][e], s[k][a][2 + e]));
+          grown |= top[a][e] * c > m_run[a][e] + kMmLazy;
         }
-        if (__any_sync(~0u, moved)) {
-          l_run[a][0] *= fct[0];
-          l_run[a][1] *= fct[1];
+      if (__any_sync(~0u, grown)) {
+#pragma unroll
+        for (int a = 0; a < NQ; ++a) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float bm = top[a][e];
+            bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 4));
+            bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 8));
+            bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 16));
+            const float mn = fmaxf(m_run[a][e], bm * c);
+            f[e] = fast_exp2(m_run[a][e] - (mn == -INFINITY ? 0.0f : mn));
+            m_run[a][e] = mn;
+            l_run[a][e] *= f[e];
+          }
 #pragma unroll
           for (int j = 0; j < DP / 16; ++j) {
-            o[j][a][0] *= fct[0];
-            o[j][a][1] *= fct[1];
-            o[j][a][2] *= fct[0];
-            o[j][a][3] *= fct[1];
+            o[j][a][0] *= f[0];
+            o[j][a][1] *= f[1];
+            o[j][a][2] *= f[0];
+            o[j][a][3] *= f[1];
           }
         }
+      }
+      uint32_t pb[KT][NQ][2];
+#pragma unroll
+      for (int a = 0; a < NQ; ++a) {
+        const float sub[2] = {m_run[a][0] == -INFINITY ? 0.0f : -m_run[a][0], m_run[a][1] == -INFINITY ? 0.0f : -m_run[a][1]};
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[k][a][e] = fast_exp2(s[k][a][e] - sub[e & 1]);
+          for (int e = 0; e < 4; ++e) s[k][a][e] = fast_exp2(fmaf(s[k][a][e], c, sub[e & 1]));
           l_run[a][0] += s[k][a][0] + s[k][a][2];
           l_run[a][1] += s[k][a][1] + s[k][a][3];
           pb[k][a][0] = transpose8(pack2<BF>(s[k][a][0], s[k][a][1]));
@@ -455,13 +468,14 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
 #pragma unroll
           for (int k = 0; k < KT; ++k) {
             uint32_t f[4];
-            const int row = k * 16 + (lane & 7) + (lane >> 4) * 8, c = 2 * j + ((lane >> 3) & 1);
-            ldsm4_trans(f, vs + at(row, c));
+            ldsm4_trans(f, ((vs + v_lane) ^ ((j & 3) << 5)) + (j >> 2) * S::PANEL + k * 2048);
 #pragma unroll
             for (int a = 0; a < NQ; ++a) mma16816<BF>(o[j][a], f, pb[k][a][0], pb[k][a][1]);
           }
         }
       }
+      __syncwarp();  // all lanes are done with this stage
+      fill();
       slot = slot + 1 == NS ? 0 : slot + 1;
       if (x.b >= 0) x.b += W;
     } while (x.b >= 0 && x.b < x.b_end);

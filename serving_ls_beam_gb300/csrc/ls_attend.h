@@ -58,7 +58,7 @@ struct AttendParams {
   // item = ((row * kv_heads + head) * m_tiles + tile) * splits + split; query = token * group + head
   AtDivisor by_split, by_tile, by_head, by_group, by_q_len, by_m;
   long long spin_limit_ns;
-  int negate;             // attend_tc.cu: scale_log2 is its absolute value, the sign goes into the queries
+  int negate;             // tensor-core kernels: scale_log2 is its absolute value, the sign goes into the queries
   // keys shared by all rows or heads (stride 0): their tensor maps have one row or head
   int kv_row_one, kv_head_one;
   int q_tma;              // attend_tc.cu: the queries' tensor map is there
