@@ -45,14 +45,21 @@ bool shape_ok(int rows, int k, int q_len, int heads, int kv_heads, int max_len, 
          dim >= 1 && dim <= kAtMaxDim;
 }
 
+// Queries that read the same keys; INT64_MAX where the count does not fit 31 bits.
+long long queries_per_key(int k, int q_len, int group) {
+  const long long tokens = (long long)k * q_len;
+  return tokens > INT_MAX ? INT64_MAX : tokens * group;
+}
+
 size_t workspace_size(int rows, int k, int q_len, int heads, int kv_heads, int max_len, int dim) {
   if (!shape_ok(rows, k, q_len, heads, kv_heads, max_len, dim)) return 0;
-  const long long m = (long long)k * q_len * (heads / kv_heads);
+  const long long m = queries_per_key(k, q_len, heads / kv_heads);
   if (m > INT_MAX) return 0;
   return kAtHeader + (size_t)attend_part_rows((int)m) * (size_t)(dim + 2) * 4;
 }
 
-// Parts of each row's keys so that about `ctas` CTAs run, each with `least` keys or more.
+// Parts of each row's keys so that about `ctas` CTAs run, each with `least` keys or more (below that
+// the launch that joins them, some 2 us, costs more than the parts save).
 int split_of(const AttendParams& p, long long base, long long ctas, int least, int forced) {
   long long s = forced > 0 ? forced : ctas / (base > 0 ? base : 1);
   const long long by_len = ((long long)p.max_len + p.nodes + least - 1) / least;
@@ -144,7 +151,9 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
   } else if (mma || step) {
     p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole) ? 1 : 4;
-    p.splits = p.warps == 1 ? 1 : split_of(p, whole, (mma ? 2 : 4) * kAtSms, mma ? 256 : 128, dbg.splits);
+    // as many CTAs as the GPU holds at once
+    const int held = step ? 4 : p.dim <= 64 || (p.dim <= 128 && p.m <= 8) ? 3 : p.dim <= 128 ? 2 : 1;
+    p.splits = p.warps == 1 ? 1 : split_of(p, whole, held * kAtSms, mma ? 512 : 256, dbg.splits);
   } else {
     p.splits = split_of(p, whole, 4 * kAtSms, 128, dbg.splits);
   }
@@ -202,7 +211,7 @@ ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view
   if (!known(dtype) || !shape_ok(batch, k, q_len, heads, kv_heads, max_src, head_dim) || !std::isfinite(scale))
     return LS_ERR_INVALID_ARG;
   if (batch == 0 || q_len == 0) return LS_OK;
-  const long long m = (long long)k * q_len * (heads / kv_heads);
+  const long long m = queries_per_key(k, q_len, heads / kv_heads);
   if ((long long)batch * k > INT_MAX || m > INT_MAX) return LS_ERR_UNSUPPORTED;
   const int es = es_of(dtype);
   if (!view_ok(q, es, false, 1, batch * k, q_len, heads) ||

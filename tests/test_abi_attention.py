@@ -60,6 +60,8 @@ def test_cross_refusals(lsb):
     assert call(out=view(lsb, row=0)) == E and call(out=view(lsb, head=0)) == E
     assert call(b=0) == 0 and call(t=0) == 0
     assert call(b=1 << 30, k=8) == UNSUPPORTED
+    assert call(b=1, k=1 << 30, t=1 << 30, h=8, hk=1) == UNSUPPORTED  # queries that no 64-bit product holds
+    assert lsb.ls_cross_attention_workspace_size(1, 1 << 30, 1 << 30, 1 << 10, 1, 5, 64) == 0
 
 
 def test_tree_refusals(lsb):
