@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
   MmaItem fx{};
   int f_len = fi < items ? __ldg(p.len + item_row(p, fi)) : 0;
   bool timed_out = false;
+  uint32_t pending = 0;  // bit i: a TMA copy into slot i is under way
   auto fill = [&]() {
     if (fi < items && !timed_out) {
       if (f_new) {
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
       }
       const uint32_t kd_ = ring + f_slot * S::STAGE, vd_ = kd_ + S::PANELS * S::PANEL;
       if (fx.b >= 0 && fx.b * KB + KB <= fx.len) {
+        pending |= 1u << f_slot;
         if (lane == 0) {
           const uint32_t bar = base + sm.bars + 8 * f_slot;
           const int h = p.kv_head_one ? 0 : fx.h, r = p.kv_row_one ? 0 : fx.r;
@@ -295,11 +297,14 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
 #pragma unroll 1
     do {
       cp_async_wait<NS - 1>();
-      if (x.b >= 0 && x.b * KB + KB <= x.len) {
-        // after a wait that ran out nothing is fetched or waited for any more; the loops just end
-        const bool there = timed_out || mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns);
-        timed_out |= !__all_sync(~0u, there);
-        phases ^= 1u << slot;
+      // after a wait that ran out nothing is fetched or waited for any more; the loops just end
+      if (((pending >> slot) & 1u) && !timed_out) {
+        if (__all_sync(~0u, mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns))) {
+          phases ^= 1u << slot;
+          pending ^= 1u << slot;
+        } else {
+          timed_out = true;
+        }
       }
       __syncwarp();  // every lane's copies of this stage are there
       if (open) {
@@ -581,7 +586,8 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
   }
   if (timed_out && lane == 0) atomicOr(p.status, kDevTimeout);
   if (timed_out) {  // every copy lands before the CTA may exit
-    for (int i = 0; i < NS; ++i) mbar_wait_bounded(base + sm.bars + 8 * i, ((phases >> i) & 1u) ^ 1u, kMmDrainNs);
+    for (int i = 0; i < NS; ++i)
+      if ((pending >> i) & 1u) mbar_wait_bounded(base + sm.bars + 8 * i, (phases >> i) & 1u, kMmDrainNs);
   }
   cp_async_wait<0>();
 }

@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     __syncwarp();
     return true;
   };
-  // After a wait that ran out: the ring's copies up to number n land before the CTA may exit.
+  // The ring's copies up to number n land before the CTA may exit (after a run without a lapsed wait
+  // they have; after one of another role's they may not).
   auto drain = [&](int n, int slots, int full) {
     for (int g = max(0, n - slots); g < n; ++g) mbar_wait_bounded(bar(full + g % slots), (uint32_t)(g / slots) & 1u, kTaDrainNs);
   };
@@ -625,10 +626,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (ok) kn = w.tile + t + 1;
       }
     }
-    if (!ok) {
-      drain(kn, NST, S::B_KF);
-      drain(qn, NQB, S::B_QF);
-    }
+    drain(kn, NST, S::B_KF);
+    drain(qn, NQB, S::B_QF);
   } else if (warp == 9) {
     // ---------------------------------------------------------------- scores
     const uint64_t q0 = desc_k(base + S::Q), k0 = desc_k(base + S::K);
@@ -717,7 +716,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (ok) vn = w.tile + t + 1;
       }
     }
-    if (!ok) drain(vn, NST, S::B_VF);
+    drain(vn, NST, S::B_VF);
   }
   }
   __syncthreads();
