@@ -297,9 +297,11 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
 #pragma unroll 1
     do {
       cp_async_wait<NS - 1>();
-      // after a wait that ran out nothing is fetched or waited for any more; the loops just end
+      // After a wait that ran out nothing is fetched or waited for any more; the loops just end.  A limit
+      // of zero is one that has run out at the first wait, whether or not its copies are there already.
       if (((pending >> slot) & 1u) && !timed_out) {
-        if (__all_sync(~0u, mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns))) {
+        const bool there = p.spin_limit_ns > 0 && mbar_wait_bounded(base + sm.bars + 8 * slot, (phases >> slot) & 1u, p.spin_limit_ns);
+        if (__all_sync(~0u, there)) {
           phases ^= 1u << slot;
           pending ^= 1u << slot;
         } else {
