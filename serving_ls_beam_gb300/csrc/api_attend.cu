@@ -106,6 +106,9 @@ bool tcgen05_pays(const AttendParams& p, long long problems) {
   return keys * ((p.m + 31) / 32) > 320;
 }
 
+// Whether the tiled f32 kernel takes a call and not the streaming one.
+bool tile_pays(const AttendParams& p) { return p.m > (p.dim > 128 ? 4 : 8); }
+
 // Whether a warp takes whole rows in the kernels that stream keys per warp (the other way is four
 // warps to a row or a part of it): many rows, each of a few of a warp's blocks.  In us, one warp /
 // four: 1500 rows of head 64 and 4 queries, 128 keys 15 / 20, 256 20 / 25, 512 32 / 34; of head 128,
@@ -136,10 +139,13 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   CUtensorMap maps[5];
   const bool tc = tensor && p.dim <= kAtTcDim && p.max_len > 0 &&
                   (dbg.kernel ? dbg.kernel == kAtForceTc : tcgen05_pays(p, base)) && encode_maps(maps, p, dtype);
-  const bool step = lines && dtype == LS_DTYPE_F32 && p.dim <= kAtStepDim && dbg.kernel != kAtForceSimt;
+  const bool f32 = lines && dtype == LS_DTYPE_F32 && dbg.kernel != kAtForceSimt;
+  const bool tile = f32 && (dbg.kernel ? dbg.kernel == kAtForceTc : tile_pays(p));
+  const bool step = f32 && !tile;
   const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt && maps_describe(p);
   p.m_step = tc     ? 2 * kAtTcSlot
-             : step ? attend_step_queries(p.m)
+             : tile ? attend_tile_queries(p.dim, p.m)
+             : step ? attend_step_queries(p.dim, p.m)
              : mma  ? attend_mma_queries(p.dim, p.m)
                     : attend_simt_queries(dtype, p.m);
   p.m_tiles = (p.m + p.m_step - 1) / p.m_step;
@@ -154,6 +160,8 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
     // as many CTAs as the GPU holds at once
     const int held = step ? 4 : p.dim <= 64 || (p.dim <= 128 && p.m <= 8) ? 3 : p.dim <= 128 ? 2 : 1;
     p.splits = p.warps == 1 ? 1 : split_of(p, whole, held * kAtSms, mma ? 512 : 256, dbg.splits);
+  } else if (tile) {
+    p.splits = split_of(p, whole, attend_tile_ctas(p.dim, p.m) * kAtSms, 128, dbg.splits);
   } else {
     p.splits = split_of(p, whole, 4 * kAtSms, 128, dbg.splits);
   }
@@ -166,6 +174,7 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   p.by_q_len.set(p.q_len);
   p.by_m.set(p.m);
   cudaError_t e = tc    ? launch_attend_tc(maps, p, dtype, stream)
+                  : tile ? launch_attend_tile(p, stream)
                   : step ? launch_attend_step(p, stream)
                   : mma ? launch_attend_mma(p, dtype, stream)
                         : launch_attend_simt(p, dtype, stream);

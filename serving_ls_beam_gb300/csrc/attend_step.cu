@@ -42,43 +42,40 @@ __device__ __forceinline__ uint4 pack_vec(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// The 8 values of each lane summed over the lanes that differ in bits 0 to 2 (and up to LPK):
-// afterwards lane l holds the sum of value (l & 1) << 2 | (l & 2) | (l >> 2 & 1).
-template <int LPK>
-__device__ __forceinline__ float reduce8(const float (&v)[8], int lane) {
-  float a[4], b[2], c;
+// The N values (8 or 4) of each lane summed over the lanes that differ in the bits below LPK: afterwards
+// lane l holds the sum of value (l & 1) << 2 | (l & 2) | (l >> 2 & 1), of four (l & 1) << 1 | (l >> 1 & 1).
+template <int LPK, int N>
+__device__ __forceinline__ float reduce_values(const float (&v)[N], int lane) {
+  float a[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool hi = lane & 1;
-    const float keep = hi ? v[i + 4] : v[i], give = hi ? v[i] : v[i + 4];
-    a[i] = keep + __shfl_xor_sync(~0u, give, 1);
+  for (int i = 0; i < N; ++i) a[i] = v[i];
+#pragma unroll
+  for (int x = 1, left = N / 2; left; x <<= 1, left >>= 1) {
+    const bool hi = lane & x;
+#pragma unroll
+    for (int i = 0; i < left; ++i) {
+      const float keep = hi ? a[i + left] : a[i], give = hi ? a[i] : a[i + left];
+      a[i] = keep + __shfl_xor_sync(~0u, give, x);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool hi = lane & 2;
-    const float keep = hi ? a[i + 2] : a[i], give = hi ? a[i] : a[i + 2];
-    b[i] = keep + __shfl_xor_sync(~0u, give, 2);
-  }
-  {
-    const bool hi = lane & 4;
-    const float keep = hi ? b[1] : b[0], give = hi ? b[0] : b[1];
-    c = keep + __shfl_xor_sync(~0u, give, 4);
-  }
-#pragma unroll
-  for (int x = 8; x < LPK; x <<= 1) c += __shfl_xor_sync(~0u, c, x);
-  return c;
+  for (int x = N; x < LPK; x <<= 1) a[0] += __shfl_xor_sync(~0u, a[0], x);
+  return a[0];
 }
 
-template <int LPK, int MQ>
-__global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kernel(const AttendParams p) {
-  constexpr int DT = DT_F32, E = 4, ES = 4, U = kAsLoads, KPL = 32 / LPK, KB = U * KPL;
+template <int LPK, int V, int MQ>
+__global__ void __launch_bounds__(kAsThreads, MQ * V <= 2 ? 4 : 1) attend_step_kernel(const AttendParams p) {
+  constexpr int DT = DT_F32, E = 4, EV = E * V, ES = 4, U = kAsLoads / V, KPL = 32 / LPK, KB = U * KPL;
+  constexpr int STEP = LPK * E;  // elements from one of a lane's vectors to its next
   __shared__ unsigned long long trees[kAsWarps][kAtMaxNodes * 12 / 8];
   __shared__ float wm[kAsWarps][MQ], wl[kAsWarps][MQ];
-  __shared__ float acc[kAsWarps][MQ][LPK * E + 4];
+  __shared__ float acc[kAsWarps][MQ][STEP * V + 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPK, gk = lane / LPK;
   const int W = p.warps, wi = W == 1 ? 0 : warp;
-  const bool cv = c < p.dim / E;  // this lane holds a part of the vectors
-  const int my_u = (lane & 1) << 2 | (lane & 2) | (lane >> 2 & 1);
+  bool cv[V];  // this lane holds a part of the vectors
+#pragma unroll
+  for (int v = 0; v < V; ++v) cv[v] = c + LPK * v < p.dim / E;
+  const int my_u = U == 8 ? (lane & 1) << 2 | (lane & 2) | (lane >> 2 & 1) : (lane & 1) << 1 | (lane >> 1 & 1);
   const TreeSeen tree = tree_at(trees[warp], kAtMaxNodes);
   const int items = (int)p.items, stride = W == 1 ? (int)gridDim.x * kAsWarps : (int)gridDim.x;
   int it = W == 1 ? (int)blockIdx.x * kAsWarps + warp : (int)blockIdx.x;
@@ -98,35 +95,44 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
     const unsigned char* vb = p.value.data + (long long)r * p.value.row + (long long)h * p.value.head + c * 16;
     const unsigned char* dkb = p.dkey.data + (long long)r * p.dkey.row + (long long)h * p.dkey.head + c * 16;
     const unsigned char* dvb = p.dvalue.data + (long long)r * p.dvalue.row + (long long)h * p.dvalue.head + c * 16;
-    auto fetch = [&](uint4(&d)[U], int blk, const unsigned char* cache, uint32_t pos, const unsigned char* draft,
+    auto fetch = [&](uint4(&d)[U][V], int blk, const unsigned char* cache, uint32_t pos, const unsigned char* draft,
                      long long dpos) {
       const int j0 = blk * KB + gk;
       if (blk * KB + KB <= len) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          d[u] = cv ? load_stream(cache + (unsigned long long)(uint32_t)(j0 + u * KPL) * pos) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            d[u][v] = cv[v] ? load_stream(cache + (unsigned long long)(uint32_t)(j0 + u * KPL) * pos + v * STEP * ES)
+                            : make_uint4(0u, 0u, 0u, 0u);
       } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int j = j0 + u * KPL;
           const unsigned char* at = j < len ? cache + (unsigned long long)(uint32_t)j * pos : draft + (long long)(j - len) * dpos;
-          d[u] = cv && j < total && blk < hi ? load_stream(at) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            d[u][v] = cv[v] && j < total && blk < hi ? load_stream(at + v * STEP * ES) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
     };
-    uint4 kr[U], vr[U];
+    uint4 kr[U][V], vr[U][V];
     if (b < hi) {
       fetch(kr, b, kb, (uint32_t)p.key.pos, dkb, p.dkey.pos);
       fetch(vr, b, vb, (uint32_t)p.value.pos, dvb, p.dvalue.pos);
     }
-    float q[MQ][E];
+    float q[MQ][EV];
 #pragma unroll
     for (int j = 0; j < MQ; ++j) {
       const unsigned char* src = p.q.data + query_offset(p, p.q, r, h, i0 + min(j, nq - 1)) + c * 16;
-      const uint4 d = cv ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
-      unpack<DT>(d, q[j]);
 #pragma unroll
-      for (int x = 0; x < E; ++x) q[j][x] *= p.scale_log2;
+      for (int v = 0; v < V; ++v) {
+        const uint4 d = cv[v] ? __ldg(reinterpret_cast<const uint4*>(src + v * STEP * ES)) : make_uint4(0u, 0u, 0u, 0u);
+        float x4[E];
+        unpack<DT>(d, x4);
+#pragma unroll
+        for (int x = 0; x < E; ++x) q[j][v * E + x] = x4[x] * p.scale_log2;
+      }
     }
     unsigned alive = ~0u;
     if (p.nodes) {
@@ -138,25 +144,31 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
       for (int j = 0; j < MQ; ++j)
         if (j < nq && tree.mask[p.by_group(i0 + j)]) alive |= 1u << j;
     }
-    float m[MQ], l[MQ], o[MQ][E];
+    float m[MQ], l[MQ], o[MQ][EV];
 #pragma unroll
     for (int j = 0; j < MQ; ++j) {
       m[j] = -INFINITY;
       l[j] = 0.0f;
 #pragma unroll
-      for (int x = 0; x < E; ++x) o[j][x] = 0.0f;
+      for (int x = 0; x < EV; ++x) o[j][x] = 0.0f;
     }
     for (; b < hi; b += W) {
       float part[MQ][U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float k[E];
-        unpack<DT>(kr[u], k);
+        float k[EV];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float x4[E];
+          unpack<DT>(kr[u][v], x4);
+#pragma unroll
+          for (int x = 0; x < E; ++x) k[v * E + x] = x4[x];
+        }
 #pragma unroll
         for (int j = 0; j < MQ; ++j) {
           float2 a = __fmul2_rn(make_float2(q[j][0], q[j][1]), make_float2(k[0], k[1]));
 #pragma unroll
-          for (int x = 2; x < E; x += 2) a = __ffma2_rn(make_float2(q[j][x], q[j][x + 1]), make_float2(k[x], k[x + 1]), a);
+          for (int x = 2; x < EV; x += 2) a = __ffma2_rn(make_float2(q[j][x], q[j][x + 1]), make_float2(k[x], k[x + 1]), a);
           part[j][u] = a.x + a.y;
         }
       }
@@ -166,7 +178,7 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
       float w[MQ];
 #pragma unroll
       for (int j = 0; j < MQ; ++j) {
-        float s = reduce8<LPK>(part[j], lane);
+        float s = reduce_values<LPK>(part[j], lane);
         bool sees = (alive >> j) & 1u;
         if (edge) {
           if (key >= len) sees = sees && key < total && (tree.mask[p.by_group(i0 + min(j, nq - 1))] >> (key - len) & 1ull);
@@ -174,7 +186,7 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
         s = sees ? s : -INFINITY;
         float bm = s;
 #pragma unroll
-        for (int x = 1; x < 8; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, x));
+        for (int x = 1; x < U; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, x));
 #pragma unroll
         for (int x = LPK; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, x));
         const float mn = fmaxf(m[j], bm), sub = mn == -INFINITY ? 0.0f : mn;
@@ -183,24 +195,26 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
           const float f = fast_exp2(m[j] - sub);
           l[j] *= f;
 #pragma unroll
-          for (int x = 0; x < E; ++x) o[j][x] *= f;
+          for (int x = 0; x < EV; ++x) o[j][x] *= f;
           m[j] = mn;
         }
         l[j] += w[j];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float v[E];
-        unpack<DT>(vr[u], v);
-        const int from = gk * LPK + ((u >> 2) | (u & 2) | (u & 1) << 2);
+        float y4[V][E];
+#pragma unroll
+        for (int v = 0; v < V; ++v) unpack<DT>(vr[u][v], y4[v]);
+        const int from = gk * LPK + (U == 8 ? (u >> 2) | (u & 2) | (u & 1) << 2 : (u >> 1) | (u & 1) << 1);
 #pragma unroll
         for (int j = 0; j < MQ; ++j) {
           const float wu = __shfl_sync(~0u, w[j], from);
           // a drafted value that the query does not see may be anything: left out, not times 0
           if (!edge || wu != 0.0f) {
 #pragma unroll
-            for (int x = 0; x < E; x += 2) {
-              const float2 y = __ffma2_rn(make_float2(wu, wu), make_float2(v[x], v[x + 1]), make_float2(o[j][x], o[j][x + 1]));
+            for (int x = 0; x < EV; x += 2) {
+              const float2 y = __ffma2_rn(make_float2(wu, wu), make_float2(y4[x / E][x % E], y4[x / E][x % E + 1]),
+                                          make_float2(o[j][x], o[j][x + 1]));
               o[j][x] = y.x;
               o[j][x + 1] = y.y;
             }
@@ -213,23 +227,27 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
 #pragma unroll
     for (int j = 0; j < MQ; ++j) {
 #pragma unroll
-      for (int x = 1; x < 8; x <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], x);
+      for (int x = 1; x < U; x <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], x);
 #pragma unroll
       for (int x = LPK; x < 32; x <<= 1) {
         l[j] += __shfl_xor_sync(~0u, l[j], x);
 #pragma unroll
-        for (int y = 0; y < E; ++y) o[j][y] += __shfl_xor_sync(~0u, o[j][y], x);
+        for (int y = 0; y < EV; ++y) o[j][y] += __shfl_xor_sync(~0u, o[j][y], x);
       }
     }
     if (W == 1) {  // never split
 #pragma unroll
       for (int j = 0; j < MQ; ++j) {
-        if (j < nq && gk == j % KPL && cv) {
-          float y[E];
+        if (j < nq && gk == j % KPL) {
           const float inv = l[j] == 0.0f ? 0.0f : 1.0f / l[j];
+          unsigned char* to = p.out.data + query_offset(p, p.out, r, h, i0 + j) + c * 16;
 #pragma unroll
-          for (int x = 0; x < E; ++x) y[x] = l[j] == 0.0f ? 0.0f : o[j][x] * inv;
-          *reinterpret_cast<uint4*>(p.out.data + query_offset(p, p.out, r, h, i0 + j) + c * 16) = pack_vec(y);
+          for (int v = 0; v < V; ++v) {
+            float y[E];
+#pragma unroll
+            for (int x = 0; x < E; ++x) y[x] = l[j] == 0.0f ? 0.0f : o[j][v * E + x] * inv;
+            if (cv[v]) *reinterpret_cast<uint4*>(to + v * STEP * ES) = pack_vec(y);
+          }
         }
       }
     } else {
@@ -241,8 +259,9 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
         }
         if (gk == j % KPL) {
 #pragma unroll
-          for (int x = 0; x < E; x += 4)
-            *reinterpret_cast<float4*>(&acc[warp][j][c * E + x]) = make_float4(o[j][x], o[j][x + 1], o[j][x + 2], o[j][x + 3]);
+          for (int v = 0; v < V; ++v)
+            *reinterpret_cast<float4*>(&acc[warp][j][c * E + v * STEP]) =
+                make_float4(o[j][v * E], o[j][v * E + 1], o[j][v * E + 2], o[j][v * E + 3]);
         }
       }
       __syncthreads();
@@ -279,38 +298,41 @@ __global__ void __launch_bounds__(kAsThreads, MQ <= 2 ? 4 : 1) attend_step_kerne
   }
 }
 
-template <int LPK, int MQ>
+template <int LPK, int V, int MQ>
 cudaError_t run_step(const AttendParams& p, cudaStream_t stream) {
   long long grid = p.items;
   if (p.warps == 1) {
     static std::atomic<uint64_t> known{0};
     int occ = 0;
-    const cudaError_t e = resident_ctas(attend_step_kernel<LPK, MQ>, kAsThreads, 0, known, &occ);
+    const cudaError_t e = resident_ctas(attend_step_kernel<LPK, V, MQ>, kAsThreads, 0, known, &occ);
     if (e != cudaSuccess) return e;
     const long long need = (p.items + kAsWarps - 1) / kAsWarps, fit = (long long)kAtSms * occ;
     grid = need < fit ? need : fit;
   }
-  attend_step_kernel<LPK, MQ><<<(unsigned)grid, kAsThreads, 0, stream>>>(p);
+  attend_step_kernel<LPK, V, MQ><<<(unsigned)grid, kAsThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int LPK>
 cudaError_t run_step_queries(const AttendParams& p, cudaStream_t stream) {
-  switch (attend_step_queries(p.m)) {
-    case 1: return run_step<LPK, 1>(p, stream);
-    case 2: return run_step<LPK, 2>(p, stream);
-    case 4: return run_step<LPK, 4>(p, stream);
-    default: return run_step<LPK, 8>(p, stream);
+  switch (p.m_step) {
+    case 1: return run_step<LPK, 1, 1>(p, stream);
+    case 2: return run_step<LPK, 1, 2>(p, stream);
+    case 4: return run_step<LPK, 1, 4>(p, stream);
+    default: return run_step<LPK, 1, 8>(p, stream);
   }
 }
 
 }  // namespace
 
-int attend_step_queries(int m) { return m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 ? 4 : 8; }
+int attend_step_queries(int dim, int m) { return m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 || dim > 128 ? 4 : 8; }
 
 cudaError_t launch_attend_step(const AttendParams& p, cudaStream_t stream) {
   if (p.dim <= 32) return run_step_queries<8>(p, stream);
-  return p.dim <= 64 ? run_step_queries<16>(p, stream) : run_step_queries<32>(p, stream);
+  if (p.dim <= 64) return run_step_queries<16>(p, stream);
+  if (p.dim <= 128) return run_step_queries<32>(p, stream);
+  if (p.m_step == 1) return run_step<32, 2, 1>(p, stream);
+  return p.m_step == 2 ? run_step<32, 2, 2>(p, stream) : run_step<32, 2, 4>(p, stream);
 }
 
 }  // namespace lsb
