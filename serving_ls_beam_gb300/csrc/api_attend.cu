@@ -106,8 +106,11 @@ bool tcgen05_pays(const AttendParams& p, long long problems) {
   return keys * ((p.m + 31) / 32) > 320;
 }
 
-// Whether the tiled f32 kernel takes a call and not the streaming one.
-bool tile_pays(const AttendParams& p) { return p.m > (p.dim > 128 ? 4 : 8); }
+// Whether the tiled f32 kernel takes a call and not the streaming one, which reads the keys anew for
+// every eight (above head 128 four) queries.  In us, streaming / tiled: 800 problems of head 64, 200 to
+// 500 positions, 8 queries 67 / 86, 12 queries 114 / 79; of head 128, 6 queries 118 / 143, 16 queries
+// 204 / 140; 1024 of head 256, 300 to 700 positions, 8 queries 417 / 442, 12 queries 592 / 445.
+bool tile_pays(const AttendParams& p) { return p.m > 8; }
 
 // Whether a warp takes whole rows in the kernels that stream keys per warp (the other way is four
 // warps to a row or a part of it): many rows, each of a few of a warp's blocks.  In us, one warp /
@@ -144,7 +147,7 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   const bool step = f32 && !tile;
   const bool mma = tensor && !tc && dbg.kernel != kAtForceSimt && maps_describe(p);
   p.m_step = tc     ? 2 * kAtTcSlot
-             : tile ? attend_tile_queries(p.dim, p.m)
+             : tile ? attend_tile_queries(p.m)
              : step ? attend_step_queries(p.dim, p.m)
              : mma  ? attend_mma_queries(p.dim, p.m)
                     : attend_simt_queries(dtype, p.m);
@@ -157,11 +160,14 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
   } else if (mma || step) {
     p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole) ? 1 : 4;
-    // as many CTAs as the GPU holds at once
+    // As many CTAs as the GPU holds at once; in f32, where rows of different lengths cost more than
+    // joining up to 64 parts, twice as many (37 trees of 6 nodes, 321 to 2357 positions: 170 -> 156 us;
+    // but one row of 86753, 76 parts 145 us and 152 parts 172 us), and three times in the tiled kernel
+    // (3 trees of 32 nodes, up to 4378 positions: 97 -> 78 us).
     const int held = step ? 4 : p.dim <= 64 || (p.dim <= 128 && p.m <= 8) ? 3 : p.dim <= 128 ? 2 : 1;
-    p.splits = p.warps == 1 ? 1 : split_of(p, whole, held * kAtSms, mma ? 512 : 256, dbg.splits);
+    p.splits = p.warps == 1 ? 1 : split_of(p, whole, (step && 2 * held * kAtSms <= 64 * whole ? 2 : 1) * held * kAtSms, mma ? 512 : 256, dbg.splits);
   } else if (tile) {
-    p.splits = split_of(p, whole, attend_tile_ctas(p.dim, p.m) * kAtSms, 128, dbg.splits);
+    p.splits = split_of(p, whole, 3 * attend_tile_ctas(p.dim, p.m) * kAtSms, 128, dbg.splits);
   } else {
     p.splits = split_of(p, whole, 4 * kAtSms, 128, dbg.splits);
   }

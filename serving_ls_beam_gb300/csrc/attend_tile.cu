@@ -31,8 +31,7 @@ struct TileShape {
   static constexpr int ROW = DP + 4, PROW = BN + 4;  // floats
   static constexpr int K = BM * ROW, V = K + BN * ROW, P = V + BN * DP, FLOATS = P + BM * PROW;
   static constexpr int BYTES = FLOATS * 4;
-  static constexpr int MOST = TQ == 2 ? 4 : 3;  // by registers
-  static constexpr int CTAS = 232448 / (BYTES + 2048) < MOST ? 232448 / (BYTES + 2048) : MOST;  // per SM
+  static constexpr int FIT = 232448 / (BYTES + 2048), CTAS = FIT < 5 ? FIT : 5;  // per SM
 };
 
 template <int DP, int TQ, int TK>
@@ -260,24 +259,19 @@ cudaError_t run_tile(const AttendParams& p, cudaStream_t stream) {
 
 template <int DP, int TK>
 cudaError_t run_tile_queries(const AttendParams& p, cudaStream_t stream) {
-  if (p.m_step == 16) return run_tile<DP, 2, TK>(p, stream);
-  if constexpr (DP <= 128) {
-    if (p.m_step == 64) return run_tile<DP, 8, TK>(p, stream);
-  }
-  return run_tile<DP, 4, TK>(p, stream);
+  return p.m_step == 16 ? run_tile<DP, 2, TK>(p, stream) : run_tile<DP, 4, TK>(p, stream);
 }
 template <int DP, int TK>
 int tile_ctas(int queries) {
-  if (queries == 16) return TileShape<DP, 2, TK>::CTAS;
-  return queries == 32 ? TileShape<DP, 4, TK>::CTAS : TileShape<DP, 8, TK>::CTAS;
+  return queries == 16 ? TileShape<DP, 2, TK>::CTAS : TileShape<DP, 4, TK>::CTAS;
 }
 
 }  // namespace
 
-int attend_tile_queries(int dim, int m) { return m <= 16 ? 16 : m <= 32 || dim > 128 ? 32 : 64; }
+int attend_tile_queries(int m) { return m <= 16 ? 16 : 32; }
 
 int attend_tile_ctas(int dim, int m) {
-  const int q = attend_tile_queries(dim, m);
+  const int q = attend_tile_queries(m);
   if (dim <= 32) return tile_ctas<32, 4>(q);
   if (dim <= 64) return tile_ctas<64, 4>(q);
   if (dim <= 96) return tile_ctas<96, 4>(q);

@@ -127,7 +127,7 @@ cudaError_t launch_attend_step(const AttendParams& p, cudaStream_t stream);
 int attend_step_queries(int dim, int m);  // queries per item
 // f32, every stride and address a multiple of 16 bytes
 cudaError_t launch_attend_tile(const AttendParams& p, cudaStream_t stream);
-int attend_tile_queries(int dim, int m);  // queries per CTA
+int attend_tile_queries(int m);  // queries per CTA
 int attend_tile_ctas(int dim, int m);     // CTAs that an SM holds
 // f16 / bf16, every stride and address a multiple of 16 bytes
 cudaError_t launch_attend_mma(const AttendParams& p, int dtype, cudaStream_t stream);
