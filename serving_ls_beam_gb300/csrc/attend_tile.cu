@@ -37,7 +37,7 @@ struct TileShape {
 template <int DP, int TQ, int TK>
 __global__ void __launch_bounds__(kAlThreads, TileShape<DP, TQ, TK>::CTAS) attend_tile_kernel(const AttendParams p) {
   using T = TileShape<DP, TQ, TK>;
-  constexpr int BM = T::BM, BN = T::BN, ND = DP / 32;
+  constexpr int BM = T::BM, BN = T::BN, ND = DP / 32, VI = (DP + 63) / 64;
   extern __shared__ float4 al_smem[];
   __shared__ unsigned long long tree_raw[kAtMaxNodes * 12 / 8];
   float* qs = reinterpret_cast<float*>(al_smem);
@@ -61,9 +61,16 @@ __global__ void __launch_bounds__(kAlThreads, TileShape<DP, TQ, TK>::CTAS) atten
   // tile b of the keys or values, 16 threads to a row; zeros past the row's end
   auto fetch = [&](int b, float* to, int row, const unsigned char* cache, long long pos, const unsigned char* draft,
                    long long dpos) {
-    if (b < hi) {
+    if (b < hi && b * BN + BN <= len) {
+      const unsigned char* at = cache + (b * BN + ty) * pos + tx * 16;
+      const uint32_t dst = smem_addr(to + ty * row + tx * 4);
+#pragma unroll
+      for (int k = 0; k < BN / 8; ++k, at += 8 * pos)
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+          if (tx + 16 * i < vecs) cp_async16_fill(dst + k * 32 * row + i * 256, at + i * 256, 16);
+    } else if (b < hi) {
       const int n = (min(BN, total - b * BN) + 15) & ~15;  // the rows that the products read
-#pragma unroll 4
       for (int k = ty; k < n; k += 8) {
         const int j = b * BN + k;
         const unsigned char* at = j < len ? cache + j * pos : j < total ? draft + (j - len) * dpos : p.q.data;
