@@ -96,6 +96,7 @@ bool encode_maps(CUtensorMap (&maps)[5], AttendParams& p, int dtype) {
 //   head 128, 8 queries, 256 problems: 1024 keys 28 / 29, 6000 keys 113 / 104
 //   head 64, 32 queries, 1500 problems: 256 keys 54 / 67, 512 keys 87 / 76
 //   head 64, 40 queries, 3200 problems: 100 keys 95 / 134
+//   head 64, 72 queries, 2800 problems: 66 keys 96 / 102; 128 queries: 68 keys 158 / 101
 //   head 64, 16 queries: 256 problems, 1024 keys 26 / 24; 1500 problems, 1024 keys 69 / 90
 //   head 64, 8 queries, 256 problems: 6000 keys 60 / 65
 bool tcgen05_pays(const AttendParams& p, long long problems) {
@@ -103,7 +104,7 @@ bool tcgen05_pays(const AttendParams& p, long long problems) {
   if (p.m <= 8) return false;
   if (p.dim > 64) return p.m > 16 || keys > 256;
   if (p.m <= 16) return keys >= 1024 && problems <= 4 * kAtSms;
-  return keys * ((p.m + 31) / 32) > 320;
+  return keys * ((p.m + 31) / 32) > 260;
 }
 
 // Whether the tiled f32 kernel takes a call and not the streaming one, which reads the keys anew for
@@ -112,14 +113,23 @@ bool tcgen05_pays(const AttendParams& p, long long problems) {
 // 204 / 140; 1024 of head 256, 300 to 700 positions, 8 queries 417 / 442, 12 queries 592 / 445.
 bool tile_pays(const AttendParams& p) { return p.m > 8; }
 
-// Whether a warp takes whole rows in the kernels that stream keys per warp (the other way is four
-// warps to a row or a part of it): many rows, each of a few of a warp's blocks.  In us, one warp /
-// four: 1500 rows of head 64 and 4 queries, 128 keys 15 / 20, 256 20 / 25, 512 32 / 34; of head 128,
-// 128 keys 21 / 28, 256 33 / 36; 256 rows of head 64, 512 keys 18 / 14; f32, 4096 rows of head 64,
-// 128 keys 56 / 67, 512 of head 128 and 2000 keys 363 / 57.
-bool warp_takes_rows(const AttendParams& p, long long items) {
-  const int bytes = (p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256);
-  return items >= 6 * kAtSms && ((long long)p.max_len + p.nodes) * bytes <= 20000;
+// CTAs that an SM holds of the kernels that stream keys per warp (registers; above head 128 the rings).
+int stream_ctas(const AttendParams& p, bool f32) {
+  if (f32) return 4;
+  if (p.dim > 128) return 1;
+  return p.m <= 8 || (p.dim <= 64 && p.m <= 16) ? 3 : 2;
+}
+
+// Whether a warp takes whole rows in these kernels (the other way is four warps to a row or a part of
+// it): so many rows that four warps to each would need a second round, each of a few of a warp's
+// blocks.  In us, one warp / four: 1500 rows of head 64 and 4 queries, 128 keys 15 / 20, 256 20 / 25,
+// 512 32 / 34; of head 128, 128 keys 21 / 28, 256 33 / 36; 256 rows of head 64, 512 keys 18 / 14; f32,
+// 4096 rows of head 64, 128 keys 56 / 67, 512 of head 128 and 2000 keys 363 / 57; 16-bit heads of 256,
+// 256 rows of 300 keys 30 / 25, 512 rows of 40 keys 18 / 25 and of 300 keys 32 / 42, 800 rows of 300
+// keys 57 / 59 and of 500 keys 86 / 75.
+bool warp_takes_rows(const AttendParams& p, long long items, bool f32) {
+  const int bytes = (p.dim <= 64 ? 64 : p.dim <= 128 ? 128 : 256), most = !f32 && p.dim > 128 ? 90000 : 20000;
+  return items >= (f32 ? 6 : 2 * stream_ctas(p, f32)) * kAtSms && ((long long)p.max_len + p.nodes) * bytes <= most;
 }
 
 ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
@@ -159,13 +169,16 @@ ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t 
   if (tc) {
     p.splits = split_of(p, whole, kAtSms, 512, dbg.splits);
   } else if (mma || step) {
-    p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole) ? 1 : 4;
+    p.warps = dbg.warps ? dbg.warps : warp_takes_rows(p, whole, step) ? 1 : 4;
     // As many CTAs as the GPU holds at once; in f32, where rows of different lengths cost more than
     // joining up to 64 parts, twice as many (37 trees of 6 nodes, 321 to 2357 positions: 170 -> 156 us;
     // but one row of 86753, 76 parts 145 us and 152 parts 172 us), and three times in the tiled kernel
-    // (3 trees of 32 nodes, up to 4378 positions: 97 -> 78 us).
-    const int held = step ? 4 : p.dim <= 64 || (p.dim <= 128 && p.m <= 8) ? 3 : p.dim <= 128 ? 2 : 1;
-    p.splits = p.warps == 1 ? 1 : split_of(p, whole, (step && 2 * held * kAtSms <= 64 * whole ? 2 : 1) * held * kAtSms, mma ? 512 : 256, dbg.splits);
+    // (3 trees of 32 nodes, up to 4378 positions: 97 -> 78 us).  16-bit heads above 128 elements, one CTA
+    // per SM: three times (42 trees of 8 nodes x 2 key heads of 256, 629 to 12695: 413 -> 172 us).
+    long long ctas = (long long)stream_ctas(p, step) * kAtSms;
+    if (step && 2 * ctas <= 64 * whole) ctas *= 2;
+    if (mma && p.dim > 128) ctas *= 3;
+    p.splits = p.warps == 1 ? 1 : split_of(p, whole, ctas, mma ? 512 : 256, dbg.splits);
   } else if (tile) {
     p.splits = split_of(p, whole, 3 * attend_tile_ctas(p.dim, p.m) * kAtSms, 128, dbg.splits);
   } else {
