@@ -28,9 +28,9 @@
 // What bounds it: the instructions around the products (a block's turn takes some 300 per warp for
 // 8 KB of keys and values), so the number of warps an SM holds counts (12, by registers and by two
 // ring slots each; a third slot in place of the third CTA: 66 against 52 us on the first of these).
-// Single-token step of 1024 beams x 16 heads of 64 elements, 48 to 63 positions: 239 MB in 47 us,
-// 0.75 of the measured copy rate; 128 trees of 13 nodes over 300 to 999 positions: 354 MB in 78 us,
-// 0.67; 64 rows x 8 key heads of 128 elements, 4 queries, 500 to 3000 positions: 460 MB in 86 us,
+// Single-token step of 1024 beams x 16 heads of 64 elements, 48 to 63 positions: 239 MB in 46 us,
+// 0.77 of the measured copy rate; 128 trees of 13 nodes over 300 to 999 positions: 354 MB in 74 us,
+// 0.71; 64 rows x 8 key heads of 128 elements, 4 queries, 500 to 3000 positions: 460 MB in 86 us,
 // 0.79.  With 16 rows of queries in place of 8 columns the first took 98 us.
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"

@@ -1,5 +1,5 @@
-// Attention over a row's keys on the CUDA cores: f32 tensors, and 16-bit tensors whose layout
-// the tensor-core kernels cannot read (a head size or stride that breaks 16-byte alignment).
+// Attention over a row's keys on the CUDA cores, for tensors whose layout the other kernels cannot
+// read (a head size or stride that breaks 16-byte alignment).
 //
 //   o_i = sum_n exp(s_in - max) v_n / sum_n exp(s_in - max),   s_in = scale q_i . k_n
 //

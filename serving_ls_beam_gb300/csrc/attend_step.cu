@@ -7,8 +7,8 @@
 // weights are not rounded.
 //
 // Keys and values go straight from memory into registers, 16 bytes per lane and load: LPK lanes
-// hold one vector, so a load instruction covers 32 / LPK keys, and a block is 8 such loads of
-// keys and 8 of values, 8 KB under way per warp.  The keys' registers are loaded again as soon as
+// hold one vector (above 128 elements two halves of it), so a load instruction covers 32 / LPK keys, and
+// a block is 8 such loads of keys and 8 of values, 8 KB under way per warp.  The keys' registers are loaded again as soon as
 // the block's scores are formed, the values' when its sums are.  The 8 dot products of a lane
 // group are reduced together, each exchange halving the products that a lane still holds (7
 // exchanges instead of 24), which leaves every lane with the score of its own key: one
@@ -17,7 +17,8 @@
 //
 // What bounds it: bytes under way for one query (512 rows x 16 heads of 64 elements, 40 to 63
 // positions: 222 MB in 42 us, 0.78 of the measured copy rate), instructions and registers for four
-// (256 x 16 heads, 24 to 128 states: 167 MB in 56 us, 0.44) and eight.
+// (256 x 16 heads, 24 to 128 states: 167 MB in 55 us, 0.45) and eight.  Heads of 256: 64 rows x 16 heads,
+// one query, 300 to 700 positions: 1.05 GB in 172 us, 0.90.
 //
 // A warp takes whole problems in turn (AttendParams::warps 1), or the four warps of a CTA take
 // the blocks of one (part of a) problem in turn and merge through shared memory (4).

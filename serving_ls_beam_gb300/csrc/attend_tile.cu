@@ -9,13 +9,20 @@
 // Both products are matrix products, so a CTA takes BM queries and goes over the keys in tiles of BN.
 // Its 128 threads form a grid of 8 x 16: thread (ty, tx) has the scores of queries ty + 8 i and keys
 // tx + 16 j, and of the sums the same queries' elements 2 tx + 32 n.  A vector of four elements that a
-// thread reads from shared memory serves 8 (a query's) or TQ (a key's) pairs, in packed f32 multiply
-// -adds over even and odd elements.  The weights of a query are written and read by the same half
+// thread reads from shared memory serves TK (a query's) or TQ (a key's) scores, in packed f32
+// multiply-adds over even and odd elements.  The weights of a query are written and read by the same half
 // warp, so they cross shared memory without a barrier.  Keys and values have one buffer each: the
 // next keys are on their way during the values' product and the next values during the scores'.
 // Rows are padded by 16 bytes: the 16 keys (and the two queries) of a load lie in distinct banks.
 //
 // The drafted tokens follow the row's keys without a gap.
+//
+// What bounds it: the multiply-adds and the latencies between them with 16 to 20 warps per SM.  4 x 1000
+// queries x 8 heads of 64 over 900 to 1000 keys: 214 us, 36 TFLOP/s; 64 trees of 13 nodes x 8 heads of
+// 64, 100 to 500 positions: 54 us; 1024 problems of 12 queries, head 256, 300 to 700 positions: 445 us,
+// 1.1 GB.  What mattered: CTAs per SM (8 queries per thread, two thirds of the loads and half the CTAs,
+// takes 288 us on the first of these as it was then, 4 queries 257) and one running address per whole
+// tile (257 -> 214 us).  16 queries to a tile where there are no more: 60 -> 54 us on the second.
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"
 #include "ls_tree.cuh"
