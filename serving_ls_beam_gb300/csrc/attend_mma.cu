@@ -402,17 +402,18 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         for (int a = 0; a < NQ; ++a)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const bool live = (alive >> (2 * a + e)) & 1u;
-            const int q = a * 8 + 2 * t + e;
-            const unsigned long long see = edge && p.nodes && live && q < x.nq ? tree.mask[p.by_group(x.i0 + q)] : 0ull;
+            const int q = a * 8 + 2 * t + e, d = x.len - n0;  // the drafted tokens' first place in the block
+            uint32_t sees = (alive >> (2 * a + e)) & 1u ? ~0u : 0u;  // bit i: key i of the block
+            if (edge && sees) {
+              const unsigned long long see = p.nodes && q < x.nq ? tree.mask[p.by_group(x.i0 + q)] : 0ull;
+              sees = x.b < 0 ? 0u : d >= 0 ? ((1u << d) - 1u) | (uint32_t)(see << d) : (uint32_t)(see >> -d);
+            }
+            sees >>= g;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int j = n0 + k * 16 + hf * 8 + g;
-                const bool ok = live && j < total && (j < x.len || ((see >> (j - x.len)) & 1ull));
-                if (!ok) s[k][a][2 * hf + e] = -INFINITY;
-              }
+              for (int hf = 0; hf < 2; ++hf)
+                if (!((sees >> (k * 16 + hf * 8)) & 1u)) s[k][a][2 * hf + e] = -INFINITY;
           }
       }
       // The maximum is taken over the lanes, and the sums rescaled, only when some lane's own has
