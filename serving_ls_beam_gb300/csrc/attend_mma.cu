@@ -28,9 +28,9 @@
 // What bounds it: the instructions around the products (a block's turn takes some 300 per warp for
 // 8 KB of keys and values), so the number of warps an SM holds counts (12, by registers and by two
 // ring slots each; a third slot in place of the third CTA: 66 against 52 us on the first of these).
-// Single-token step of 1024 beams x 16 heads of 64 elements, 48 to 63 positions: 239 MB in 46 us,
-// 0.77 of the measured copy rate; 128 trees of 13 nodes over 300 to 999 positions: 354 MB in 74 us,
-// 0.71; 64 rows x 8 key heads of 128 elements, 4 queries, 500 to 3000 positions: 460 MB in 86 us,
+// Single-token step of 1024 beams x 16 heads of 64 elements, 48 to 63 positions: 239 MB in 42 us,
+// 0.84 of the measured copy rate; 128 trees of 13 nodes over 300 to 999 positions: 354 MB in 68 us,
+// 0.77; 64 rows x 8 key heads of 128 elements, 4 queries, 500 to 3000 positions: 460 MB in 86 us,
 // 0.79.  With 16 rows of queries in place of 8 columns the first took 98 us.
 #include "ls_device.cuh"
 #include "ls_dtype.cuh"
@@ -249,16 +249,23 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         const unsigned char* fv = p.value.data + (long long)fx.r * p.value.row + (long long)fx.h * p.value.head + fo;
         const unsigned char* dk = p.dkey.data + (long long)fx.r * p.dkey.row + (long long)fx.h * p.dkey.head + fo;
         const unsigned char* dv = p.dvalue.data + (long long)fx.r * p.dvalue.row + (long long)fx.h * p.dvalue.head + fo;
-        const uint32_t kpos = (uint32_t)p.key.pos, vpos = (uint32_t)p.value.pos;
-#pragma unroll 4
+        // the lane's place in the cache and among the drafted tokens, advanced row by row of its copies
+        const unsigned char* ck = fk + j0 * p.key.pos;
+        const unsigned char* cv = fv + j0 * p.value.pos;
+        const unsigned char* nk = dk + (j0 - fx.len) * p.dkey.pos;
+        const unsigned char* nv = dv + (j0 - fx.len) * p.dvalue.pos;
+        const long long ks = RPI * p.key.pos, vs = RPI * p.value.pos, nks = RPI * p.dkey.pos, nvs = RPI * p.dvalue.pos;
+#pragma unroll
         for (int u = 0; u < KB / RPI; ++u) {
           const uint32_t off = at(u * RPI + fr, fc);
           const int j = j0 + u * RPI;
-          const bool ok = fcv && j < total && j >= 0;
-          const unsigned char* ka = j < fx.len ? fk + (unsigned long long)(uint32_t)j * kpos : dk + (long long)(j - fx.len) * p.dkey.pos;
-          const unsigned char* va = j < fx.len ? fv + (unsigned long long)(uint32_t)j * vpos : dv + (long long)(j - fx.len) * p.dvalue.pos;
-          cp_async16_fill(kd_ + off, ok ? ka : p.q.data, ok ? 16 : 0);
-          cp_async16_fill(vd_ + off, ok ? va : p.q.data, ok ? 16 : 0);
+          const bool ok = fcv && j < total && j >= 0, cached = j < fx.len;
+          cp_async16_fill(kd_ + off, ok ? (cached ? ck : nk) : p.q.data, ok ? 16 : 0);
+          cp_async16_fill(vd_ + off, ok ? (cached ? cv : nv) : p.q.data, ok ? 16 : 0);
+          ck += ks;
+          cv += vs;
+          nk += nks;
+          nv += nvs;
         }
       }
       if (fx.b >= 0) fx.b += W;
