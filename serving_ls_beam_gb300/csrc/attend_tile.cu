@@ -19,7 +19,7 @@
 //
 // What bounds it: the multiply-adds and the latencies between them with 16 to 20 warps per SM.  4 x 1000
 // queries x 8 heads of 64 over 900 to 1000 keys: 214 us, 36 TFLOP/s; 64 trees of 13 nodes x 8 heads of
-// 64, 100 to 500 positions: 54 us; 1024 problems of 12 queries, head 256, 300 to 700 positions: 445 us,
+// 64, 100 to 500 positions: 51 us with the join; 1024 problems of 12 queries, head 256, 300 to 700 positions: 445 us,
 // 1.1 GB.  What mattered: CTAs per SM (8 queries per thread, two thirds of the loads and half the CTAs,
 // takes 288 us on the first of these as it was then, 4 queries 257) and one running address per whole
 // tile (257 -> 214 us).  16 queries to a tile where there are no more: 60 -> 54 us on the second.
