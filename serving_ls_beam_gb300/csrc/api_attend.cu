@@ -58,6 +58,11 @@ size_t workspace_size(int rows, int k, int q_len, int heads, int kv_heads, int m
   return kAtHeader + (size_t)attend_part_rows((int)m) * (size_t)(dim + 2) * 4;
 }
 
+// `need`: workspace_size's answer, 0 where the call has no size at all.
+bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
+  return workspace && !misaligned(workspace, 256) && need > 0 && bytes >= need;
+}
+
 // Parts of each row's keys so that about `ctas` CTAs run, each with `least` keys or more (below that
 // the launch that joins them, some 2 us, costs more than the parts save).
 int split_of(const AttendParams& p, long long base, long long ctas, int least, int forced) {
@@ -247,8 +252,8 @@ ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view
   if (max_src > 0 && (!view_ok(key, es, false, 1, batch, max_src, kv_heads) ||
                       !view_ok(value, es, false, 1, batch, max_src, kv_heads)))
     return LS_ERR_INVALID_ARG;
-  if (!src_len || misaligned(src_len, 4) || !workspace || misaligned(workspace, 256) ||
-      workspace_bytes < workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim))
+  if (!src_len || misaligned(src_len, 4) ||
+      !workspace_ok(workspace, workspace_bytes, workspace_size(batch, k, q_len, heads, kv_heads, max_src, head_dim)))
     return LS_ERR_INVALID_ARG;
   const void* ptrs[] = {q->data, max_src ? key->data : nullptr, max_src ? value->data : nullptr, src_len, out->data,
                         workspace};
@@ -283,6 +288,8 @@ ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls
       !shape_ok(rows, 1, nodes, heads, kv_heads, max_len, head_dim))
     return LS_ERR_INVALID_ARG;
   if (rows == 0) return LS_OK;
+  const long long m = queries_per_key(1, nodes, heads / kv_heads);
+  if (m > INT_MAX) return LS_ERR_UNSUPPORTED;
   const int es = es_of(dtype);
   if (!view_ok(q, es, false, 1, rows, nodes, heads) || !view_ok(out, es, true, 1, rows, nodes, heads) ||
       !view_ok(draft_key, es, false, 1, rows, nodes, kv_heads) || !view_ok(draft_value, es, false, 1, rows, nodes, kv_heads))
@@ -290,8 +297,8 @@ ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls
   if (max_len > 0 && (!view_ok(cache_key, es, false, 1, rows, max_len, kv_heads) ||
                       !view_ok(cache_value, es, false, 1, rows, max_len, kv_heads)))
     return LS_ERR_INVALID_ARG;
-  if (!cache_len || misaligned(cache_len, 4) || !parent || misaligned(parent, 4) || !workspace ||
-      misaligned(workspace, 256) || workspace_bytes < workspace_size(rows, 1, nodes, heads, kv_heads, max_len, head_dim))
+  if (!cache_len || misaligned(cache_len, 4) || !parent || misaligned(parent, 4) ||
+      !workspace_ok(workspace, workspace_bytes, workspace_size(rows, 1, nodes, heads, kv_heads, max_len, head_dim)))
     return LS_ERR_INVALID_ARG;
   const void* ptrs[] = {q->data,   max_len ? cache_key->data : nullptr, max_len ? cache_value->data : nullptr,
                         cache_len, draft_key->data, draft_value->data,  parent, out->data, workspace};
@@ -317,7 +324,7 @@ ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls
   p.max_len = max_len;
   p.nodes = nodes;
   p.tokens = nodes;
-  p.m = nodes * p.group;
+  p.m = (int)m;
   return attend(p, dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 

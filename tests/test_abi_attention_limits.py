@@ -1,0 +1,48 @@
+"""Counts that 32 or 64 bits do not hold are refused by the attention and commit entry points (no GPU: all
+of it is found on the host).  Each call runs in a process of its own, with the pointer checks off, so that
+an abort would be a failed test and nothing else."""
+import subprocess
+import sys
+
+import pytest
+
+INVALID, UNSUPPORTED = 1, 2
+
+CALL = """
+import os
+os.environ["LS_BEAM_DEBUG"] = "nocheck"
+import serving_ls_beam_gb300 as lsb
+L, P = lsb.load_library(), 4096  # an address that no refused call looks behind
+def view(row=64, pos=64, head=8):
+    return lsb._View(P, 0, row, pos, head)
+def cross(b=2, k=4, t=1, h=8, hk=8, n=16, d=8, size=1 << 40):
+    return L.ls_cross_attention(view(), view(), view(), 1, P, 1.0, b, k, t, h, hk, n, d, view(), P, size, None)
+def tree(rows=2, nodes=4, h=8, hk=8, n=16, d=8, size=1 << 40):
+    return L.ls_tree_attention(view(), view(), view(), P, view(), view(), P, 2, 1.0, rows, nodes, h, hk, n, d, view(), P,
+                               size, None)
+print("status", EXPR)
+"""
+
+
+@pytest.fixture(scope="module")
+def call():
+    from serving_ls_beam_gb300 import _build
+
+    _build.build()
+
+    def run(expr):
+        r = subprocess.run([sys.executable, "-c", CALL.replace("EXPR", expr)], capture_output=True, text=True, timeout=120)
+        assert r.returncode == 0, (expr, r.returncode, r.stderr[-400:])
+        return int(r.stdout.split()[-1])
+
+    return run
+
+
+def test_queries_per_key_of_a_tree(call):
+    """nodes * group past 31 bits: products that wrap to 0 (a division by it) and to a small count (64)."""
+    assert call("tree(nodes=4, h=1 << 30, hk=1)") == UNSUPPORTED
+    assert call("tree(nodes=64, h=1 << 27, hk=1)") == UNSUPPORTED
+    assert call("tree(nodes=64, h=(1 << 26) + 1, hk=1)") == UNSUPPORTED
+    assert call("tree(nodes=64, h=(1 << 26) + 1, hk=1, size=0)") == UNSUPPORTED  # and no workspace is looked at
+    assert call("cross(k=1 << 26, t=64, h=8, hk=1)") == UNSUPPORTED
+    assert call("tree(size=0)") == INVALID
