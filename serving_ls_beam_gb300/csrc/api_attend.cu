@@ -139,7 +139,7 @@ bool warp_takes_rows(const AttendParams& p, long long items, bool f32) {
 
 ls_status attend(AttendParams& p, ls_dtype dtype, void* workspace, cudaStream_t stream) {
   const long long base = (long long)p.rows * p.kv_heads;
-  if (base * p.m > INT_MAX) return LS_ERR_UNSUPPORTED;
+  if (base > INT_MAX / p.m) return LS_ERR_UNSUPPORTED;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.spin_limit_ns = wait_limit_ns();

@@ -46,3 +46,12 @@ def test_queries_per_key_of_a_tree(call):
     assert call("tree(nodes=64, h=(1 << 26) + 1, hk=1, size=0)") == UNSUPPORTED  # and no workspace is looked at
     assert call("cross(k=1 << 26, t=64, h=8, hk=1)") == UNSUPPORTED
     assert call("tree(size=0)") == INVALID
+
+
+def test_queries_of_a_call(call):
+    """Rows x key heads x queries per key past 31 bits, also where 64 bits do not hold the product (2^64, 2^64 + 2^14)."""
+    assert call("cross(b=1 << 30, k=1, t=1 << 14, h=1 << 20, hk=1 << 20)") == UNSUPPORTED
+    assert call("cross(b=(1 << 30) + 1, k=1, t=1 << 14, h=1 << 20, hk=1 << 20)") == UNSUPPORTED
+    assert call("cross(b=1 << 20, k=1, t=1 << 11, h=1, hk=1)") == UNSUPPORTED
+    assert call("tree(rows=1 << 30, nodes=64, h=1 << 28, hk=1 << 28)") == UNSUPPORTED
+    assert call("tree(rows=1 << 30, nodes=2, h=1, hk=1)") == UNSUPPORTED
