@@ -55,3 +55,6 @@ def test_queries_of_a_call(call):
     assert call("cross(b=1 << 20, k=1, t=1 << 11, h=1, hk=1)") == UNSUPPORTED
     assert call("tree(rows=1 << 30, nodes=64, h=1 << 28, hk=1 << 28)") == UNSUPPORTED
     assert call("tree(rows=1 << 30, nodes=2, h=1, hk=1)") == UNSUPPORTED
+    # rows long enough to be cut in parts: the number of parts is divided by that product
+    assert call("cross(b=1 << 30, k=1, t=1 << 14, h=1 << 20, hk=1 << 20, n=1 << 16)") == UNSUPPORTED
+    assert call("tree(rows=1 << 30, nodes=64, h=1 << 28, hk=1 << 28, n=1 << 16)") == UNSUPPORTED
