@@ -352,7 +352,8 @@ ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cach
                         move ? cache_value : nullptr, move ? draft_key->data : nullptr, move ? draft_value->data : nullptr};
   if (!pointers_reachable(ptrs, 15)) return LS_ERR_INVALID_ARG;
   const long long head_bytes = (long long)head_dim * es;
-  if (move && (layers > 65535 || 2ll * nodes * heads * head_dim > 1ll << 30)) return LS_ERR_UNSUPPORTED;
+  // (the copies of a row and layer are counted in 32 bits)
+  if (move && (layers > 65535 || (long long)heads * head_dim > (1ll << 30) / (2 * nodes))) return LS_ERR_UNSUPPORTED;
   CommitParams p{};
   if (move) {
     p.cache_key = static_cast<unsigned char*>(cache_key);

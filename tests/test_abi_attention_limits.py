@@ -20,6 +20,9 @@ def cross(b=2, k=4, t=1, h=8, hk=8, n=16, d=8, size=1 << 40):
 def tree(rows=2, nodes=4, h=8, hk=8, n=16, d=8, size=1 << 40):
     return L.ls_tree_attention(view(), view(), view(), P, view(), view(), P, 2, 1.0, rows, nodes, h, hk, n, d, view(), P,
                                size, None)
+def commit(rows=2, layers=1, nodes=4, heads=2, n=8, d=8):
+    return L.ls_tree_commit(P, 2 * P, P, view(), view(), 1, P, P, P, None, 2, layers, rows, nodes, heads, n, d, 2 * P, P, P, P,
+                            None, None, None)
 print("status", EXPR)
 """
 
@@ -58,3 +61,11 @@ def test_queries_of_a_call(call):
     # rows long enough to be cut in parts: the number of parts is divided by that product
     assert call("cross(b=1 << 30, k=1, t=1 << 14, h=1 << 20, hk=1 << 20, n=1 << 16)") == UNSUPPORTED
     assert call("tree(rows=1 << 30, nodes=64, h=1 << 28, hk=1 << 28, n=1 << 16)") == UNSUPPORTED
+
+
+def test_elements_of_a_commit(call):
+    """nodes x heads x head_dim elements past 2^30, also where 64 bits do not hold the product."""
+    assert call("commit(nodes=8, heads=1 << 30, d=1 << 30)") == UNSUPPORTED
+    assert call("commit(nodes=64, heads=(1 << 31) - 1, d=(1 << 31) - 1)") == UNSUPPORTED
+    assert call("commit(nodes=64, heads=1 << 14, d=(1 << 9) + 1)") == UNSUPPORTED
+    assert call("commit(layers=65536)") == UNSUPPORTED
