@@ -282,7 +282,8 @@ typedef struct {
  *              the others.  Calls sharing it must be ordered.
  *  Inputs that a query reads are finite; otherwise its result is unspecified (no fault).
  *  batch == 0 or q_len == 0 is a no-op.  Fastest when every stride and address is a multiple of
- *  16 bytes.  More than 2^31 - 1 blocks of work return LS_ERR_UNSUPPORTED.
+ *  16 bytes.  More than 2^31 - 1 queries or blocks of work, or more than 2^31 - 1024 positions,
+ *  return LS_ERR_UNSUPPORTED.
  */
 LS_API size_t ls_cross_attention_workspace_size(int batch, int k, int q_len, int heads, int kv_heads, int max_src,
                                                 int head_dim);

@@ -245,7 +245,7 @@ ls_status ls_cross_attention(const ls_view* q, const ls_view* key, const ls_view
     return LS_ERR_INVALID_ARG;
   if (batch == 0 || q_len == 0) return LS_OK;
   const long long m = queries_per_key(k, q_len, heads / kv_heads);
-  if ((long long)batch * k > INT_MAX || m > INT_MAX) return LS_ERR_UNSUPPORTED;
+  if ((long long)batch * k > INT_MAX || m > INT_MAX || max_src > kAtMaxKeys) return LS_ERR_UNSUPPORTED;
   const int es = es_of(dtype);
   if (!view_ok(q, es, false, 1, batch * k, q_len, heads) ||
       !view_ok(out, es, true, 1, batch * k, q_len, heads)) return LS_ERR_INVALID_ARG;
@@ -289,7 +289,7 @@ ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, const ls
     return LS_ERR_INVALID_ARG;
   if (rows == 0) return LS_OK;
   const long long m = queries_per_key(1, nodes, heads / kv_heads);
-  if (m > INT_MAX) return LS_ERR_UNSUPPORTED;
+  if (m > INT_MAX || max_len > kAtMaxKeys) return LS_ERR_UNSUPPORTED;
   const int es = es_of(dtype);
   if (!view_ok(q, es, false, 1, rows, nodes, heads) || !view_ok(out, es, true, 1, rows, nodes, heads) ||
       !view_ok(draft_key, es, false, 1, rows, nodes, kv_heads) || !view_ok(draft_value, es, false, 1, rows, nodes, kv_heads))

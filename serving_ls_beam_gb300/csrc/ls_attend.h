@@ -16,6 +16,8 @@ namespace lsb {
 
 constexpr int kAtMaxDim = 256;   // largest head size
 constexpr int kAtMaxNodes = LS_MAX_NODES;
+// positions of a row: the kernels add its drafted tokens and a block of up to 128 keys in 32 bits
+constexpr int kAtMaxKeys = INT32_MAX - 1023;
 constexpr int kAtSms = 152;
 
 // Division of 0 <= n < 2^31 by a number known on the host (Granlund and Montgomery, 1994).

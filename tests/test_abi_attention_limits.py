@@ -69,3 +69,11 @@ def test_elements_of_a_commit(call):
     assert call("commit(nodes=64, heads=(1 << 31) - 1, d=(1 << 31) - 1)") == UNSUPPORTED
     assert call("commit(nodes=64, heads=1 << 14, d=(1 << 9) + 1)") == UNSUPPORTED
     assert call("commit(layers=65536)") == UNSUPPORTED
+
+
+def test_positions_of_a_row(call):
+    """Lengths whose sums with the drafted tokens and a block's keys 32 bits would not hold."""
+    for n in ((1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 1023):
+        assert call(f"cross(n={n})") == UNSUPPORTED
+        assert call(f"tree(n={n})") == UNSUPPORTED
+        assert call(f"cross(n={n}, b=0)") == 0 and call(f"tree(n={n}, rows=0)") == 0
