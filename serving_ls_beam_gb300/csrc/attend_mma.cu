@@ -200,15 +200,17 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
   auto at = [&](int r, int c) { return (uint32_t)((c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
   const uint32_t k_lane = at(lane & 15, lane >> 4), v_lane = at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
   const uint32_t flip = p.negate ? 0x80008000u : 0u;  // a negative scale: the queries' signs
-  const int items = (int)p.items;
-  const int stride = W == 1 ? (int)gridDim.x * kMmWarps : (int)gridDim.x;
-  const int first = W == 1 ? (int)blockIdx.x * kMmWarps + warp : (int)blockIdx.x;
+  // (unsigned: an item's number plus the stride, each below 2^31, may pass it)
+  const uint32_t items = (uint32_t)p.items;
+  const uint32_t stride = W == 1 ? gridDim.x * kMmWarps : gridDim.x;
+  const uint32_t first = W == 1 ? blockIdx.x * kMmWarps + warp : blockIdx.x;
 
   // ---- the ring's filling side: item `fi` (its length loaded one item ahead), block `fx.b`
   const int fc = lane % CPR, fr = lane / CPR;  // this lane's vector of a row, and its row of a copy
   const bool fcv = fc < chunks;
   const int fsz = fcv ? 16 : 0, fo = fcv ? fc * 16 : 0;
-  int fi = first, f_seq = 0, f_slot = 0;
+  uint32_t fi = first;
+  int f_seq = 0, f_slot = 0;
   bool f_new = true;
   MmaItem fx{};
   int f_len = fi < items ? __ldg(p.len + item_row(p, fi)) : 0;
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
   uint32_t phases = 0;  // bit i: the parity that slot i's barrier completes next
   int c_len = first < items ? __ldg(p.len + item_row(p, first)) : 0;
 #pragma unroll 1
-  for (int it = first; it < items; it += stride) {
+  for (uint32_t it = first; it < items; it += stride) {
     MmaItem x = open_item<KB, NQ>(p, it, c_len, wi);
     if (x.len != c_len && lane == 0) atomicOr(p.status, kDevInternal);
     if (it + stride < items) c_len = __ldg(p.len + item_row(p, it + stride));

@@ -78,11 +78,12 @@ __global__ void __launch_bounds__(kAsThreads, MQ * V <= 2 ? 4 : 1) attend_step_k
   for (int v = 0; v < V; ++v) cv[v] = c + LPK * v < p.dim / E;
   const int my_u = U == 8 ? (lane & 1) << 2 | (lane & 2) | (lane >> 2 & 1) : (lane & 1) << 1 | (lane >> 1 & 1);
   const TreeSeen tree = tree_at(trees[warp], kAtMaxNodes);
-  const int items = (int)p.items, stride = W == 1 ? (int)gridDim.x * kAsWarps : (int)gridDim.x;
-  int it = W == 1 ? (int)blockIdx.x * kAsWarps + warp : (int)blockIdx.x;
+  // (unsigned: an item's number plus the stride, each below 2^31, may pass it)
+  const uint32_t items = (uint32_t)p.items, stride = W == 1 ? gridDim.x * kAsWarps : gridDim.x;
+  uint32_t it = W == 1 ? blockIdx.x * kAsWarps + warp : blockIdx.x;
   int next_len = it < items ? __ldg(p.len + p.by_head(p.by_tile(p.by_split(it)))) : 0;
   for (; it < items; it += stride) {
-    const int ia = p.by_split(it), split = it - ia * p.splits, ib = p.by_tile(ia);
+    const int ia = p.by_split(it), split = (int)it - ia * p.splits, ib = p.by_tile(ia);
     const int i0 = (ia - ib * p.m_tiles) * MQ, r = p.by_head(ib), h = ib - r * p.kv_heads;
     const int nq = min(MQ, p.m - i0);
     const int len = min(max(next_len, 0), p.max_len);

@@ -180,17 +180,18 @@ __device__ __forceinline__ TcItem<N> tc_item(const AttendParams& p, int it, int 
 // A walk over this CTA's items that have tiles: the next length is loaded while an item is worked on.
 template <int N>
 struct TcWalk {
-  int it, next_len;
+  unsigned it;  // (unsigned: an item's number plus the stride, each below 2^31, may pass it)
+  int next_len;
   int active;   // items with tiles before this one
   int job, tile;  // jobs and tiles before this item's
   TcItem<N> x;
   bool valid;
-  __device__ __forceinline__ void load(const AttendParams& p, int i) {
+  __device__ __forceinline__ void load(const AttendParams& p, unsigned i) {
     // the shuffle tells the compiler that the value is one for the warp
-    next_len = __shfl_sync(~0u, i < (int)p.items ? __ldg(p.len + tc_row(p, i)) : 0, 0);
+    next_len = __shfl_sync(~0u, i < (unsigned)p.items ? __ldg(p.len + tc_row(p, i)) : 0, 0);
   }
   __device__ __forceinline__ void find(const AttendParams& p) {
-    for (; it < (int)p.items; it += gridDim.x) {
+    for (; it < (unsigned)p.items; it += gridDim.x) {
       x = tc_item<N>(p, it, next_len);
       load(p, it + gridDim.x);
       if (x.nt > 0) {
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     int sums[2] = {0, 0};  // items before in which the slot had a job
     bool ok = true;
     int turn = 1;
-    for (int it = blockIdx.x; it < (int)p.items && ok; it += gridDim.x) {
+    for (unsigned it = blockIdx.x; it < (unsigned)p.items && ok; it += gridDim.x) {
       turn ^= 1;
       const TcItem<N> x = tc_item<N>(p, it, next_len);
       if (x.len != next_len && tid == 0) atomicOr(p.status, kDevInternal);
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               uint4 d = *at;
               if (clear_non_finite<BF>(d)) {
                 *at = d;
-                bad_values[turn] = it + 1;
+                bad_values[turn] = (int)it + 1;
               }
             }
           }
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           f *= inv;
           f_other *= inv;
         }
-        const bool has_bad = bad_values[turn] == it + 1;
+        const bool has_bad = bad_values[turn] == (int)it + 1;
         const bool rare = has_bad || __any_sync(~0u, zero);
         const unsigned char* dv = p.dvalue.data + (long long)x.r * p.dvalue.row + (long long)x.h * p.dvalue.head;
         const long long pr = (((long long)x.r * p.kv_heads + x.h) * p.m + qi) * p.splits + x.split;
