@@ -222,8 +222,14 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
         fx = open_item<KB, NQ>(p, fi, f_len, wi);
         if (fi + stride < items) f_len = __ldg(p.len + item_row(p, fi + stride));
         const uint32_t qd = base + sm.q + f_seq * sm.q_one;
-        for (int i = fr; i < fx.nq; i += RPI)
-          cp_async16_fill(qd + i * sm.q_row + fc * 16, p.q.data + query_offset(p, p.q, fx.r, fx.h, fx.i0 + i) + fo, fsz);
+        // (ldmatrix reads all places: those past the last query are zeros, so that their scores, which say
+        // when the maximum is reduced, do not depend on what lay there)
+        const int places = S::QREG ? fx.nq : 8 * NQ;
+        for (int i = fr; i < places; i += RPI) {
+          const bool there = i < fx.nq;
+          const unsigned char* from = there ? p.q.data + query_offset(p, p.q, fx.r, fx.h, fx.i0 + i) + fo : p.q.data;
+          cp_async16_fill(qd + i * sm.q_row + fc * 16, from, there ? fsz : 0);
+        }
         for (int i = lane; i < p.nodes; i += 32)
           cp_async4(base + sm.par + f_seq * sm.par_one + i * 4, p.parent + (long long)fx.r * p.nodes + i);
         f_seq = f_seq + 1 == sets ? 0 : f_seq + 1;
