@@ -272,7 +272,8 @@ typedef struct {
  *              whatever they hold.
  *  dtype       f32, f16 or bf16 (one for all).  Scores, softmax and sums are f32; for 16-bit
  *              types the softmax weights are rounded to the type for the product with the
- *              values, and the result is rounded once.
+ *              values (in f16 those under 2^-32 of a row's largest count in the sum alone), and
+ *              the result is rounded once.
  *  src_len     [batch] int32, device.  A length outside [0, max_src] is clamped and sets
  *              LS_ERR_INTERNAL in the workspace's status word.
  *  heads       a multiple of kv_heads; head_dim 1..256; k >= 1, not limited by LS_MAX_K.

@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
           }
       }
       // The maximum is taken over the lanes, and the sums rescaled, only when some lane's own has
-      // grown by more than 2^8: until then weights are at most 2^8 instead of 1, which f32 sums and the
-      // 16-bit types hold without loss.
+      // grown by more than 2^8: until then weights are at most 2^8 times as large (in f16 2^15, kAtLift),
+      // which f32 sums and the 16-bit types hold without loss.
       float top[NQ][2];
       bool grown = false;
 #pragma unroll
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
           top[a][e] = fmaxf(s[0][a][e], s[0][a][2 + e]);
 #pragma unroll
           for (int k = 1; k < KT; ++k) top[a][e] = fmaxf(top[a][e], fmaxf(s[k][a][e], s[k][a][2 + e]));
-          grown |= top[a][e] * c > m_run[a][e] + kMmLazy;
+          grown |= fmaf(top[a][e], c, -kAtLift<BF>) > m_run[a][e] + kMmLazy;
         }
       if (__any_sync(~0u, grown)) {
 #pragma unroll
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kMmThreads, MmaShape<DP, NQ>::CTAS)
             bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 4));
             bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 8));
             bm = fmaxf(bm, __shfl_xor_sync(~0u, bm, 16));
-            const float mn = fmaxf(m_run[a][e], bm * c);
+            const float mn = fmaxf(m_run[a][e], fmaf(bm, c, -kAtLift<BF>));
             f[e] = fast_exp2(m_run[a][e] - (mn == -INFINITY ? 0.0f : mn));
             m_run[a][e] = mn;
             l_run[a][e] *= f[e];

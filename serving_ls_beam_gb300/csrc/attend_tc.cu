@@ -41,8 +41,8 @@
 //   plus 4 us to join the parts, 0.88 of the measured copy rate.
 //
 // The accumulator is rescaled only when a query's maximum has grown by more than 2^8 since the
-// last time: until then its weights are at most 2^8 instead of 1, which f32 sums and the 16-bit
-// types hold without loss.  Every wait is bounded: one that runs out sets the timeout bit of the
+// last time: until then its weights are at most 2^8 times as large (in f16 2^15, kAtLift), which f32
+// sums and the 16-bit types hold without loss.  Every wait is bounded: one that runs out sets the timeout bit of the
 // status word, and the CTA lets its copies and products finish, frees its tensor memory and
 // returns.
 #include <cuda.h>
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           float mn = m4[0];
 #pragma unroll
           for (int k = 1; k < CH; ++k) mn = fmaxf(mn, m4[k]);
-          mn *= c;
+          mn = fmaf(mn, c, -kAtLift<BF>);
           const bool grow = mn > m_run + kTaLazy;  // from -inf at the first finite score
           if (__any_sync(~0u, grow)) {
             const float to_m = fmaxf(m_run, mn), sub = to_m == -INFINITY ? 0.0f : to_m;

@@ -86,6 +86,14 @@ __device__ __forceinline__ bool clear_non_finite(uint4& d) {
   return true;
 }
 
+// The 16-bit kernels' weights are 2^(score - reference); the reference lies this far under a row's maximum,
+// for the sums and the weighted values alike, so that it cancels.  f16 has 2^-24 as its smallest number:
+// with weights of up to 2^15 (2^8 of a maximum that has not been raised yet) it keeps what is 2^-31 of the largest
+// weight or more, where weights of up to 1 would lose a long flat tail under one large score at 2^-25.
+// (One key at weight 1 and 131000 at 2^-25.1: -0.9966 for -0.9927.)  bf16 has the exponents of f32.
+template <bool BF>
+constexpr float kAtLift = BF ? 0.0f : 7.0f;
+
 // acc + f * x of a part with the sum l: nothing of an empty part, and an infinite or NaN x as
 // it is (f may have underflowed).
 __device__ __forceinline__ float add_part(float acc, float f, float x, float l) {
