@@ -14,13 +14,28 @@ is that.
 Everything stays on the GPU and every buffer is allocated once, so that a step can be captured in a
 CUDA graph (the memory-reuse rule of the LightSeq inference article, 31duo.com, itemid-283120, as
 in ``loop.py``; the two sets of lengths alternate, so capture two steps).
+
+``stream`` (a stream of torch's or its handle; torch's current one by default) is where a call's work
+goes, all of it.  The caller orders that stream behind the inputs and keeps them until it has passed.
+``reset`` works on the current stream.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
 from . import (check, ls_cross_attention, ls_cross_attention_workspace_size, ls_sample, ls_sample_workspace_size,
                ls_tree_attention, ls_tree_attention_workspace_size, ls_tree_commit, ls_workspace_init)
+
+
+def _torch_on(stream, device):
+    """Torch's own operations on the stream that the library's calls are given."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 class DraftTreeDecoder:
@@ -72,8 +87,9 @@ class DraftTreeDecoder:
     def self_attention(self, layer: int, q, key, value, parent, stream=None) -> torch.Tensor:
         """q [rows, nodes, heads, head_dim], key and value [rows, nodes, kv_heads, head_dim] of this layer's nodes, parent
         [rows, nodes] int32.  Returns a buffer that the next attention overwrites."""
-        self.draft_key[layer].copy_(key)
-        self.draft_value[layer].copy_(value)
+        with _torch_on(stream, self.draft_key.device):
+            self.draft_key[layer].copy_(key)
+            self.draft_value[layer].copy_(value)
         check(ls_tree_attention(q, self.cache_key[layer], self.cache_value[layer], self.lengths[self.cur],
                                 self.draft_key[layer], self.draft_value[layer], parent, self.attended, self.workspace,
                                 stream=stream), "ls_tree_attention")
