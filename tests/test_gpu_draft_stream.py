@@ -1,10 +1,11 @@
-"""DraftTreeDecoder on a stream of the caller's: the same tokens, lengths and
+"""DraftTreeDecoder on a stream of the caller's, and captured in a CUDA graph: the same tokens, lengths and
 caches as on the current stream."""
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+import serving_ls_beam_gb300 as lsb  # noqa: E402
 from serving_ls_beam_gb300.draft import DraftTreeDecoder  # noqa: E402
 
 L, R, N, H, HK, D, S, V, EOS = 2, 3, 4, 4, 2, 64, 64, 50, 1
@@ -86,3 +87,27 @@ def test_a_stream_of_the_callers(integer):
     for n in range(6):
         p.step(side, side.cuda_stream if integer else side)
         assert same(p.state(), want[n]), n
+
+
+def test_two_steps_captured():
+    """The two sets of lengths alternate: two captured steps, replayed, go on as single ones do."""
+    want = eager(8)
+    p = Program()
+    p.reset()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        p.step()
+        p.step()
+    torch.cuda.current_stream().wait_stream(warm)
+    assert same(p.state(), want[1])
+    p.reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.step()
+        p.step()
+    for n in range(4):
+        graph.replay()
+        assert same(p.state()[:5], want[2 * n + 1][:5]), n
+    assert same(p.state(), want[7])
+    assert lsb.ls_read_status(p.dec.workspace) == lsb.LS_OK
