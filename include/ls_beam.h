@@ -344,7 +344,8 @@ LS_API ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, c
  *  out_count   [rows] int32: nodes appended.
  *  out_token   [rows] int32: the next token, target of the branch's last node (the next tree's
  *              node 0); token[r, 0] when nothing could be appended.
- *  out_finished  [rows] uint8 or NULL: finished, or the next token is eos_id.
+ *  out_finished  [rows] uint8 or NULL: finished, or the next token is eos_id; not the array
+ *              finished itself.
  *  workspace   NULL, or a workspace initialised by ls_workspace_init: a length out of range, a
  *              full cache or a tree whose node 0 is not its root (each: the row appends nothing)
  *              sets LS_ERR_INTERNAL in its status word.

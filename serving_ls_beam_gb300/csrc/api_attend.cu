@@ -346,7 +346,8 @@ ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cach
   const void* words[] = {cache_len, parent, token, target, out_len, out_path, out_count, out_token};
   for (const void* w : words)
     if (!w || misaligned(w, 4)) return LS_ERR_INVALID_ARG;
-  if (out_len == cache_len || (workspace && misaligned(workspace, 256))) return LS_ERR_INVALID_ARG;
+  // (every layer's block reads these inputs, whichever of them has written the outputs)
+  if (out_len == cache_len || (finished && out_finished == finished) || (workspace && misaligned(workspace, 256))) return LS_ERR_INVALID_ARG;
   const void* ptrs[] = {cache_len, parent,    token,     target,       out_len,   out_path, out_count,
                         out_token, finished,  out_finished, workspace, move ? cache_key : nullptr,
                         move ? cache_value : nullptr, move ? draft_key->data : nullptr, move ? draft_value->data : nullptr};

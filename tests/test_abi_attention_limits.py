@@ -1,5 +1,5 @@
-"""Counts that 32 or 64 bits do not hold are refused by the attention and commit entry points (no GPU: all
-of it is found on the host).  Each call runs in a process of its own, with the pointer checks off, so that
+"""Counts that 32 or 64 bits do not hold, and outputs that are inputs, are refused by the attention and commit
+entry points (no GPU: all of it is found on the host).  Each call runs in a process of its own, with the pointer checks off, so that
 an abort would be a failed test and nothing else."""
 import subprocess
 import sys
@@ -20,9 +20,9 @@ def cross(b=2, k=4, t=1, h=8, hk=8, n=16, d=8, size=1 << 40):
 def tree(rows=2, nodes=4, h=8, hk=8, n=16, d=8, size=1 << 40):
     return L.ls_tree_attention(view(), view(), view(), P, view(), view(), P, 2, 1.0, rows, nodes, h, hk, n, d, view(), P,
                                size, None)
-def commit(rows=2, layers=1, nodes=4, heads=2, n=8, d=8):
-    return L.ls_tree_commit(P, 2 * P, P, view(), view(), 1, P, P, P, None, 2, layers, rows, nodes, heads, n, d, 2 * P, P, P, P,
-                            None, None, None)
+def commit(rows=2, layers=1, nodes=4, heads=2, n=8, d=8, out_len=2 * P, finished=None, out_finished=None):
+    return L.ls_tree_commit(P, 2 * P, P, view(), view(), 1, P, P, P, finished, 2, layers, rows, nodes, heads, n, d, out_len,
+                            P, P, P, out_finished, None, None)
 print("status", EXPR)
 """
 
@@ -77,3 +77,10 @@ def test_positions_of_a_row(call):
         assert call(f"cross(n={n})") == UNSUPPORTED
         assert call(f"tree(n={n})") == UNSUPPORTED
         assert call(f"cross(n={n}, b=0)") == 0 and call(f"tree(n={n}, rows=0)") == 0
+
+
+def test_outputs_that_every_layer_reads(call):
+    """A layer's block may run after the first one's results are written."""
+    assert call("commit(out_len=P)") == INVALID  # cache_len itself
+    assert call("commit(layers=6, finished=3 * P, out_finished=3 * P)") == INVALID
+    assert call("commit(layers=1, finished=3 * P + 1, out_finished=3 * P + 1)") == INVALID
