@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   auto bar = [&](int i) { return base + S::BAR + 8u * (uint32_t)i; };
   volatile uint32_t* tmem_at = reinterpret_cast<volatile uint32_t*>(gbase + S::WORDS);
   volatile int* abort = reinterpret_cast<volatile int*>(gbase + S::WORDS + 4);
-  // [2] item + 1, by turns: one slot's softmax may be an item ahead of the other's
+  // [2] item + 1, by turns of the items that have tiles: one slot's softmax may be one such item ahead of
+  // the other's, and any number of items without tiles
   volatile int* bad_values = reinterpret_cast<volatile int*>(gbase + S::WORDS + 8);
 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -272,10 +273,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     int jobs_before = 0, tiles_before = 0, joins = 0, active = 0;
     int sums[2] = {0, 0};  // items before in which the slot had a job
     bool ok = true;
-    int turn = 1;
     for (unsigned it = blockIdx.x; it < (unsigned)p.items && ok; it += gridDim.x) {
-      turn ^= 1;
       const TcItem<N> x = tc_item<N>(p, it, next_len);
+      const int turn = active & 1;
       if (x.len != next_len && tid == 0) atomicOr(p.status, kDevInternal);
       if (it + gridDim.x < p.items) next_len = __ldg(p.len + tc_row(p, it + gridDim.x));
       const int qn = x.wide ? min(kTaM, x.nq - slot * kTaM) : x.nq;  // queries of the slot
