@@ -26,8 +26,8 @@
 //      results in shared memory.
 //
 // What bounds it: the instructions around the products (a block's turn takes some 300 per warp for
-// 8 KB of keys and values), so the number of warps an SM holds counts (12, by registers and by two
-// ring slots each; a third slot in place of the third CTA: 66 against 52 us on the first of these).
+// 8 KB of keys and values), so the number of warps an SM holds counts (12, by two ring slots each
+// and by registers; a third slot in place of the third CTA: 66 against 52 us on the first of these).
 // Single-token step of 1024 beams x 16 heads of 64 elements, 48 to 63 positions: 239 MB in 42 us,
 // 0.84 of the measured copy rate; 128 trees of 13 nodes over 300 to 999 positions: 354 MB in 68 us,
 // 0.77; 64 rows x 8 key heads of 128 elements, 4 queries, 500 to 3000 positions: 460 MB in 86 us,
@@ -114,7 +114,11 @@ struct MmaShape {
   static constexpr int PANEL = KB * 128;               // a block's rows of 64 elements
   static constexpr int STAGE = 2 * PANELS * PANEL;     // keys, then values
   static constexpr bool QREG = NQ * DP <= 256;         // the queries' fragments stay in registers
-  static constexpr int CTAS = NQ * DP <= 64 ? 4 : NQ * DP <= 128 ? 3 : 2;  // per SM, by registers
+  // CTAs per SM: three by the rings, 64 KB a CTA (128 KB for heads above 128: one); two by registers from 32
+  // queries of 64 elements or 16 of 128 on.  (With four as the cap, which the rings do not allow, eight queries
+  // of 64 elements had 128 registers and the first example above took 41.8 us; now 158 registers, 41.6 us.)
+  static constexpr int CTAS = DP > 128 ? 1 : NQ * DP <= 128 ? 3 : 2;
+  static_assert(CTAS * (kMmWarps * NS * STAGE + 1024) <= 228 * 1024, "what an SM's shared memory holds");
 };
 
 // Bytes of one warp's shared memory after its ring, and where the parts begin.  With four warps
