@@ -350,6 +350,7 @@ LS_API ls_status ls_tree_attention(const ls_view* q, const ls_view* cache_key, c
  *              full cache or a tree whose node 0 is not its root (each: the row appends nothing)
  *              sets LS_ERR_INTERNAL in its status word.
  *  The outputs are apart from the inputs.  nodes 1..LS_MAX_NODES.  Nothing is allocated.
+ *  More than 65535 layers, or 2 * nodes * heads * head_dim above 2^30, return LS_ERR_UNSUPPORTED.
  *  rows == 0 is a no-op; layers or heads or head_dim == 0 only finds the branch.
  */
 LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_t* cache_len, const ls_view* draft_key,

@@ -33,12 +33,15 @@
 // What bounds it:
 // - head size 128: the scores' products, which read 6 KB of shared memory per 64-key instruction
 //   (at its 128 bytes a clock 48 cycles, for 32 of tensor work).  509 queries over up to 2048
-//   states, 32 x 16 heads: 203 us, 1165 TFLOP/s, 0.61 of the measured bf16 rate;
-// - head size 64: the softmax's instructions (two warps a scheduler; per score half a multiply-add,
-//   an exponential, half an addition, half a conversion, half a maximum), then the turn from item
-//   to item.  400 queries over up to 1021 states, 24 x 16 heads: 64 us, 530 TFLOP/s;
-// - few queries over long rows: memory.  64 queries over 131000 positions, 8 heads: 537 MB in 86 us
-//   plus 4 us to join the parts, 0.88 of the measured copy rate.
+//   states, 32 x 16 heads: 217 us, 1090 TFLOP/s, 0.57 of the measured bf16 rate;
+// - head size 64: the chain of a job (the wait for its scores, their load, maximum, exponentials, store and
+//   hand-over) with two softmax warps a scheduler: 40% of the issue slots and 28% of the tensor pipe are
+//   used; then the turn from item to item.  400 queries over up to 1021 states, 24 x 16 heads: 63 us,
+//   537 TFLOP/s;
+// - rows of different lengths: items go to CTAs by their index.  32 trees of 64 nodes x 4 query heads over
+//   1025 to 4000 positions, 8 key heads: 107 us, where the longest CTA has 113 key tiles and the mean is 68;
+// - few queries over long rows: memory.  64 queries over 131000 positions, 8 heads: 537 MB in 88 us with
+//   the joining of the parts, 0.90 of the measured copy rate.
 //
 // The accumulator is rescaled only when a query's maximum has grown by more than 2^8 since the
 // last time: until then its weights are at most 2^8 times as large (in f16 2^15, kAtLift), which f32

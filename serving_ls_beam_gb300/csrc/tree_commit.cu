@@ -13,7 +13,8 @@
 // the layout allows, eight copies under way per thread.  Nothing of the rejected nodes is read
 // or written.  256 trees of 31 nodes (1 to 31 confirmed), 6 layers x 16 heads of 64 elements: 90 MB in
 // 25 us, 0.53 of the copy rate; what is left is the chain load - walk - load - store of each CTA
-// (128 threads a CTA: 28 us; twice the parts: 28 us).
+// (128 threads a CTA: 28 us; twice the parts: 28 us).  60 registers a thread: an SM holds four CTAs, and the
+// 1536 of this case are two and a half rounds.
 #include "ls_device.cuh"
 #include "ls_tree.cuh"
 
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kTcThreads) tree_commit_kernel(const CommitPar
 }  // namespace
 
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t stream) {
-  // parts of a (row, layer): one batch per thread at most, within two waves of the GPU
+  // parts of a (row, layer): one batch per thread at most, and not above 16 CTAs per SM, four rounds
   const long long units = 2ll * p.nodes * p.heads * p.vec_units, pairs = (long long)p.rows * p.layers;
   const long long need = (units + kTcThreads * kTcBatch - 1) / (kTcThreads * kTcBatch), room = 2ll * kAtSms * 8 / pairs;
   const long long parts = need < room ? need : room;

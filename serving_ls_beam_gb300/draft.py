@@ -9,7 +9,8 @@ cache and the node's own branch, ``ls_tree_attention``) and, with an encoder, ``
 the nodes' logits, chooses a token after every node (``ls_sample`` with one candidate), finds the
 branch those choices confirm and appends its keys and values to the cache of every layer
 (``ls_tree_commit``).  The result is that of decoding one token at a time; with ``nodes`` = 1 it
-is that.
+is that.  Every row decodes greedily for itself, those of one sentence too: there is no selection
+among beams here (``loop.py`` has it).
 
 Everything stays on the GPU and every buffer is allocated once, so that a step can be captured in a
 CUDA graph (the memory-reuse rule of the LightSeq inference article, 31duo.com, itemid-283120, as
