@@ -50,7 +50,8 @@ typedef enum {
   LS_ERR_INTERNAL = 5     /* device-detected inconsistency, e.g. a parent index out of range */
 } ls_status;
 
-typedef enum { LS_DTYPE_F32 = 0, LS_DTYPE_F16 = 1, LS_DTYPE_BF16 = 2 } ls_dtype;
+/* The 8-bit types are those of a paged cache (ls_pages) only. */
+typedef enum { LS_DTYPE_F32 = 0, LS_DTYPE_F16 = 1, LS_DTYPE_BF16 = 2, LS_DTYPE_E4M3 = 3, LS_DTYPE_I8 = 4 } ls_dtype;
 
 /* Largest beam width supported. */
 #define LS_MAX_K 64
@@ -359,6 +360,128 @@ LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_
                                 int nodes, int heads, int max_len, int head_dim, int32_t* out_len, int32_t* out_path,
                                 int32_t* out_count, int32_t* out_token, uint8_t* out_finished, void* workspace,
                                 void* stream);
+
+/*
+ * Sampling with filters (article: decoding by sampling; ls_sample is its form for up to LS_MAX_K
+ * candidates and one setting for all rows): one token per row, each row with a temperature, a
+ * top-k, a top-p and a min-p of its own, drawn at the caller's uniform.
+ *
+ *  With x = logit + bias, M the row's largest x and w = exp((x - M) / temperature), the tokens in
+ *  the order of falling x (ties: the smaller token first) are cut to
+ *    the first top_k of them,
+ *    of these the shortest prefix whose w reaches top_p of the sum of theirs,
+ *    of these the ones with w >= min_p;
+ *  out_token is the first kept token, in the order of the vocabulary, whose cumulative w exceeds u
+ *  times the kept sum, and out_logprob the logarithm of the probability that it was drawn with,
+ *  log(w / kept sum).
+ *
+ *  logits      [rows, vocab], logit_dtype (f32, f16 or bf16), device: row r at logits + r *
+ *              row_stride elements (row_stride >= vocab); bias [vocab] f32 or NULL.
+ *  u           [rows] f32 in [0, 1).
+ *  temperature [rows] f32 or NULL (1): 0 gives the first largest x with log-probability 0.
+ *  top_k       [rows] int32 or NULL: 0, or vocab and more, keeps all.
+ *  top_p       [rows] f32 or NULL: in (0, 1]; 1 keeps all.
+ *  min_p       [rows] f32 or NULL: in [0, 1]; 0 keeps all.
+ *  out_token   [rows] int32; out_logprob [rows] f32 or NULL.
+ *  workspace   NULL, or a workspace initialised by ls_workspace_init: a parameter outside its range
+ *              (NaN among them) sets LS_ERR_INTERNAL in its status word.  Such a temperature counts
+ *              as 0, such a filter as off.
+ *  Logits of -inf are never drawn, and NaN counts as -inf; a row of nothing else gives token -1 with
+ *  log-probability -inf.  +inf is not supported (no fault; the result is unspecified).  The weights
+ *  are formed to some 2^-30 of their value and summed in integers, in units of at most 2^-44 of the
+ *  largest (vocab up to 2^18; one bit coarser for each doubling): the result does not depend on the
+ *  order of any sum.  A w below that unit counts as 0.
+ *  vocab 1..2^28.  rows == 0 is a no-op.  Nothing is allocated.
+ */
+LS_API ls_status ls_sample_filtered(const void* logits, ls_dtype logit_dtype, int64_t row_stride, const float* bias,
+                                    const float* u, const float* temperature, const int32_t* top_k,
+                                    const float* top_p, const float* min_p, int rows, int vocab, int32_t* out_token,
+                                    float* out_logprob, void* workspace, void* stream);
+
+/*
+ * A cache of keys and values in pages (no counterpart in the article, whose caches hold max_len
+ * positions for every row): position n of row r lies in page table[r * table_row + n / page_size],
+ * at place n % page_size.  Rows may share pages.
+ *
+ *  key, value  views [num_pages, page_size, kv_heads, head_dim] of dtype (`row` is the stride from
+ *              page to page, `pos` from place to place), device.
+ *  dtype       f32, f16 or bf16: the keys and values as they are.  LS_DTYPE_E4M3 or LS_DTYPE_I8:
+ *              8-bit codes, a head vector being its codes times its scale.
+ *  key_scale, value_scale  views [num_pages, page_size, kv_heads] of f32 (the same strides, in f32
+ *              elements), for the 8-bit types; not read otherwise.
+ *  table       [rows, max_pages] int32, device, `table_row` elements from row to row (>= 0).  Of a row
+ *              only the pages of the positions in use are looked up.
+ */
+typedef struct {
+  ls_view key, value, key_scale, value_scale;
+  const int32_t* table;
+  int64_t table_row;
+  ls_dtype dtype;
+  int num_pages, page_size, max_pages, kv_heads, head_dim;
+} ls_pages;
+
+/*
+ * New tokens into a paged cache: token i < count[r] of row r goes to position start[r] + i.
+ *
+ *  key, value  [rows, tokens, kv_heads, head_dim] views of dtype (f32, f16 or bf16; the pages' own type
+ *              where that is not an 8-bit one, and then the copy is bitwise).
+ *  8-bit pages: each head vector is quantised by itself, a the largest |x| of its elements.
+ *    e4m3: scale = the least power of two >= 2^-126 with a <= 448 scale; code = x / scale (exact)
+ *          rounded to the nearest e4m3, ties to even.
+ *    i8:   scale = a times the f32 next to 1 / 127, rounded to f32, 2^-126 at least; code = x / scale
+ *          rounded to the nearest whole number, ties to even (the quotient's own value decides, not
+ *          its f32 rounding), which is at most 127.
+ *  start       [rows] int32; count [rows] int32 or NULL (= tokens everywhere).
+ *  workspace   NULL, or a workspace initialised by ls_workspace_init: a count outside [0, tokens]
+ *              (clamped), a position outside [0, max_pages * page_size) and a page outside
+ *              [0, num_pages) set LS_ERR_INTERNAL in its status word; such tokens are not written.
+ *  Where two tokens go to the same place, each element there is one of theirs.  Elements are finite;
+ *  otherwise their vector's codes are unspecified.  head_dim 1..256.  rows == 0 or tokens == 0 is a
+ *  no-op.  Fastest when every stride and address is a multiple of 16 bytes and head_dim of 16.
+ *  rows * tokens * kv_heads above 2^31 - 1, or max_pages * page_size above 2^31 - 1024, returns
+ *  LS_ERR_UNSUPPORTED.
+ */
+LS_API ls_status ls_paged_write(const ls_view* key, const ls_view* value, ls_dtype dtype, const int32_t* start,
+                                const int32_t* count, const ls_pages* pages, int rows, int tokens, void* workspace,
+                                void* stream);
+
+/*
+ * Positions of a paged cache as dense tensors: position start[r] + i, i < count[r], of row r goes to
+ * key[r, i] and value[r, i].  Everything as in ls_paged_write, in the other direction: key, value are
+ * written where i < count[r] only (a position or page out of range leaves its place as it is); codes
+ * are multiplied by their scale in f32 and the product is rounded to dtype.  start NULL: 0 everywhere.
+ */
+LS_API ls_status ls_paged_read(const ls_pages* pages, const int32_t* start, const int32_t* count, const ls_view* key,
+                               const ls_view* value, ls_dtype dtype, int rows, int tokens, void* workspace,
+                               void* stream);
+
+/*
+ * Attention of one new token per row over its paged cache:
+ *   out[r, h] = sum_n softmax_n(scale * q[r, h] . key_n) value_n,  n < len[r],
+ * key_n and value_n the row's position n in key head h / (heads / kv_heads).  A row of length 0 gives
+ * zeros.
+ *
+ *  q, out      [rows, heads, head_dim] views of dtype (f32, f16 or bf16; the pages' own type where that
+ *              is not an 8-bit one); `pos` is not used.  out's elements are distinct and apart from the inputs.
+ *  len         [rows] int32, device.  A length outside [0, max_pages * page_size] is clamped, and a
+ *              page outside [0, num_pages) is left out; both set LS_ERR_INTERNAL in the status word.
+ *  Positions at or past len are not used, whatever they hold.  Scores, softmax and sums are f32; with q
+ *  in 16 bits the softmax weights are rounded for the product with the values, to f16 for 8-bit pages
+ *  and else to their type (in f16 those under 2^-32 of the largest count in the sum alone), and the
+ *  result is rounded once.
+ *  heads       a multiple of kv_heads; head_dim 1..256.
+ *  workspace   >= ls_paged_attention_workspace_size(rows, heads, kv_heads, head_dim) bytes, 256-byte
+ *              aligned, initialised once by ls_workspace_init; the size grows with heads / kv_heads (up
+ *              to 16) and head_dim only.  Calls sharing it must be ordered.
+ *  Inputs that a query reads are finite; otherwise its result is unspecified (no fault).  rows == 0 is a
+ *  no-op.  Fastest with q in 16 bits, strides and addresses that are multiples of 16 bytes, head_dim of
+ *  16 (16-bit pages: 8), and pages of a multiple of 8 positions.  rows * heads above 2^31 - 1, or max_pages *
+ *  page_size above 2^31 - 1024, returns LS_ERR_UNSUPPORTED.
+ */
+LS_API size_t ls_paged_attention_workspace_size(int rows, int heads, int kv_heads, int head_dim);
+LS_API ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int32_t* len, ls_dtype dtype,
+                                    float scale, int rows, int heads, const ls_view* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * Synchronise `stream`, return the status the device recorded in `workspace` since

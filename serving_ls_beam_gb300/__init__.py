@@ -22,11 +22,14 @@ __all__ = [
     "ls_backtrack",
     "ls_sample_workspace_size", "ls_sample", "ls_cache_refresh_inplace", "ls_logits_beam_step",
     "ls_beam_step_refresh_inplace", "LS_MAX_NODES", "ls_cross_attention_workspace_size", "ls_cross_attention",
-    "ls_tree_attention_workspace_size", "ls_tree_attention", "ls_tree_commit",
+    "ls_tree_attention_workspace_size", "ls_tree_attention", "ls_tree_commit", "LS_DTYPE_E4M3", "LS_DTYPE_I8", "LsPages",
+    "ls_pages", "ls_paged_write", "ls_paged_read", "ls_paged_attention_workspace_size", "ls_paged_attention",
+    "ls_sample_filtered",
 ]
 
 LS_OK, LS_ERR_INVALID_ARG, LS_ERR_UNSUPPORTED, LS_ERR_CUDA, LS_ERR_TIMEOUT, LS_ERR_INTERNAL = range(6)
 LS_DTYPE_F32, LS_DTYPE_F16, LS_DTYPE_BF16 = 0, 1, 2
+LS_DTYPE_E4M3, LS_DTYPE_I8 = 3, 4  # a paged cache's
 LS_MAX_K = 64
 LS_MAX_NODES = 64
 
@@ -43,6 +46,14 @@ class _View(ctypes.Structure):
     """ls_view: a device pointer and the element strides of [layer, row, pos, head, head_dim]."""
     _fields_ = [("data", ctypes.c_void_p), ("layer", ctypes.c_int64), ("row", ctypes.c_int64), ("pos", ctypes.c_int64),
                 ("head", ctypes.c_int64)]
+
+
+class _Pages(ctypes.Structure):
+    """ls_pages: the views of a paged cache, its table and sizes."""
+    _fields_ = [("key", _View), ("value", _View), ("key_scale", _View), ("value_scale", _View),
+                ("table", ctypes.c_void_p), ("table_row", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 def library_path() -> str:
@@ -106,6 +117,17 @@ def load_library():
         lib.ls_tree_commit.argtypes = [vp, vp, vp, view, view, ip, vp, vp, vp, vp, ip, ip, ip, ip, ip, ip, ip, vp, vp,
                                        vp, vp, vp, vp, vp]
         lib.ls_tree_commit.restype = ip
+        pages = ctypes.POINTER(_Pages)
+        lib.ls_paged_write.argtypes = [view, view, ip, vp, vp, pages, ip, ip, vp, vp]
+        lib.ls_paged_write.restype = ip
+        lib.ls_paged_read.argtypes = [pages, vp, vp, view, view, ip, ip, ip, vp, vp]
+        lib.ls_paged_read.restype = ip
+        lib.ls_paged_attention_workspace_size.argtypes = [ip] * 4
+        lib.ls_paged_attention_workspace_size.restype = sz
+        lib.ls_paged_attention.argtypes = [view, pages, vp, ip, fl, ip, ip, view, vp, sz, vp]
+        lib.ls_paged_attention.restype = ip
+        lib.ls_sample_filtered.argtypes = [vp, ip, ctypes.c_int64, vp, vp, vp, vp, vp, vp, ip, ip, vp, vp, vp, vp]
+        lib.ls_sample_filtered.restype = ip
         _lib = lib
         return lib
 
@@ -373,6 +395,125 @@ def ls_tree_commit(cache_key, cache_value, cache_len, draft_key, draft_value, pa
         _dtype_code(cache_key), parent.data_ptr(), token.data_ptr(), target.data_ptr(), _ptr(finished), eos_id, layers,
         rows, nodes, heads, max_len, dim, out_len.data_ptr(), out_path.data_ptr(), out_count.data_ptr(),
         out_token.data_ptr(), _ptr(out_finished), _ptr(workspace), _stream(stream))
+
+
+class LsPages:
+    """One layer's cache in pages, as the calls below take it: the C structure, made once, and the tensors that it points
+    to.  Holds no state of its own: what the tensors hold may change between calls, their memory may not."""
+
+    __slots__ = ("c", "tensors", "rows", "kv_heads", "head_dim", "dtype", "coded")
+
+    def __init__(self, key, value, table, key_scale=None, value_scale=None):
+        import torch
+
+        codes = {torch.float32: LS_DTYPE_F32, torch.float16: LS_DTYPE_F16, torch.bfloat16: LS_DTYPE_BF16,
+                 torch.float8_e4m3fn: LS_DTYPE_E4M3, torch.int8: LS_DTYPE_I8}
+        if key.dtype not in codes:
+            raise TypeError(f"unsupported dtype {key.dtype}")
+        code = codes[key.dtype]
+        self.coded = code in (LS_DTYPE_E4M3, LS_DTYPE_I8)
+        ok = (key.dim() == 4 and value.shape == key.shape and value.dtype is key.dtype and table.dim() == 2
+              and table.dtype is torch.int32 and (table.shape[1] <= 1 or table.stride(1) == 1)
+              and (key.shape[3] == 1 or key.stride(3) == value.stride(3) == 1)
+              and (key_scale is not None) == (value_scale is not None) == self.coded)
+        if ok and self.coded:
+            ok = (key_scale.shape == key.shape[:3] and value_scale.shape == key.shape[:3]
+                  and key_scale.dtype is torch.float32 and value_scale.dtype is torch.float32)
+        if not ok:
+            _refuse("ls_pages", key, value, table, key_scale, value_scale)
+
+        def view(t):
+            return _View() if t is None else _View(t.data_ptr(), 0, t.stride(0), t.stride(2), t.stride(1))
+
+        pages, heads, size, dim = key.shape
+        self.rows, self.kv_heads, self.head_dim, self.dtype = table.shape[0], heads, dim, key.dtype
+        self.tensors = (key, value, table, key_scale, value_scale)
+        self.c = _Pages(view(key), view(value), view(key_scale), view(value_scale), table.data_ptr(), table.stride(0), code,
+                        pages, size, table.shape[1], heads, dim)
+
+
+def ls_pages(key, value, table, key_scale=None, value_scale=None) -> LsPages:
+    """A cache's pages key, value [num_pages, kv_heads, page_size, head_dim] (f32, f16, bf16, float8_e4m3fn or int8; strided
+    views with the last dimension contiguous, so a [num_pages, page_size, kv_heads, head_dim] tensor goes in as its
+    transpose(1, 2)), for the 8-bit types with the scales [num_pages, kv_heads, page_size] f32 (strided views too), and the
+    table [rows, max_pages] int32 of each row's pages."""
+    return LsPages(key, value, table, key_scale, value_scale)
+
+
+def _paged_dense(what, key, value, pages, start, count) -> None:
+    import torch
+
+    i32 = torch.int32
+    if not (key.dim() == 4 and key.shape[0] == pages.rows and key.shape[2] == pages.kv_heads and key.shape[3] == pages.head_dim
+            and value.shape == key.shape and value.dtype is key.dtype and (pages.coded or key.dtype is pages.dtype)
+            and (key.shape[3] == 1 or key.stride(3) == value.stride(3) == 1)
+            and (start is None or _index(start, (pages.rows,), i32)) and (count is None or _index(count, (pages.rows,), i32))):
+        _refuse(what, key, value, start, count)
+
+
+def ls_paged_write(key, value, start, count, pages: LsPages, workspace=None, stream=None) -> int:
+    """New tokens key, value [rows, tokens, kv_heads, head_dim] (f32, f16 or bf16 strided views; the pages' own type where
+    that is not an 8-bit one) to the positions start [rows] int32 and on of their rows' pages, the first count [rows] int32
+    of each row (None: all), quantised where the pages have 8 bits."""
+    _paged_dense("ls_paged_write", key, value, pages, start, count)
+    sk, sv = key.stride(), value.stride()
+    return load_library().ls_paged_write(
+        _View(key.data_ptr(), 0, sk[0], sk[1], sk[2]), _View(value.data_ptr(), 0, sv[0], sv[1], sv[2]), _dtype_code(key),
+        _ptr(start), _ptr(count), pages.c, pages.rows, key.shape[1], _ptr(workspace), _stream(stream))
+
+
+def ls_paged_read(pages: LsPages, start, count, key, value, workspace=None, stream=None) -> int:
+    """Positions start (None: 0) and on of every row, count [rows] int32 (None: all) of them, into key, value [rows, tokens,
+    kv_heads, head_dim] (f32, f16 or bf16 strided views); what lies behind a row's count stays as it is."""
+    _paged_dense("ls_paged_read", key, value, pages, start, count)
+    sk, sv = key.stride(), value.stride()
+    return load_library().ls_paged_read(
+        pages.c, _ptr(start), _ptr(count), _View(key.data_ptr(), 0, sk[0], sk[1], sk[2]),
+        _View(value.data_ptr(), 0, sv[0], sv[1], sv[2]), _dtype_code(key), pages.rows, key.shape[1], _ptr(workspace),
+        _stream(stream))
+
+
+def ls_paged_attention_workspace_size(rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load_library().ls_paged_attention_workspace_size(rows, heads, kv_heads, head_dim))
+
+
+def ls_paged_attention(q, pages: LsPages, length, out, workspace, scale: float | None = None, stream=None) -> int:
+    """Attention of one new token per row: q, out [rows, heads, head_dim] (strided views, last dimension contiguous) over the
+    positions < length [rows] int32 of the rows' pages.  scale: 1/sqrt(head_dim) by default.  workspace:
+    ls_paged_attention_workspace_size() bytes."""
+    import torch
+
+    shape, dt = q.shape, q.dtype
+    rows, heads, dim = shape
+    sq, so = q.stride(), out.stride()
+    if not (rows == pages.rows and dim == pages.head_dim and heads % pages.kv_heads == 0 and out.shape == shape
+            and out.dtype is dt and (pages.coded or pages.dtype is dt) and _index(length, (rows,), torch.int32)
+            and (dim == 1 or sq[2] == so[2] == 1)):
+        _refuse("ls_paged_attention", q, length, out)
+    return load_library().ls_paged_attention(
+        _View(q.data_ptr(), 0, sq[0], 0, sq[1]), pages.c, length.data_ptr(), _dtype_code(q),
+        dim ** -0.5 if scale is None else scale, rows, heads, _View(out.data_ptr(), 0, so[0], 0, so[1]),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def ls_sample_filtered(logits, bias, u, temperature, top_k, top_p, min_p, out_token, out_logprob=None, workspace=None,
+                       stream=None) -> int:
+    """One token per row of logits [rows, vocab] (f32/f16/bf16; rows may be strided) with a temperature, top_k (0: off), top_p
+    and min_p of its own: each [rows] (top_k int32, the others f32) or None for off, drawn at u [rows] f32.  bias [vocab]
+    f32 or None, out_token [rows] int32, out_logprob [rows] f32 or None: of the probability that it was drawn with."""
+    import torch
+
+    rows, vocab = logits.shape
+    f32, i32, row = torch.float32, torch.int32, (rows,)
+    if not ((vocab <= 1 or logits.stride(1) == 1) and (bias is None or _index(bias, (vocab,), f32)) and _index(u, row, f32)
+            and (temperature is None or _index(temperature, row, f32)) and (top_k is None or _index(top_k, row, i32))
+            and (top_p is None or _index(top_p, row, f32)) and (min_p is None or _index(min_p, row, f32))
+            and _index(out_token, row, i32) and (out_logprob is None or _index(out_logprob, row, f32))):
+        _refuse("ls_sample_filtered", logits, bias, u, temperature, top_k, top_p, min_p, out_token, out_logprob)
+    return load_library().ls_sample_filtered(
+        _ptr(logits), _dtype_code(logits), logits.stride(0) if rows > 1 else vocab, _ptr(bias), _ptr(u), _ptr(temperature),
+        _ptr(top_k), _ptr(top_p), _ptr(min_p), rows, vocab, _ptr(out_token), _ptr(out_logprob), _ptr(workspace),
+        _stream(stream))
 
 
 def ls_read_status(workspace, stream=None) -> int:
