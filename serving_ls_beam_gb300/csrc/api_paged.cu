@@ -120,7 +120,10 @@ ls_status move(const ls_view* key, const ls_view* value, ls_dtype dtype, const i
 }
 
 // Rows of partial sums: two places for each worker of the largest launch, of up to 16 queries.
-long long part_rows(int group) { return 2ll * (kPgMaxWorkers + 1) * (group < kPgMaxTile ? group : kPgMaxTile); }
+long long part_rows(int group, int dim) {
+  const int most = dim <= 64 ? kPgMaxWorkers : kPgMaxWorkers / 4 * 3;  // (paged_mma_ctas, paged_simt_ctas)
+  return 2ll * (most + 1) * (group < kPgMaxTile ? group : kPgMaxTile);
+}
 
 }  // namespace
 
@@ -138,7 +141,7 @@ ls_status ls_paged_read(const ls_pages* pages, const int32_t* start, const int32
 
 size_t ls_paged_attention_workspace_size(int rows, int heads, int kv_heads, int head_dim) {
   if (rows < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 || head_dim > kAtMaxDim) return 0;
-  return kPgHeader + (size_t)kPgMaxWorkers * 4 + (size_t)part_rows(heads / kv_heads) * (size_t)(head_dim + 2) * 4;
+  return kPgHeader + (size_t)kPgMaxWorkers * 4 + (size_t)part_rows(heads / kv_heads, head_dim) * (size_t)(head_dim + 2) * 4;
 }
 
 ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int32_t* len, ls_dtype dtype, float scale, int rows,
@@ -170,19 +173,24 @@ ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int3
   p.group = heads / pages->kv_heads;
   p.dim = pages->head_dim;
   p.part_ml = reinterpret_cast<float2*>(p.arrived + kPgMaxWorkers);
-  p.part_o = reinterpret_cast<float*>(p.part_ml + part_rows(p.group));
+  p.part_o = reinterpret_cast<float*>(p.part_ml + part_rows(p.group, p.dim));
   const PagedDebug dbg = paged_debug();
   const int ec = bytes_of(pages->dtype);
-  const bool vec = page_lines(p.pages) && p.dim * ec % 16 == 0 && dtype == LS_DTYPE_F32;
-  p.tile = paged_simt_queries(p.group, vec);
+  const bool whole = page_lines(p.pages) && p.dim * ec % 16 == 0;  // 16-byte vectors
+  const bool mma = whole && dtype != LS_DTYPE_F32 && lines(p.q) && lines(p.out) && dbg.kernel != kPgForceSimt;
+  const bool vec = whole && dtype == LS_DTYPE_F32;
+  p.tile = mma ? paged_mma_queries(p.dim, p.group) : paged_simt_queries(p.group, vec);
   p.tiles = (p.group + p.tile - 1) / p.tile;
   if (p.tile > p.group) p.tile = p.group;
   p.per_row = p.kv_heads * p.tiles;
   p.by_tiles.set(p.tiles);
-  int ctas = kAtSms * paged_simt_ctas(p.dim, pages->dtype, vec);
+  int ctas = kAtSms * (mma ? paged_mma_ctas(p.dim, p.group) : paged_simt_ctas(vec, p.tile));
   if (dbg.ctas > 0 && dbg.ctas < ctas) ctas = dbg.ctas;
-  p.workers = ctas;
-  return report_cuda(launch_paged_simt(p, dtype, pages->dtype, vec, static_cast<cudaStream_t>(stream)));
+  const bool by_warp = mma && (dbg.warps ? dbg.warps == 1 : paged_mma_warps(p));
+  p.workers = by_warp ? ctas * kPgWarps : ctas;
+  p.least = by_warp ? 8 : 16;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return report_cuda(mma ? launch_paged_mma(p, dtype, pages->dtype, by_warp, st) : launch_paged_simt(p, dtype, pages->dtype, vec, st));
 }
 
 ls_status ls_sample_filtered(const void* logits, ls_dtype logit_dtype, int64_t row_stride, const float* bias, const float* u,

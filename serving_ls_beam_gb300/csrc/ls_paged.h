@@ -47,7 +47,7 @@ cudaError_t launch_page_read(const PageMoveParams& p, int dtype, int cache, bool
 // part's blocks in turn, or a warp by itself.
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = kPgWarps * 32;
-constexpr int kPgMaxWorkers = 3 * kPgWarps * kAtSms;  // the most workers of a launch: three CTAs per SM, by warps
+constexpr int kPgMaxWorkers = 4 * kPgWarps * kAtSms;  // the most workers of a launch: four CTAs per SM, by warps
 constexpr int kPgMaxTile = 16;          // the most queries of an item
 
 struct PagedParams {
@@ -64,16 +64,17 @@ struct PagedParams {
   int tiles;            // ceil(group / tile)
   int per_row;          // items of a row: kv_heads * tiles
   int workers;
-  int least;            // blocks of a part, where the rows are not long enough for one part per worker
+  int least;            // blocks of a part where there is less than that much work for each worker
   AtDivisor by_tiles;
 };
 // 16-bit queries; every stride and address a multiple of 16 bytes, the vectors of 16
-cudaError_t launch_paged_mma(PagedParams p, int dtype, int cache, bool warps, cudaStream_t stream);
+cudaError_t launch_paged_mma(PagedParams p, int dtype, int cache, bool by_warp, cudaStream_t stream);
 bool paged_mma_warps(const PagedParams& p);
-int paged_mma_queries(int group);
-int paged_mma_ctas(int dim, int group, int cache);  // CTAs that an SM holds
+int paged_mma_queries(int dim, int group);
+int paged_mma_ctas(int dim, int group);  // CTAs that an SM holds
+// any types; vec: f32 queries, every stride and address a multiple of 16 bytes, the vectors of 16
 cudaError_t launch_paged_simt(PagedParams p, int dtype, int cache, bool vec, cudaStream_t stream);
 int paged_simt_queries(int group, bool vec);
-int paged_simt_ctas(int dim, int cache, bool vec);
+int paged_simt_ctas(bool vec, int tile);
 
 }  // namespace lsb

@@ -328,10 +328,9 @@ cudaError_t run_simt_dim(const PagedParams& p, int dtype, cudaStream_t stream) {
 }  // namespace
 
 int paged_simt_queries(int group, bool vec) { return vec && group == 1 ? 1 : 4; }
-int paged_simt_ctas(int, int, bool) { return 2; }
+int paged_simt_ctas(bool vec, int tile) { return vec && tile == 1 ? 3 : 2; }
 
 cudaError_t launch_paged_simt(PagedParams p, int dtype, int cache, bool vec, cudaStream_t stream) {
-  p.least = 16;
   if (vec) {  // f32 queries
     if (cache == CT_F32) return run_simt_dim<CT_F32, true>(p, dtype, stream);
     return cache == CT_E4M3 ? run_simt_dim<CT_E4M3, true>(p, dtype, stream) : run_simt_dim<CT_I8, true>(p, dtype, stream);
