@@ -57,13 +57,13 @@ struct Debug {
   int stage = -1;  // K2 after K0: 1 = stage the batch's slots, 0 = read them in place, -1 = plan
   bool check_ptrs = true;
   AttendDebug attend{0, 0, 0};  // attention: kernel, warps per item, parts of a row's keys (0 = plan)
-  PagedDebug paged{0, 0, 0, 0};
+  PagedDebug paged{0, 0, 0, 0, 0};
 };
 
 // LS_BEAM_DEBUG: comma-separated "exact", "ipplain", "iptma", "ipwords", "ipstatic", "steprefresh", "chunk", "strips",
 // "fused", "nofused", "cluster", "nocluster", "spin=<ns>", "vpl=<4|8|16>", "stages=<2..8>", "parts=<n>", "ipw=<words>",
 // "ipkeff=<parents>", "ipstage=<bytes>", "stage=<0|1>", "nocheck", "atsimt", "atmma", "attc", "atwarps=<1|4>", "atsplits=<n>",
-// "pgsimt", "pgwarps=<1|4>", "pgworkers=<CTAs>", "sfcluster=<1|2|4|8>".
+// "pgsimt", "pgwarps=<1|4>", "pgworkers=<CTAs>", "pgleast=<blocks>", "sfcluster=<1|2|4|8>".
 Debug read_debug() {
   Debug d;
   const char* env = std::getenv("LS_BEAM_DEBUG");
@@ -101,6 +101,7 @@ Debug read_debug() {
     else if (!std::strcmp(tok, "pgsimt")) d.paged.kernel = kPgForceSimt;
     else if (!std::strncmp(tok, "pgwarps=", 8)) d.paged.warps = std::atoi(tok + 8) == 1 ? 1 : 4;
     else if (!std::strncmp(tok, "pgworkers=", 10)) d.paged.ctas = std::atoi(tok + 10);
+    else if (!std::strncmp(tok, "pgleast=", 8)) d.paged.least = std::atoi(tok + 8);
     else if (!std::strncmp(tok, "sfcluster=", 10)) d.paged.cluster = std::atoi(tok + 10);
   }
   if (d.spin_ns < 0) d.spin_ns = 0;

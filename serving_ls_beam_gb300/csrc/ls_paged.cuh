@@ -18,10 +18,10 @@ namespace lsb {
 
 using PgCount = unsigned long long;
 
-// A worker's part of an item: blocks [lo, hi) of nb.
+// A worker's part of an item: blocks [lo, hi).
 struct PgPart {
-  int r, h, i0, nq, len, nb, lo, hi;
-  int parts, part, base;  // of a cut item: their number, this one's, and where their places begin
+  int r, h, i0, nq, len, lo, hi;
+  int parts, part, base;  // the item's parts, this one's number, and (if there are others) where their places begin
 };
 __device__ __forceinline__ int pg_slot(int base, int part) { return 2 * (base + part) + (part == 0); }
 
@@ -34,148 +34,169 @@ __device__ __forceinline__ PgCount pg_scan(PgCount v, int lane) {  // inclusive,
   return v;
 }
 
+struct PgChunk {  // a run of rows: their blocks, and the parts of one item each
+  PgCount blocks, parts;
+};
+struct PgState {  // a warp's place in its share (the same for all lanes; shared memory, read and written now and then)
+  PgCount at, end;      // long rows: blocks; short: parts, by steps of the workers
+  PgCount total, each;  // blocks of all items, and of a worker; `rest` workers have one more between them
+  PgCount row_u;        // blocks before the row that `at` lies in
+  int rest, r, len, nb, item;
+  bool cut;             // long rows
+};
+struct PgShare {
+  PgChunk chunks[32];
+  PgState state[kPgWarps];
+};
+
 template <int KB>
 struct PgWalk {
   const PagedParams& p;
+  PgShare& sh;
+  PgState& st;
   const int worker, lane;
-  int run;              // rows of a lane
-  PgCount before_u, sum_u, before_p, sum_p;  // blocks and parts (of one item) before the lane's rows, and in them
-  PgCount total;        // blocks of all items
-  PgCount at, end;      // long rows: blocks; short: parts, by steps of the workers
-  bool cut;             // long rows
-  // the row that `at` lies in
-  int r, len, nb, next_len;
-  PgCount row_u, row_p;
-  int item;             // of the row, the next to take (long rows)
+  int next_len;         // of the row after (long rows)
 
   __device__ __forceinline__ int keys_of(int row) const { return row < p.rows ? __ldg(p.len + row) : 0; }
   __device__ __forceinline__ int clamp_len(int n) const { return min(max(n, 0), p.pages.places); }
   __device__ __forceinline__ static int blocks_of(int n) { return max((n + KB - 1) / KB, 1); }
   __device__ __forceinline__ int parts_of(int blocks) const { return (blocks + p.least - 1) / p.least; }
 
-  __device__ __forceinline__ PgWalk(const PagedParams& params, int worker_, int lane_) : p(params), worker(worker_), lane(lane_) {
-    run = (p.rows + 31) / 32;
-    PgCount u = 0, n = 0;
-    const int first = min(lane * run, p.rows), last = min(first + run, p.rows);
+  // by all threads of the CTA
+  __device__ __forceinline__ PgWalk(const PagedParams& params, PgShare& share, int worker_, int warp, int lane_)
+      : p(params), sh(share), st(share.state[warp]), worker(worker_), lane(lane_), next_len(0) {
+    {
+      constexpr int PER = kPgThreads / 32;  // threads of a chunk
+      const int c = threadIdx.x / PER, run = (p.rows + 31) / 32;
+      PgCount u = 0, n = 0;
+      const int last = (int)min((long long)(c + 1) * run, (long long)p.rows);
 #pragma unroll 4
-    for (int i = first; i < last; ++i) {
-      const int b = blocks_of(clamp_len(__ldg(p.len + i)));
-      u += b;
-      n += parts_of(b);
+      for (long long i = (long long)c * run + threadIdx.x % PER; i < last; i += PER) {
+        const int b = blocks_of(clamp_len(__ldg(p.len + i)));
+        u += b;
+        n += parts_of(b);
+      }
+#pragma unroll
+      for (int o = 1; o < PER; o <<= 1) {
+        u += __shfl_xor_sync(~0u, u, o);
+        n += __shfl_xor_sync(~0u, n, o);
+      }
+      if (threadIdx.x % PER == 0) sh.chunks[c] = PgChunk{u, n};
     }
-    sum_u = u;
-    sum_p = n;
-    before_u = pg_scan(u, lane);
-    before_p = pg_scan(n, lane);
-    const PgCount all_u = __shfl_sync(~0u, before_u, 31), all_p = __shfl_sync(~0u, before_p, 31);
-    before_u -= u;
-    before_p -= n;
-    total = all_u * p.per_row;
-    const PgCount workers = p.workers;
-    cut = total >= workers * p.least;
-    if (cut) {
-      // worker * total / workers, without the product's overflow
-      const PgCount q = total / workers, rest = total - q * workers;
-      at = q * worker + rest * worker / workers;
-      end = q * (worker + 1) + rest * (worker + 1) / workers;
-      locate();
-      const PgCount off = at - row_u;
-      item = (int)(off / nb);
+    __syncthreads();
+    PgState s;
+    const PgChunk mine = sh.chunks[lane];
+    s.total = __shfl_sync(~0u, pg_scan(mine.blocks, lane), 31) * p.per_row;
+    s.cut = s.total >= (PgCount)p.workers * p.least;
+    s.each = s.total / p.workers;
+    s.rest = (int)(s.total - s.each * p.workers);
+    s.row_u = 0;
+    s.r = s.len = s.nb = s.item = 0;
+    if (s.cut) {
+      s.at = start_of(s, worker);
+      s.end = start_of(s, worker + 1);
+      PgCount unused;
+      locate(s, unused);
+      s.item = (int)((s.at - s.row_u) / s.nb);
     } else {
-      at = worker;
-      end = all_p * p.per_row;
+      s.at = worker;
+      s.end = __shfl_sync(~0u, pg_scan(mine.parts, lane), 31) * p.per_row;
     }
+    if (lane == 0) st = s;
+    __syncwarp();
   }
+  // worker * total / workers, without the product's overflow
+  __device__ __forceinline__ PgCount start_of(const PgState& s, long long w) const { return s.each * w + (PgCount)s.rest * w / (unsigned)p.workers; }
 
-  // The row that holds `at` (blocks, or parts), by all lanes.
-  __device__ __forceinline__ void locate() {
-    const PgCount per = p.per_row, mine = cut ? before_u : before_p, sum = cut ? sum_u : sum_p;
-    const unsigned hit = __ballot_sync(~0u, at >= mine * per && at < (mine + sum) * per);
-    const int src = hit ? __ffs(hit) - 1 : 0;
-    PgCount u = __shfl_sync(~0u, before_u, src), n = __shfl_sync(~0u, before_p, src);
-    const int first = src * run, last = min(first + run, p.rows);
-    for (int i = first;; i += 32) {
-      const int row = i + lane, l = row < last ? clamp_len(__ldg(p.len + row)) : 0, b = row < last ? blocks_of(l) : 0;
-      const int k = row < last ? parts_of(b) : 0;
+  // The row that s.at (blocks, or parts) lies in, by all lanes; row_p: parts before it.
+  __device__ __forceinline__ void locate(PgState& s, PgCount& row_p) {
+    const PgChunk mine = sh.chunks[lane];
+    const PgCount per = p.per_row, up_u = pg_scan(mine.blocks, lane), up_n = pg_scan(mine.parts, lane);
+    const PgCount upto = s.cut ? up_u : up_n;
+    const unsigned over = __ballot_sync(~0u, s.at < upto * per);
+    const int src = over ? __ffs(over) - 1 : 31;
+    PgCount u = __shfl_sync(~0u, up_u - mine.blocks, src), n = __shfl_sync(~0u, up_n - mine.parts, src);
+    const long long run = (p.rows + 31) / 32;
+    const int last = (int)min((src + 1) * run, (long long)p.rows);
+    for (int i = (int)min(src * run, (long long)p.rows);; i += 32) {
+      const int row = i + lane;
+      const bool in = row < last;
+      const int l = in ? clamp_len(__ldg(p.len + row)) : 0, b = in ? blocks_of(l) : 0, k = in ? parts_of(b) : 0;
       const PgCount su = pg_scan((PgCount)b, lane) + u, sn = pg_scan((PgCount)k, lane) + n;
-      const unsigned past = __ballot_sync(~0u, at < (cut ? su : sn) * per);
+      const unsigned past = __ballot_sync(~0u, in && s.at < (s.cut ? su : sn) * per);
       if (past || i + 32 >= last) {
         const int j = past ? __ffs(past) - 1 : 0;
-        r = i + j;
-        len = __shfl_sync(~0u, l, j);
-        nb = __shfl_sync(~0u, b, j);
-        row_u = __shfl_sync(~0u, su - b, j) * per;
+        s.r = i + j;
+        s.len = __shfl_sync(~0u, l, j);
+        s.nb = max(__shfl_sync(~0u, b, j), 1);
+        s.row_u = __shfl_sync(~0u, su - b, j) * per;
         row_p = __shfl_sync(~0u, sn - k, j) * per;
         break;
       }
       u = __shfl_sync(~0u, su, 31);
       n = __shfl_sync(~0u, sn, 31);
     }
-    nb = max(nb, 1);
-    next_len = keys_of(r + 1);
+    if (s.cut) next_len = keys_of(s.r + 1);
   }
 
+  // The next part (by all lanes), or false.
   __device__ __forceinline__ bool next(PgPart& x) {
-    if (at >= end) return false;
-    PgCount item_u;
-    if (cut) {
-      if (item == p.per_row) {
-        ++r;
-        row_u += (PgCount)nb * p.per_row;
-        len = clamp_len(next_len);
-        nb = blocks_of(len);
-        next_len = keys_of(r + 1);
-        item = 0;
+    PgState s = st;
+    if (s.at >= s.end) return false;
+    if (s.cut) {
+      if (s.item == p.per_row) {
+        ++s.r;
+        s.row_u += (PgCount)s.nb * p.per_row;
+        s.len = clamp_len(next_len);
+        s.nb = blocks_of(s.len);
+        s.item = 0;
+        next_len = keys_of(s.r + 1);
       }
-      item_u = row_u + (PgCount)item * nb;
-      x.lo = (int)(at - item_u);
-      x.hi = (int)min((PgCount)nb, x.lo + (end - at));
-    } else {
-      locate();
-      const int k = parts_of(nb);
-      const PgCount off = at - row_p;
-      item = (int)(off / k);
-      x.part = (int)(off - (PgCount)item * k);
-      x.lo = x.part * p.least;
-      x.hi = min(x.lo + p.least, nb);
-      item_u = row_u + (PgCount)item * nb;
-    }
-    x.r = r;
-    x.h = p.by_tiles(item);
-    x.i0 = (item - x.h * p.tiles) * p.tile;
-    x.nq = min(p.tile, p.group - x.i0);
-    x.len = len;
-    x.nb = nb;
-    x.parts = 1;
-    if (x.lo > 0 || x.hi < nb) {
-      if (cut) {
-        const PgCount w = p.workers;
-        x.base = owner(item_u, w);
-        x.parts = owner(item_u + nb - 1, w) - x.base + 1;
+      const PgCount item_u = s.row_u + (PgCount)s.item * s.nb;
+      x.lo = (int)(s.at - item_u);
+      x.hi = (int)min((PgCount)s.nb, x.lo + (s.end - s.at));
+      x.parts = 1;
+      if (x.lo > 0 || x.hi < s.nb) {
+        x.base = owner(s, item_u);
+        x.parts = owner(s, item_u + s.nb - 1) - x.base + 1;
         x.part = worker - x.base;
-      } else {
-        x.base = (int)(item_u / p.least);
-        x.parts = parts_of(nb);
       }
-    }
-    if (cut) {
-      at += x.hi - x.lo;
-      if (x.hi == nb) ++item;
     } else {
-      at += p.workers;
+      PgCount row_p;
+      locate(s, row_p);
+      const int k = parts_of(s.nb);
+      const unsigned off = (unsigned)(s.at - row_p);  // (below parts of an item * items of a row, on the short path)
+      s.item = (int)(off / (unsigned)k);
+      x.part = (int)(off - (unsigned)s.item * k);
+      x.lo = x.part * p.least;
+      x.hi = min(x.lo + p.least, s.nb);
+      x.parts = k;
+      x.base = k > 1 ? (int)((s.row_u + (PgCount)s.item * s.nb) / p.least) : 0;
     }
+    x.r = s.r;
+    x.h = p.by_tiles(s.item);
+    x.i0 = (s.item - x.h * p.tiles) * p.tile;
+    x.nq = min(p.tile, p.group - x.i0);
+    x.len = s.len;
+    if (s.cut) {
+      s.at += x.hi - x.lo;
+      if (x.hi == s.nb) ++s.item;
+    } else {
+      s.at += p.workers;
+    }
+    __syncwarp();
+    if (lane == 0) st = s;
+    __syncwarp();
     return true;
   }
 
-  // The worker whose run holds block u: the last c with floor(c total / workers) <= u.
-  __device__ __forceinline__ int owner(PgCount u, PgCount workers) const {
-    const PgCount q = total / workers, rest = total - q * workers;
-    // an estimate, put right against the exact bounds
-    long long c = (long long)((double)(u + 1) * (double)workers / (double)total);
-    c = max(0ll, min(c, (long long)workers - 1));
-    while (c + 1 < (long long)workers && q * (c + 1) + rest * (c + 1) / workers <= u) ++c;
-    while (c > 0 && q * c + rest * c / workers > u) --c;
-    return (int)c;
+  // The worker whose run holds block u: the last w with start_of(w) <= u.  An estimate, put right.
+  __device__ __forceinline__ int owner(const PgState& s, PgCount u) const {
+    long long w = (long long)((float)u * (float)p.workers / (float)s.total);
+    w = max(0ll, min(w, (long long)p.workers - 1));
+    while (w + 1 < p.workers && start_of(s, w + 1) <= u) ++w;
+    while (w > 0 && start_of(s, w) > u) --w;
+    return (int)w;
   }
 };
 
@@ -230,41 +251,70 @@ __device__ __forceinline__ bool pg_last(const PagedParams& p, const PgPart& x, i
   return last;
 }
 
-// The parts of an item added up, in their order, by N threads.
-__device__ __forceinline__ void pg_join(const PagedParams& p, const PgPart& x, int dtype, int t, int n) {
-  const bool four = p.dim % 4 == 0;
-  const int step = four ? 4 : 1, per = p.dim / step;
-  for (int e = t; e < x.nq * per; e += n) {
-    const int q = e / per, d = (e - q * per) * step;
+// The parts of an item added up, in their order, by `warps` warps, a query each.  The lanes first take a part each
+// for its factor, then the elements, 8 parts' loads under way at once.
+template <int EL>  // elements of a lane's load: 4 where the head size is a multiple of 4
+__device__ __forceinline__ void pg_join_by(const PagedParams& p, const PgPart& x, int dtype, int warp, int warps, int lane) {
+  const int es = dtype == DT_F32 ? 4 : 2;
+  for (int q = warp; q < x.nq; q += warps) {
     float m = -INFINITY;
-    for (int j = 0; j < x.parts; ++j) m = fmaxf(m, __ldcg(p.part_ml + (long long)pg_slot(x.base, j) * p.tile + q).x);
-    const float sub = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int j = 0; j < x.parts; ++j) {
-      const long long at = (long long)pg_slot(x.base, j) * p.tile + q;
-      const float2 ml = __ldcg(p.part_ml + at);
-      const float f = fast_exp2(ml.x - sub);
-      const float* from = p.part_o + at * p.dim + d;
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (four) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
-        v[0] = y.x;
-        v[1] = y.y;
-        v[2] = y.z;
-        v[3] = y.w;
-      } else {
-        v[0] = __ldcg(from);
-      }
-      l = fmaf(f, ml.y, l);
+    for (int j = lane; j < x.parts; j += 32) m = fmaxf(m, __ldcg(p.part_ml + (long long)pg_slot(x.base, j) * p.tile + q).x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(f, v[i], o[i]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float sub = m == -INFINITY ? 0.0f : m;
+    for (int d0 = 0; d0 < p.dim; d0 += 32 * EL) {
+      const int d = d0 + lane * EL;
+      const bool mine = d < p.dim;
+      float l = 0.0f, o[EL];
+#pragma unroll
+      for (int i = 0; i < EL; ++i) o[i] = 0.0f;
+      for (int j0 = 0; j0 < x.parts; j0 += 32) {
+        float f = 0.0f;
+        if (j0 + lane < x.parts) {
+          const float2 ml = __ldcg(p.part_ml + (long long)pg_slot(x.base, j0 + lane) * p.tile + q);
+          f = fast_exp2(ml.x - sub);
+          l = fmaf(f, ml.y, l);
+        }
+        constexpr int AT_ONCE = 8;
+        for (int k = 0; k < min(32, x.parts - j0); k += AT_ONCE) {
+          float v[AT_ONCE][EL];
+#pragma unroll
+          for (int y = 0; y < AT_ONCE; ++y) {
+            const bool there = mine && j0 + k + y < x.parts;
+            const float* from = p.part_o + ((long long)pg_slot(x.base, there ? j0 + k + y : 0) * p.tile + q) * p.dim + (mine ? d : 0);
+            if constexpr (EL == 4) {
+              const float4 z = there ? __ldcg(reinterpret_cast<const float4*>(from)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              v[y][0] = z.x;
+              v[y][1] = z.y;
+              v[y][2] = z.z;
+              v[y][3] = z.w;
+            } else {
+              v[y][0] = there ? __ldcg(from) : 0.0f;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < AT_ONCE; ++y) {
+            const float fy = __shfl_sync(~0u, f, k + y);
+#pragma unroll
+            for (int i = 0; i < EL; ++i) o[i] = fmaf(fy, v[y][i], o[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(~0u, l, k);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      unsigned char* out = pg_out(p, x, q) + (long long)d * es;
+#pragma unroll
+      for (int i = 0; i < EL; ++i)
+        if (mine) pg_store_as(dtype, out + i * es, o[i] * inv);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    unsigned char* out = pg_out(p, x, q);
-    const int es = dtype == DT_F32 ? 4 : 2;
-    for (int i = 0; i < step; ++i) pg_store_as(dtype, out + (long long)(d + i) * es, o[i] * inv);
   }
+}
+__device__ __forceinline__ void pg_join(const PagedParams& p, const PgPart& x, int dtype, int warp, int warps, int lane) {
+  if (p.dim % 4 == 0)
+    pg_join_by<4>(p, x, dtype, warp, warps, lane);
+  else
+    pg_join_by<1>(p, x, dtype, warp, warps, lane);
 }
 
 // Eight-bit codes as floats.

@@ -24,7 +24,7 @@ struct PageViews {
 // LS_BEAM_DEBUG's choices: the attention kernel, a part's warps, the CTAs; the sampler's CTAs of a row (0 = plan)
 constexpr int kPgForceSimt = 1;
 struct PagedDebug {
-  int kernel, warps, ctas, cluster;
+  int kernel, warps, ctas, least, cluster;
 };
 PagedDebug paged_debug();
 
@@ -68,7 +68,8 @@ struct PagedParams {
   AtDivisor by_tiles;
 };
 // 16-bit queries; every stride and address a multiple of 16 bytes, the vectors of 16
-cudaError_t launch_paged_mma(PagedParams p, int dtype, int cache, bool by_warp, cudaStream_t stream);
+cudaError_t launch_paged_mma(const PagedParams& p, int dtype, int cache, bool by_warp, cudaStream_t stream);
+cudaError_t launch_paged_mma_codes(const PagedParams& p, int dtype, int cache, bool by_warp, cudaStream_t stream);
 bool paged_mma_warps(const PagedParams& p);
 int paged_mma_queries(int dim, int group);
 int paged_mma_ctas(int dim, int group);  // CTAs that an SM holds

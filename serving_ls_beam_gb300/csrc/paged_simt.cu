@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kPgThreads, MQ == 1 ? 3 : 2) paged_simt_kernel
 #pragma unroll
   for (int v = 0; v < V; ++v) cv[v] = (c + LPK * v) * E < p.dim;
   bool bad = false;
-  PgWalk<KB> walk(p, blockIdx.x, lane);
+  __shared__ PgShare share;
+  PgWalk<KB> walk(p, share, blockIdx.x, warp, lane);
   PgPart x;
   while (walk.next(x)) {
     const long long table = (long long)x.r * p.pages.table_row;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kPgThreads, MQ == 1 ? 3 : 2) paged_simt_kernel
       }
     }
     if (x.parts > 1) {
-      if (pg_last(p, x, threadIdx.x, &flag, [] { __syncthreads(); })) pg_join(p, x, dtype, threadIdx.x, kPgThreads);
+      if (pg_last(p, x, threadIdx.x, &flag, [] { __syncthreads(); })) pg_join(p, x, dtype, warp, kPgWarps, lane);
     }
     __syncthreads();
   }

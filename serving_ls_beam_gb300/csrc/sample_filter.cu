@@ -35,7 +35,10 @@ using u64 = unsigned long long;
 constexpr int kSfWarps = kSfThreads / 32;
 constexpr int kSfBins = 2048;
 constexpr int kSfList = 2048;        // entries of the list, in the histogram's place
-constexpr int kSfRank = 512;         // lists up to this are ranked, longer ones sorted by exchanges
+constexpr int kSfRank = 512;         // lists up to this are ranked, longer ones sorted by exchanges; the fewest kept
+                                     // tokens that are drawn by a pass over the row
+constexpr int kSfCoarse = kSfThreads;  // steps of the histogram of maxima, one per thread
+constexpr int kSfListed = 1000;      // the largest top-k that goes by a list alone
 constexpr int kSfSteps = 64;         // steps of an octave in the table of powers
 constexpr float kSfMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number in the low bits
 
@@ -87,16 +90,19 @@ struct Range {
 
 struct Shared {  // fixed part of a CTA's shared memory
   uint2 powers[kSfSteps];
-  u64 warp_sum[kSfWarps];
+  u64 warp_sum[2][kSfWarps];
   float warp_max[kSfWarps];
   u64 publish_sum[4];       // what the cluster's CTAs tell each other, a place per purpose
   float publish_max;
   uint32_t publish_key[2];
-  u64 before;               // of the crossing step
+  u64 before, limit;        // of the crossing step
   int crossing;
   unsigned listed;          // entries of the list (the first CTA's)
   Cut cut;
-  int found;
+  int drawn;                // the list gave the token
+  double min_cut;           // T ln(min_p)
+  float least;              // the smallest x with w >= min_p
+  int found, kept;
   u64 rest;
 };
 
@@ -107,14 +113,13 @@ struct Sampler {
   const FilterParams& p;
   Shared& s;
   unsigned char* store;   // the CTA's share of the row
-  float* unit_max;        // [units]
   u64* unit_sum;          // [units]
   u64* hist;              // [kSfBins], then the list
-  u64* sorted;            // [kSfRank]
+  u64* sorted;            // [kSfRank], then as many weights
   int row, rank, lead, vectors, first_vec;
   const unsigned char* base;  // the row's first 16-byte vector
   RowScale sc;
-  int tid, warp, lane;
+  int tid, warp, lane, flip;
 
   __device__ __forceinline__ void sync() const {
     if constexpr (CL)
@@ -148,35 +153,64 @@ struct Sampler {
     return d;
   }
   __device__ __forceinline__ int index_of(int v, int e) const { return (first_vec + v) * E + e - lead; }
-  __device__ __forceinline__ void values_of(const uint4& d, int v, float (&x)[E]) const {
-    unpack<DT>(d, x);
-    if constexpr (BIAS) {
+  // A vector as it is kept: its bits, or with a bias the sums as f32.  (NaN needs no care: no comparison
+  // holds for it, and a maximum passes it over.)
+  struct Vec {
+    uint4 d[SV / 16];
+  };
+  __device__ __forceinline__ Vec with_bias(const uint4& raw, int v) const {
+    Vec y;
+    if constexpr (!BIAS) {
+      y.d[0] = raw;
+    } else {
+      float x[E];
+      unpack<DT>(raw, x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int i = index_of(v, e);
         if (i >= 0 && i < p.vocab) x[e] += __ldg(p.bias + i);
       }
-    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] == x[e] ? x[e] : -INFINITY;
+      for (int j = 0; j < E / 4; ++j)
+        y.d[j] = make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
+    }
+    return y;
   }
-  __device__ __forceinline__ void get(int v, float (&x)[E]) const {
-    if (!p.resident) {
-      values_of(fetch(v), v, x);
-    } else if constexpr (BIAS) {
-      const float4* from = reinterpret_cast<const float4*>(store + (size_t)v * SV);
+  __device__ __forceinline__ Vec get(int v) const {
+    if (!p.resident) return with_bias(fetch(v), v);
+    Vec y;
+#pragma unroll
+    for (int j = 0; j < SV / 16; ++j) y.d[j] = reinterpret_cast<const uint4*>(store + (size_t)v * SV)[j];
+    return y;
+  }
+  __device__ __forceinline__ static void values_of(const Vec& y, float (&x)[E]) {
+    if constexpr (!BIAS) {
+      unpack<DT>(y.d[0], x);
+    } else {
 #pragma unroll
       for (int j = 0; j < E / 4; ++j) {
-        const float4 y = from[j];
-        x[4 * j] = y.x;
-        x[4 * j + 1] = y.y;
-        x[4 * j + 2] = y.z;
-        x[4 * j + 3] = y.w;
+        x[4 * j] = __uint_as_float(y.d[j].x);
+        x[4 * j + 1] = __uint_as_float(y.d[j].y);
+        x[4 * j + 2] = __uint_as_float(y.d[j].z);
+        x[4 * j + 3] = __uint_as_float(y.d[j].w);
       }
+    }
+  }
+  __device__ __forceinline__ static float max_of(const Vec& y) {
+    if constexpr (!BIAS && DT == DT_F16) {
+      const __half2* h = reinterpret_cast<const __half2*>(&y.d[0]);
+      const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      return fmaxf(-INFINITY, fmaxf(__low2float(m), __high2float(m)));
+    } else if constexpr (!BIAS && DT == DT_BF16) {
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&y.d[0]);
+      const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      return fmaxf(-INFINITY, fmaxf(__low2float(m), __high2float(m)));
     } else {
-      unpack<DT>(*reinterpret_cast<const uint4*>(store + (size_t)v * SV), x);
+      float x[E], m = -INFINITY;
+      values_of(y, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = x[e] == x[e] ? x[e] : -INFINITY;
+      for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);
+      return m;
     }
   }
 
@@ -216,56 +250,52 @@ struct Sampler {
       const u64 t = __shfl_up_sync(~0u, v, o);
       if (lane >= o) v += t;
     }
+    u64* sums = s.warp_sum[flip];
+    flip ^= 1;  // (two in turn: one barrier each)
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    if (lane == 31) s.warp_sum[warp] = v;
-    __syncthreads();
-    u64 before = 0;
-    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-    return v + before;
+    return v + warp_total(lane < warp ? sums[lane & (kSfWarps - 1)] : 0);
   }
   __device__ __forceinline__ u64 block_total(u64 v) {
     v = warp_total(v);
+    u64* sums = s.warp_sum[flip];
+    flip ^= 1;
+    if (lane == 0) sums[warp] = v;
     __syncthreads();
-    if (lane == 0) s.warp_sum[warp] = v;
-    __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int w = 0; w < kSfWarps; ++w) t += s.warp_sum[w];
-    return t;
+    return warp_total(lane < kSfWarps ? sums[lane & (kSfWarps - 1)] : 0);
   }
-  __device__ __forceinline__ u64 row_total(u64 v, int place) {
-    const u64 t = block_total(v);
-    if constexpr (!CL) return t;
-    if (tid == 0) s.publish_sum[place] = t;
+  // the cluster's sum of the CTAs' sums `here` (each the same in all of its threads)
+  __device__ __forceinline__ u64 row_sum_of(u64 here) {
+    if constexpr (!CL) return here;
+    if (tid == 0) s.publish_sum[1] = here;
     sync();
     u64 all = 0;
-    for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[place], c);
+    for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[1], c);
     sync();
     return all;
   }
 
-  // ---- passes over the share: f(v, x) for every vector of the units whose maximum passes `worth`
+  // ---- passes over the share: f(v, x) for the vectors of the warp's units, 32 at a time, where one of them
+  // holds a value that is `worth` it; done(unit) after each
   template <class Worth, class F, class Done>
-  __device__ __forceinline__ void each_unit(Worth worth, F f, Done done) {
+  __device__ __forceinline__ void each_unit(Worth worth, F f, Done done) const {
     for (int un = warp; un < p.units; un += kSfWarps) {
-      if (!worth(unit_max[un])) {
-        done(un, false);
-        continue;
-      }
       for (int i = 0; i < p.unit_vecs; ++i) {
         const int v = (un * p.unit_vecs + i) * 32 + lane;
+        const Vec y = get(v);
+        if (!__any_sync(~0u, worth(max_of(y)))) continue;
         float x[E];
-        get(v, x);
+        values_of(y, x);
         f(v, x);
       }
-      done(un, true);
+      done(un);
     }
   }
 
   __device__ __forceinline__ float load_row() {
     float mine = -INFINITY;
     const int n = p.units * p.unit_vecs;  // groups of 32 vectors
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = 5;
     for (int g0 = warp; g0 < n; g0 += kSfWarps * AHEAD) {
       uint4 d[AHEAD];
 #pragma unroll
@@ -278,40 +308,12 @@ struct Sampler {
         const int g = g0 + a * kSfWarps;
         if (g >= n) break;
         const int v = g * 32 + lane;
-        float x[E], m = -INFINITY;
-        values_of(d[a], v, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);
+        const Vec y = with_bias(d[a], v);
+        mine = fmaxf(mine, max_of(y));
         if (p.resident) {
-          if constexpr (BIAS) {
 #pragma unroll
-            for (int j = 0; j < E / 4; ++j)
-              reinterpret_cast<float4*>(store + (size_t)v * SV)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-          } else {
-            *reinterpret_cast<uint4*>(store + (size_t)v * SV) = d[a];
-          }
+          for (int j = 0; j < SV / 16; ++j) reinterpret_cast<uint4*>(store + (size_t)v * SV)[j] = y.d[j];
         }
-        mine = fmaxf(mine, m);
-        if (p.unit_vecs == 1) {
-#pragma unroll
-          for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-          if (lane == 0) unit_max[g] = m;
-        }
-      }
-    }
-    if (p.unit_vecs > 1) {
-      __syncthreads();
-      for (int un = warp; un < p.units; un += kSfWarps) {
-        float m = -INFINITY;
-        for (int i = 0; i < p.unit_vecs; ++i) {
-          float x[E];
-          get((un * p.unit_vecs + i) * 32 + lane, x);
-#pragma unroll
-          for (int e = 0; e < E; ++e) m = fmaxf(m, x[e]);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        if (lane == 0) unit_max[un] = m;
       }
     }
     return mine;
@@ -329,7 +331,12 @@ struct Sampler {
     if (high) atomicAdd(h + 1, high);
   }
   // The first step at which `base` and the steps up to it reach `limit` (or the last), and the sum before it.
-  __device__ __forceinline__ void cross(u64 base_sum, u64 limit, int& bin, u64& before) {
+  // top_p below 1: the limit is that share of the steps' sum and `more`, of all CTAs.
+  __device__ __forceinline__ void cross(u64 base_sum, u64& limit, int& bin, u64& before, float top_p = 1.0f, u64 more = 0) {
+    if (top_p < 1.0f) {
+      more = block_total(more);
+      if (tid == 0) s.publish_sum[0] = more;
+    }
     sync();
     if (rank == 0) {
       constexpr int PER = kSfBins / kSfThreads;
@@ -344,6 +351,15 @@ struct Sampler {
 #pragma unroll
       for (int i = 0; i < PER; ++i) mine += h[i];
       const u64 upto = scan(mine) + base_sum, from = upto - mine;
+      if (top_p < 1.0f) {
+        if (tid == kSfThreads - 1) {
+          u64 all = upto;
+          for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[0], c);
+          s.limit = share_of(top_p, all);
+        }
+        __syncthreads();
+        limit = s.limit;
+      }
       if (tid == kSfThreads - 1 && upto < limit) {  // not reached: the last step
         s.crossing = kSfBins - 1;
         s.before = upto - h[PER - 1];
@@ -365,6 +381,7 @@ struct Sampler {
     sync();
     bin = *at(&s.crossing, 0);
     before = *at(&s.before, 0);
+    if (top_p < 1.0f) limit = *at(&s.limit, 0);
     sync();  // (the steps are read; the list may take their place)
   }
 
@@ -376,91 +393,87 @@ struct Sampler {
     const uint32_t key = float_ord(x);
     return b >= g.lo && b <= g.hi && key >= g.from && key <= g.to && within.keeps(x, i);
   }
-  __device__ __forceinline__ unsigned gather(const Range& g, const Cut& within) {
-    if (rank == 0 && tid == 0) s.listed = 0;
-    sync();
+  __device__ __forceinline__ static u64 list_key(float x, int i) { return (u64)~float_ord(x) << 32 | (uint32_t)i; }
+  __device__ __forceinline__ static float list_x(u64 key) { return ord_float(~(uint32_t)(key >> 32)); }
+  // The elements that `hit` says, of the vectors with a maximum `worth` it; their number (which may be more than the
+  // list holds).
+  template <class Worth, class Hit>
+  __device__ __forceinline__ unsigned gather(Worth worth, Hit hit) {
     u64* list = at(hist, 0);
     unsigned* listed = at(&s.listed, 0);
     each_unit(
-        [&](float top) {
-          const float t = steps_below(top);
-          return t < sc.t_end && bin_of(t) <= g.hi && top >= within.value && float_ord(top) >= g.from;
-        },
+        worth,
         [&](int v, const float(&x)[E]) {
           unsigned hits = 0;
 #pragma unroll
-          for (int e = 0; e < E; ++e) hits |= (in_range(x[e], index_of(v, e), g, within) ? 1u : 0u) << e;
-          if (!__any_sync(~0u, hits != 0)) return;
+          for (int e = 0; e < E; ++e) hits |= (hit(x[e], index_of(v, e)) ? 1u : 0u) << e;
+          if (hits) {
+            unsigned to = atomicAdd(listed, (unsigned)__popc(hits));
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const bool hit = (hits >> e) & 1u;
-            const unsigned mask = __ballot_sync(~0u, hit);
-            if (!mask) continue;
-            unsigned from = 0;
-            if (lane == __ffs(mask) - 1) from = atomicAdd(listed, (unsigned)__popc(mask));
-            from = __shfl_sync(~0u, from, __ffs(mask) - 1) + __popc(mask & ((1u << lane) - 1u));
-            if (hit && from < kSfList) list[from] = (u64)~float_ord(x[e]) << 32 | (uint32_t)index_of(v, e);
+            for (int e = 0; e < E; ++e)
+              if ((hits >> e) & 1u) {
+                if (to < kSfList) list[to] = list_key(x[e], index_of(v, e));
+                ++to;
+              }
           }
         },
-        [](int, bool) {});
+        [](int) {});
     sync();
-    const unsigned n = *listed;
-    sync();
-    return n;
+    return *listed;
   }
-  __device__ __forceinline__ static float list_x(u64 key) { return ord_float(~(uint32_t)(key >> 32)); }
 
-  // The list's first entry at which the count reaches k or the weight `limit`; top_p (below 1) instead of a limit:
-  // of the weight of the list's first k.  The first CTA works it out, every thread gets the cut.
-  __device__ __forceinline__ Cut finish_list(unsigned n, u64 base_count, u64 k, u64 base_sum, u64 limit, float top_p) {
-    if (rank == 0) {
-      const u64* keys = hist;
-      if (n <= kSfRank) {
-        for (unsigned i = tid; i < n; i += kSfThreads) {
-          const u64 mine = hist[i];
-          unsigned before = 0;
-          for (unsigned j = 0; j < n; ++j) before += hist[j] < mine;
-          sorted[before] = mine;
-        }
-        keys = sorted;
-        __syncthreads();
-      } else {  // bitonic, the places past the list last
-        for (unsigned i = n + tid; i < kSfList; i += kSfThreads) hist[i] = ~0ull;
-        __syncthreads();
-        for (unsigned size = 2; size <= kSfList; size <<= 1)
-          for (unsigned gap = size >> 1; gap; gap >>= 1) {
-            for (unsigned t = tid; t < kSfList / 2; t += kSfThreads) {
-              const unsigned i = 2 * t - (t & (gap - 1)), j = i + gap;
-              const u64 a = hist[i], b = hist[j];
-              if ((a > b) == ((i & size) == 0)) {
-                hist[i] = b;
-                hist[j] = a;
-              }
-            }
-            __syncthreads();
-          }
+  // The list in order, by the first CTA: where it lies then.
+  __device__ __forceinline__ const u64* sort_list(unsigned n) {
+    if (n <= kSfRank) {  // a warp to an entry: how many come before it
+      for (unsigned i = warp; i < n; i += kSfWarps) {
+        const u64 mine = hist[i];
+        unsigned before = 0;
+        for (unsigned j = lane; j < n; j += 32) before += hist[j] < mine;
+        before = __reduce_add_sync(~0u, before);
+        if (lane == 0) sorted[before] = mine;
       }
-      constexpr int PER = kSfList / kSfThreads;
-      const unsigned first = tid * PER;
-      u64 w[PER], mine = 0;
+      __syncthreads();
+      return sorted;
+    }
+    unsigned most = kSfRank;
+    while (most < n) most <<= 1;
+    for (unsigned i = n + tid; i < most; i += kSfThreads) hist[i] = ~0ull;  // last
+    __syncthreads();
+    for (unsigned size = 2; size <= most; size <<= 1)  // bitonic
+      for (unsigned gap = size >> 1; gap; gap >>= 1) {
+        for (unsigned t = tid; t < most / 2; t += kSfThreads) {
+          const unsigned i = 2 * t - (t & (gap - 1)), j = i + gap;
+          const u64 a = hist[i], b = hist[j];
+          if ((a > b) == ((i & size) == 0)) {
+            hist[i] = b;
+            hist[j] = a;
+          }
+        }
+        __syncthreads();
+      }
+    return hist;
+  }
+  static constexpr int kPer = kSfList / kSfThreads;
+  // A thread's entries of the sorted list: one, or kPer next to each other.
+  __device__ __forceinline__ static unsigned entries(unsigned n) { return n <= kSfRank ? 1 : kPer; }
+
+  // The list's first entry at which the count reaches k or the weight `limit`, as the cut.
+  __device__ __forceinline__ Cut finish_list(unsigned n, u64 base_count, u64 k, u64 base_sum, u64 limit) {
+    if (rank == 0) {
+      const u64* keys = sort_list(n);
+      const unsigned per = entries(n), first = tid * per;
+      u64 w[kPer], mine = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        w[i] = first + i < n && base_count + first + i < k ? weight(list_x(keys[first + i])) : 0;
+      for (int i = 0; i < kPer; ++i) {
+        w[i] = i < per && first + i < n && limit != ~0ull ? weight(list_x(keys[first + i])) : 0;
         mine += w[i];
       }
-      const u64 upto = scan(mine);
-      if (top_p < 1.0f) {
-        if (tid == kSfThreads - 1) s.rest = upto;
-        __syncthreads();
-        limit = share_of(top_p, s.rest);
-      }
       if (tid == 0) s.found = (int)n - 1;
-      __syncthreads();
-      u64 run = base_sum + upto - mine;
+      u64 run = scan(mine) + base_sum - mine;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
+      for (int i = 0; i < kPer; ++i) {
         run += w[i];
-        if (first + i < n && (base_count + first + i + 1 >= k || run >= limit)) {
+        if (i < per && first + i < n && (base_count + first + i + 1 >= k || run >= limit)) {
           atomicMin(&s.found, (int)(first + i));
           break;
         }
@@ -476,8 +489,90 @@ struct Sampler {
     sync();
     return c;
   }
-  __device__ __forceinline__ static u64 share_of(float f, u64 all) {  // the least whole number >= f * all
-    const u64 n = (u64)ceil((double)f * (double)all);
+
+  // All filters on a list that holds the row's first k tokens: the draw itself where few are kept, or the cut.
+  __device__ __forceinline__ bool draw_list(unsigned n, unsigned k, float top_p, float least, float u, Cut& cut) {
+    if (rank == 0) {
+      const u64* keys = sort_list(n);
+      const unsigned per = entries(n), first = tid * per;
+      n = min(n, k);
+      u64 w[kPer], mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        w[i] = i < per && first + i < n ? weight(list_x(keys[first + i])) : 0;
+        mine += w[i];
+      }
+      u64* weights = sorted + kSfRank;
+      if (per == 1 && first < n) weights[tid] = mine;
+      if (tid == 0) s.kept = 0;
+      const u64 upto = scan(mine);
+      if (tid == kSfThreads - 1) s.limit = top_p < 1.0f ? share_of(top_p, upto) : ~0ull;
+      __syncthreads();
+      const u64 limit = s.limit;
+      u64 run = upto - mine;
+      unsigned keep = 0;  // this thread's kept entries: those that begin before the limit is reached
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (i < per && first + i < n && run < limit && list_x(keys[first + i]) >= least) ++keep;
+        run += w[i];
+      }
+      keep = __reduce_add_sync(~0u, keep);
+      if (lane == 0 && keep) atomicAdd(&s.kept, (int)keep);
+      __syncthreads();
+      const unsigned kept = s.kept;
+      if (kept <= kSfRank && per == 1) {
+        if (tid == kept - 1) s.rest = upto;
+        __syncthreads();
+        const u64 all = s.rest;
+        bool cut_off;
+        const u64 target = min(part_of(u, all, cut_off), all - 1);
+        for (unsigned i = warp; i < kept; i += kSfWarps) {
+          const uint32_t index = (uint32_t)keys[i];
+          u64 up = 0;
+          for (unsigned j = lane; j < kept; j += 32)
+            if ((uint32_t)keys[j] <= index) up += weights[j];
+          up = warp_total(up);
+          if (lane == 0 && up > target && up - weights[i] <= target) write(index, weights[i], all);
+        }
+        if (tid == 0) s.drawn = 1;
+      } else if (tid == 0) {
+        const u64 key = keys[max((int)kept - 1, 0)];
+        s.cut = Cut{list_x(key), (int)(uint32_t)key};
+        s.drawn = 0;
+      }
+    }
+    sync();
+    const bool drawn = *at(&s.drawn, 0);
+    cut = *at(&s.cut, 0);
+    sync();
+    return drawn;
+  }
+  __device__ __forceinline__ void write(int token, u64 w, u64 all) const {
+    p.out_token[row] = token;
+    // (near 1 from what is missing)
+    if (p.out_logprob) p.out_logprob[row] = w > all / 2 ? log1pf(-((float)(all - w) / (float)all)) : logf((float)w / (float)all);
+  }
+  // f * all, f in [0, 1], rounded down to a whole number; rest: whether anything was cut off.  (f is a whole
+  // number of 24 bits times a power of two: the product is exact, and FP64 is slow on this part.)
+  __device__ __forceinline__ static u64 part_of(float f, u64 all, bool& rest) {
+    const uint32_t bits = __float_as_uint(f), exponent = bits >> 23;
+    const u64 whole = exponent ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+    const int down = 150 - (int)max(exponent, 1u);  // f = whole / 2^down, 23 <= down <= 149
+    const u64 high = __umul64hi(all, whole), low = all * whole;
+    if (down >= 128) {
+      rest = (high | low) != 0;
+      return 0;
+    }
+    if (down >= 64) {
+      rest = low != 0 || (high & ((1ull << (down - 64)) - 1)) != 0;
+      return high >> (down - 64);
+    }
+    rest = (low & ((1ull << down) - 1)) != 0;
+    return high << (64 - down) | low >> down;
+  }
+  __device__ __forceinline__ static u64 share_of(float f, u64 all) {  // the least whole number >= f * all, 1 at least
+    bool rest;
+    const u64 n = part_of(f, all, rest) + rest;
     return min(max(n, 1ull), all);
   }
 
@@ -520,7 +615,7 @@ struct Sampler {
         for (int i = 0; i < p.unit_vecs; ++i) {
           const int v = (un * p.unit_vecs + i) * 32 + lane;
           float x[E];
-          get(v, x);
+          values_of(get(v), x);
           u64 w[E], sum2 = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -559,7 +654,7 @@ struct Sampler {
     return token;
   }
 
-  // The units' sums of f (over units whose maximum passes `worth`); the CTA's sum for every thread.
+  // The units' sums of f; the CTA's sum for every thread.
   template <class Worth, class F>
   __device__ __forceinline__ u64 sum_units(Worth worth, F f) {
     u64 run = 0, all = 0;
@@ -569,8 +664,8 @@ struct Sampler {
 #pragma unroll
           for (int e = 0; e < E; ++e) run += f(x[e], index_of(v, e));
         },
-        [&](int un, bool any) {
-          const u64 t = any ? warp_total(run) : 0;
+        [&](int un) {
+          const u64 t = __any_sync(~0u, run != 0) ? warp_total(run) : 0;
           if (lane == 0) unit_sum[un] = t;
           all += t;
           run = 0;
@@ -578,37 +673,54 @@ struct Sampler {
     return block_total(lane == 0 ? all : 0);
   }
 
-  // The cut at which the count (by weight: the weights' sum) over the tokens `within` reaches `limit`.
+  // The cut at which the count (MASS: the weights' sum) over the tokens `within` reaches `limit` (top_p of their sum).
   template <bool MASS>
-  __device__ __forceinline__ Cut select(u64 limit, const Cut& within) {
+  __device__ __forceinline__ Cut select(u64 limit, float top_p, const Cut& within, float thread_max) {
     auto value = [&](float x) -> u64 { return MASS ? weight(x) : 1ull; };
+    auto worth = [&](float top) { return top >= within.value && steps_below(top) < sc.t_end; };
     clear_hist();
-    each_unit([&](float top) { return top >= within.value && steps_below(top) < sc.t_end; },
+    u64 small = 0, border = 0;
+    if constexpr (MASS) {
+      // Weights under (1 - top_p) / vocab of the sum are together under 1 - top_p of it: the limit is passed before
+      // them, and they need no steps.  The sum is at least that of the threads' maxima, where all are within.
+      if (within.value == -INFINITY) {
+        const u64 some = row_sum_of(block_total(weight(thread_max)));
+        border = (u64)((1.0f - top_p) * 0.99f * (float)some / (float)p.vocab);
+      }
+    }
+    each_unit(worth,
               [&](int v, const float(&x)[E]) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                   const float t = steps_below(x[e]);
                   if (t < sc.t_end && within.keeps(x[e], index_of(v, e))) {
-                    if constexpr (MASS)
-                      add_to(bin_of(t), weight(x[e]));
-                    else
+                    if constexpr (MASS) {
+                      const u64 w = weight(x[e]);
+                      if (w < border)
+                        small += w;
+                      else
+                        add_to(bin_of(t), w);
+                    } else {
                       atomicAdd(reinterpret_cast<uint32_t*>(hist + bin_of(t)), 1u);
+                    }
                   }
                 }
               },
-              [](int, bool) {});
+              [](int) {});
     int bin;
     u64 before;
-    cross(0, limit, bin, before);
+    cross(0, limit, bin, before, MASS ? top_p : 1.0f, small);
     Range g{bin, bin, 0u, ~0u};
     // (each round divides the keys by 2048: three end it)
     for (int round = 0; round < 5; ++round) {
-      const unsigned n = gather(g, within);
-      if (n <= kSfList)
-        return MASS ? finish_list(n, 0, ~0ull, before, limit, 1.0f) : finish_list(n, before, limit, 0, ~0ull, 1.0f);
+      if (rank == 0 && tid == 0) s.listed = 0;
+      sync();
+      const unsigned n = gather([&](float top) { return worth(top) && bin_of(steps_below(top)) <= g.hi && float_ord(top) >= g.from; },
+                                [&](float x, int i) { return in_range(x, i, g, within); });
+      sync();
+      if (n <= kSfList) return MASS ? finish_list(n, 0, ~0ull, before, limit) : finish_list(n, before, limit, 0, ~0ull);
       // too many: by the bits of x
       uint32_t least = ~0u, most = 0;
-      auto worth = [&](float top) { return top >= within.value && steps_below(top) < sc.t_end; };
       each_unit(worth,
                 [&](int v, const float(&x)[E]) {
 #pragma unroll
@@ -618,7 +730,7 @@ struct Sampler {
                       most = max(most, float_ord(x[e]));
                     }
                 },
-                [](int, bool) {});
+                [](int) {});
       least = __reduce_min_sync(~0u, least);
       most = __reduce_max_sync(~0u, most);
       if (tid == 0) {
@@ -656,7 +768,7 @@ struct Sampler {
                   for (int e = 0; e < E; ++e)
                     if (in_range(x[e], index_of(v, e), g, within)) add_to((int)((most - float_ord(x[e])) >> down), value(x[e]));
                 },
-                [](int, bool) {});
+                [](int) {});
       const u64 base_sum = before;
       cross(base_sum, limit, bin, before);
       g.to = most - ((uint32_t)bin << down);
@@ -665,17 +777,6 @@ struct Sampler {
     }
     return within;
   }
-  // the cluster's sum of the CTAs' sums `here` (the same in all of a CTA's threads)
-  __device__ __forceinline__ u64 row_sum_of(u64 here) {
-    if constexpr (!CL) return here;
-    if (tid == 0) s.publish_sum[1] = here;
-    sync();
-    u64 all = 0;
-    for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[1], c);
-    sync();
-    return all;
-  }
-
   __device__ __forceinline__ void run() {
     for (int j = tid; j < kSfSteps; j += kSfThreads) s.powers[j] = make_uint2(c_powers.whole[j], __float_as_uint(c_powers.value[j]));
     // the row's settings
@@ -691,6 +792,8 @@ struct Sampler {
     if (bad && rank == 0 && tid == 0 && p.status) atomicOr(p.status, kDevInternal);
     if (temp == 0.0f) top_k = 1, top_p = 1.0f, min_p = 0.0f, temp = 1.0f;
     if (top_k >= p.vocab) top_k = 0;
+    if (min_p > 0.0f && tid == kSfThreads - 1) s.min_cut = (double)temp * log((double)min_p);  // (once: FP64 is slow)
+    for (int i = tid; i < kSfCoarse / 2; i += kSfThreads) hist[i] = 0;  // (a cluster's CTAs count in the first's)
     const float mine = load_row();
     // the row's maximum
     float m = mine;
@@ -705,7 +808,7 @@ struct Sampler {
       sync();
       for (int c = 0; c < ctas(); ++c) m = fmaxf(m, *at(&s.publish_max, c));
     }
-    if (m == -INFINITY) {
+    if (!(fabsf(m) < INFINITY)) {  // nothing to draw (or +inf, which is not supported)
       if (rank == 0 && tid == 0) {
         p.out_token[row] = -1;
         if (p.out_logprob) p.out_logprob[row] = -INFINITY;
@@ -714,52 +817,62 @@ struct Sampler {
       return;
     }
     sc.top = m;
-    const double c = fmin(92.33248261893502 / (double)temp, 1e30);  // 64 log2(e) / T
-    sc.hi = (float)c;
-    sc.lo = (float)(c - (double)sc.hi);
+    // 64 log2(e) / T as a pair: the quotient, and what it leaves
+    constexpr double kSteps = kSfSteps * 1.4426950408889634073599;
+    constexpr float kStepsHi = (float)kSteps, kStepsLo = (float)(kSteps - (double)kStepsHi);
+    sc.hi = fminf(__fdiv_rn(kStepsHi, temp), 1e30f);
+    sc.lo = sc.hi < 1e30f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-sc.hi, temp, kStepsHi), kStepsLo), temp) : 0.0f;
+    if (min_p > 0.0f) {
+      if (tid == 0) s.least = __double2float_ru((double)m + s.min_cut);
+      __syncthreads();
+    }
     sc.t_end = (float)(kSfSteps * (p.shift + 31));
     sc.per_bin = (float)kSfBins / fminf(sc.t_end, 48.0f * sc.hi);
     Cut cut = cut_none();
-    bool open = true;  // top-p still to do
-    if (top_k > 0 && top_k <= kSfThreads * ctas() / 4) {
-      // the k-th largest of the threads' maxima, by the histogram's steps
-      clear_hist();
-      const float t = steps_below(mine);
-      if (t < sc.t_end) atomicAdd(reinterpret_cast<uint32_t*>(hist + bin_of(t)), 1u);
-      int bin;
-      u64 before;
-      cross(0, top_k, bin, before);
-      const unsigned n = gather(Range{0, bin, 0u, ~0u}, cut);
+    bool open = true;  // the list has not done it
+    if (top_k > 0 && top_k <= kSfListed && (top_k <= kSfThreads * ctas() / 4 || top_k <= vectors / 4)) {
+      // The k-th largest of the threads' maxima, or of the vectors', by coarse steps: at least k tokens lie there
+      // or above, and not many more.
+      const float per_step = (float)kSfCoarse / fminf(sc.t_end, 48.0f * sc.hi);
+      auto* steps = reinterpret_cast<uint32_t*>(at(hist, 0));
+      auto count = [&](float top) {
+        const float t = steps_below(top);
+        if (t < sc.t_end) atomicAdd(steps + (int)fminf(t * per_step, (float)(kSfCoarse - 1)), 1u);
+      };
+      if (top_k <= kSfThreads * ctas() / 4)
+        count(mine);
+      else
+        for (int v = tid; v < p.units * p.unit_vecs * 32; v += kSfThreads) count(max_of(get(v)));
+      sync();
+      if (rank == 0) {
+        const u64 here = reinterpret_cast<const uint32_t*>(hist)[tid], upto = scan(here);
+        if (upto >= top_k && upto - here < top_k) s.crossing = tid;
+        if (tid == kSfThreads - 1 && upto < top_k) s.crossing = -1;
+        if (tid == 0) s.listed = 0;
+      }
+      sync();
+      const int step = *at(&s.crossing, 0);
+      // (a little below the step: a lower bound is all it has to be)
+      float bound = __fsub_rd(m, __fdiv_rn((float)(step + 1) * 1.001f, per_step * sc.hi));
+      if (step < 0 || !(bound <= m)) bound = -INFINITY;
+      const unsigned n = gather([&](float top) { return top >= bound; }, [&](float x, int) { return x >= bound && x > -INFINITY; });
+      if constexpr (CL) sync();  // (the first CTA's counter has been read)
       if (n <= kSfList) {
-        cut = finish_list(n, 0, top_k, 0, ~0ull, top_p);
         open = false;
+        if (draw_list(n, top_k, top_p, min_p > 0.0f ? s.least : -INFINITY, u, cut)) return;
       }
     }
-    if (open && top_k > 0) cut = select<false>(top_k, cut);
-    if (open && top_p < 1.0f) {
-      const Cut by_k = cut;
-      const u64 here = sum_units([&](float top) { return top >= by_k.value; },
-                                 [&](float x, int i) -> u64 { return by_k.keeps(x, i) ? weight(x) : 0ull; });
-      cut = select<true>(share_of(top_p, row_sum_of(here)), by_k);
-    }
-    if (min_p > 0.0f) {
-      const float least = __double2float_ru((double)m + (double)temp * log((double)min_p));
-      if (least > cut.value) cut = Cut{least, 0x7fffffff};
-    }
+    if (open && top_k > 0) cut = select<false>(top_k, 1.0f, cut, mine);
+    if (open && top_p < 1.0f) cut = select<true>(0, top_p, cut, mine);
+    if (min_p > 0.0f && s.least > cut.value) cut = Cut{s.least, 0x7fffffff};
     auto kept = [&](float x, int i) -> u64 { return cut.keeps(x, i) ? weight(x) : 0ull; };
     const u64 here = sum_units([&](float top) { return top >= cut.value; }, kept);
     const u64 all = row_sum_of(here);
-    u64 target = (u64)((double)u * (double)all);
-    target = min(target, all - 1);
+    bool cut_off;
+    const u64 target = min(part_of(u, all, cut_off), all - 1);
     u64 w;
     const int token = locate(kept, here, target, w);
-    if (rank == 0 && tid == 0) {
-      p.out_token[row] = token;
-      if (p.out_logprob) {
-        // near 1 from what is missing
-        p.out_logprob[row] = w > all / 2 ? log1pf(-((float)(all - w) / (float)all)) : logf((float)w / (float)all);
-      }
-    }
+    if (rank == 0 && tid == 0) write(token, w, all);
   }
 };
 
@@ -773,19 +886,18 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filter_kernel(const __gr
   unsigned char* after = sf_raw + stored;
   u64* hist = reinterpret_cast<u64*>(after);
   u64* sorted = hist + kSfBins;
-  u64* unit_sum = sorted + kSfRank;
-  float* unit_max = reinterpret_cast<float*>(unit_sum + p.units);
+  u64* unit_sum = sorted + 2 * kSfRank;
   const unsigned char* at = p.logits + (long long)row * p.row_bytes;
   const unsigned lead_bytes = (unsigned)(reinterpret_cast<uintptr_t>(at) & 15);
   const int lead = (int)(lead_bytes / S::B);
-  S s{p, shared, sf_raw, unit_max, unit_sum, hist, sorted, row, rank, lead, (int)(((long long)lead + p.vocab + S::E - 1) / S::E),
+  S s{p, shared, sf_raw, unit_sum, hist, sorted, row, rank, lead, (int)(((long long)lead + p.vocab + S::E - 1) / S::E),
       rank * p.units * p.unit_vecs * 32, at - lead_bytes, RowScale{}, (int)threadIdx.x, (int)threadIdx.x >> 5,
-      (int)threadIdx.x & 31};
+      (int)threadIdx.x & 31, 0};
   s.run();
 }
 
 size_t filter_smem(const FilterParams& p, int stored_vector) {
-  return (p.resident ? (size_t)p.units * p.unit_vecs * 32 * stored_vector : 0) + (kSfBins + kSfRank) * 8 + (size_t)p.units * 12;
+  return (p.resident ? (size_t)p.units * p.unit_vecs * 32 * stored_vector : 0) + (kSfBins + 2 * kSfRank + (size_t)p.units) * 8;
 }
 
 template <int DT, bool BIAS, bool CL>
