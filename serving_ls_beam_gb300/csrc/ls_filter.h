@@ -6,7 +6,7 @@
 
 namespace lsb {
 
-constexpr int kSfThreads = 512;
+constexpr int kSfThreads = 256;
 constexpr int kSfMaxCluster = 8;
 constexpr int kSfMaxUnits = 2048;  // units of a CTA's share of a row
 
@@ -28,7 +28,12 @@ struct FilterParams {
   int units;                 // of a CTA
   int shift;                 // weights are sums of 2^-(29 + shift) of the largest
   int resident;              // a CTA's share of the row stays in shared memory
+  int thread_vecs;           // vectors of a thread
+  uint32_t thread_magic;     // division by them
+  int thread_shift;
 };
-cudaError_t launch_sample_filter(FilterParams p, int dtype, cudaStream_t stream);
+cudaError_t launch_sample_filter(const FilterParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_sample_filter_f16(const FilterParams& p, cudaStream_t stream);
+cudaError_t launch_sample_filter_bf16(const FilterParams& p, cudaStream_t stream);
 
 }  // namespace lsb

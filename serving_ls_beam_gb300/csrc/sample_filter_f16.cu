@@ -1,0 +1,10 @@
+// Sampling with filters of f16 logits (the kernel is in ls_filter.cuh).
+#include "ls_filter.cuh"
+
+namespace lsb {
+
+cudaError_t launch_sample_filter_f16(const FilterParams& p, cudaStream_t stream) {
+  return p.bias ? plan_filter<DT_F16, true>(p, stream) : plan_filter<DT_F16, false>(p, stream);
+}
+
+}  // namespace lsb
