@@ -401,7 +401,7 @@ class LsPages:
     """One layer's cache in pages, as the calls below take it: the C structure, made once, and the tensors that it points
     to.  Holds no state of its own: what the tensors hold may change between calls, their memory may not."""
 
-    __slots__ = ("c", "tensors", "rows", "kv_heads", "head_dim", "dtype", "coded")
+    __slots__ = ("c", "ref", "tensors", "rows", "row", "kv_heads", "head_dim", "dtype", "coded", "int32")
 
     def __init__(self, key, value, table, key_scale=None, value_scale=None):
         import torch
@@ -430,6 +430,7 @@ class LsPages:
         self.tensors = (key, value, table, key_scale, value_scale)
         self.c = _Pages(view(key), view(value), view(key_scale), view(value_scale), table.data_ptr(), table.stride(0), code,
                         pages, size, table.shape[1], heads, dim)
+        self.ref, self.row, self.int32 = ctypes.byref(self.c), (self.rows,), torch.int32
 
 
 def ls_pages(key, value, table, key_scale=None, value_scale=None) -> LsPages:
@@ -440,37 +441,35 @@ def ls_pages(key, value, table, key_scale=None, value_scale=None) -> LsPages:
     return LsPages(key, value, table, key_scale, value_scale)
 
 
-def _paged_dense(what, key, value, pages, start, count) -> None:
-    import torch
-
-    i32 = torch.int32
-    if not (key.dim() == 4 and key.shape[0] == pages.rows and key.shape[2] == pages.kv_heads and key.shape[3] == pages.head_dim
-            and value.shape == key.shape and value.dtype is key.dtype and (pages.coded or key.dtype is pages.dtype)
-            and (key.shape[3] == 1 or key.stride(3) == value.stride(3) == 1)
-            and (start is None or _index(start, (pages.rows,), i32)) and (count is None or _index(count, (pages.rows,), i32))):
-        _refuse(what, key, value, start, count)
-
-
 def ls_paged_write(key, value, start, count, pages: LsPages, workspace=None, stream=None) -> int:
     """New tokens key, value [rows, tokens, kv_heads, head_dim] (f32, f16 or bf16 strided views; the pages' own type where
     that is not an 8-bit one) to the positions start [rows] int32 and on of their rows' pages, the first count [rows] int32
     of each row (None: all), quantised where the pages have 8 bits."""
-    _paged_dense("ls_paged_write", key, value, pages, start, count)
+    shape, dt, i32, row = key.shape, key.dtype, pages.int32, pages.row
+    rows, tokens, heads, dim = shape
     sk, sv = key.stride(), value.stride()
+    if not (rows == pages.rows and heads == pages.kv_heads and dim == pages.head_dim and value.shape == shape
+            and value.dtype is dt and (pages.coded or dt is pages.dtype) and (dim == 1 or sk[3] == sv[3] == 1)
+            and _index(start, row, i32) and (count is None or _index(count, row, i32))):
+        _refuse("ls_paged_write", key, value, start, count)
     return load_library().ls_paged_write(
         _View(key.data_ptr(), 0, sk[0], sk[1], sk[2]), _View(value.data_ptr(), 0, sv[0], sv[1], sv[2]), _dtype_code(key),
-        _ptr(start), _ptr(count), pages.c, pages.rows, key.shape[1], _ptr(workspace), _stream(stream))
+        start.data_ptr(), _ptr(count), pages.ref, rows, tokens, _ptr(workspace), _stream(stream))
 
 
 def ls_paged_read(pages: LsPages, start, count, key, value, workspace=None, stream=None) -> int:
     """Positions start (None: 0) and on of every row, count [rows] int32 (None: all) of them, into key, value [rows, tokens,
     kv_heads, head_dim] (f32, f16 or bf16 strided views); what lies behind a row's count stays as it is."""
-    _paged_dense("ls_paged_read", key, value, pages, start, count)
+    shape, dt, i32, row = key.shape, key.dtype, pages.int32, pages.row
+    rows, tokens, heads, dim = shape
     sk, sv = key.stride(), value.stride()
+    if not (rows == pages.rows and heads == pages.kv_heads and dim == pages.head_dim and value.shape == shape
+            and value.dtype is dt and (pages.coded or dt is pages.dtype) and (dim == 1 or sk[3] == sv[3] == 1)
+            and (start is None or _index(start, row, i32)) and (count is None or _index(count, row, i32))):
+        _refuse("ls_paged_read", key, value, start, count)
     return load_library().ls_paged_read(
-        pages.c, _ptr(start), _ptr(count), _View(key.data_ptr(), 0, sk[0], sk[1], sk[2]),
-        _View(value.data_ptr(), 0, sv[0], sv[1], sv[2]), _dtype_code(key), pages.rows, key.shape[1], _ptr(workspace),
-        _stream(stream))
+        pages.ref, _ptr(start), _ptr(count), _View(key.data_ptr(), 0, sk[0], sk[1], sk[2]),
+        _View(value.data_ptr(), 0, sv[0], sv[1], sv[2]), _dtype_code(key), rows, tokens, _ptr(workspace), _stream(stream))
 
 
 def ls_paged_attention_workspace_size(rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -481,17 +480,15 @@ def ls_paged_attention(q, pages: LsPages, length, out, workspace, scale: float |
     """Attention of one new token per row: q, out [rows, heads, head_dim] (strided views, last dimension contiguous) over the
     positions < length [rows] int32 of the rows' pages.  scale: 1/sqrt(head_dim) by default.  workspace:
     ls_paged_attention_workspace_size() bytes."""
-    import torch
-
     shape, dt = q.shape, q.dtype
     rows, heads, dim = shape
     sq, so = q.stride(), out.stride()
     if not (rows == pages.rows and dim == pages.head_dim and heads % pages.kv_heads == 0 and out.shape == shape
-            and out.dtype is dt and (pages.coded or pages.dtype is dt) and _index(length, (rows,), torch.int32)
+            and out.dtype is dt and (pages.coded or pages.dtype is dt) and _index(length, pages.row, pages.int32)
             and (dim == 1 or sq[2] == so[2] == 1)):
         _refuse("ls_paged_attention", q, length, out)
     return load_library().ls_paged_attention(
-        _View(q.data_ptr(), 0, sq[0], 0, sq[1]), pages.c, length.data_ptr(), _dtype_code(q),
+        _View(q.data_ptr(), 0, sq[0], 0, sq[1]), pages.ref, length.data_ptr(), _dtype_code(q),
         dim ** -0.5 if scale is None else scale, rows, heads, _View(out.data_ptr(), 0, so[0], 0, so[1]),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
 
