@@ -184,11 +184,11 @@ ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int3
   if (p.tile > p.group) p.tile = p.group;
   p.per_row = p.kv_heads * p.tiles;
   p.by_tiles.set(p.tiles);
-  int ctas = kAtSms * (mma ? paged_mma_ctas(p.dim, p.group) : paged_simt_ctas(vec, p.tile));
+  int ctas = kAtSms * (mma ? paged_mma_ctas(p.dim, p.group) : paged_simt_ctas(vec, coded(pages->dtype), p.tile));
   if (dbg.ctas > 0 && dbg.ctas < ctas) ctas = dbg.ctas;
   const bool by_warp = mma && (dbg.warps ? dbg.warps == 1 : paged_mma_warps(p));
   p.workers = by_warp ? ctas * kPgWarps : ctas;
-  p.least = dbg.least > 0 ? dbg.least : by_warp ? 8 : 16;
+  p.least = dbg.least > 0 ? dbg.least : by_warp ? 4 : 8;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return report_cuda(mma ? launch_paged_mma(p, dtype, pages->dtype, by_warp, st) : launch_paged_simt(p, dtype, pages->dtype, vec, st));
 }

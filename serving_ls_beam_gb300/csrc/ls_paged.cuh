@@ -141,51 +141,67 @@ struct PgWalk {
 
   // The next part (by all lanes), or false.
   __device__ __forceinline__ bool next(PgPart& x) {
-    PgState s = st;
-    if (s.at >= s.end) return false;
-    if (s.cut) {
-      if (s.item == p.per_row) {
-        ++s.r;
-        s.row_u += (PgCount)s.nb * p.per_row;
-        s.len = clamp_len(next_len);
-        s.nb = blocks_of(s.len);
-        s.item = 0;
-        next_len = keys_of(s.r + 1);
+    const PgCount at = st.at, end = st.end;
+    if (at >= end) return false;
+    int r = st.r, len = st.len, nb = st.nb, item = st.item;
+    PgCount row_u = st.row_u, step = p.workers;
+    const bool cut = st.cut;
+    bool moved = false;  // to another row
+    if (cut) {
+      if (item == p.per_row) {
+        moved = true;
+        ++r;
+        row_u += (PgCount)nb * p.per_row;
+        len = clamp_len(next_len);
+        nb = blocks_of(len);
+        item = 0;
+        next_len = keys_of(r + 1);
       }
-      const PgCount item_u = s.row_u + (PgCount)s.item * s.nb;
-      x.lo = (int)(s.at - item_u);
-      x.hi = (int)min((PgCount)s.nb, x.lo + (s.end - s.at));
+      const PgCount item_u = row_u + (PgCount)item * nb;
+      x.lo = (int)(at - item_u);
+      x.hi = (int)min((PgCount)nb, x.lo + (end - at));
       x.parts = 1;
-      if (x.lo > 0 || x.hi < s.nb) {
+      if (x.lo > 0 || x.hi < nb) {
+        const PgState s = st;
         x.base = owner(s, item_u);
-        x.parts = owner(s, item_u + s.nb - 1) - x.base + 1;
+        x.parts = owner(s, item_u + nb - 1) - x.base + 1;
         x.part = worker - x.base;
       }
+      step = x.hi - x.lo;
     } else {
+      moved = true;
+      PgState s = st;
       PgCount row_p;
       locate(s, row_p);
-      const int k = parts_of(s.nb);
-      const unsigned off = (unsigned)(s.at - row_p);  // (below parts of an item * items of a row, on the short path)
-      s.item = (int)(off / (unsigned)k);
-      x.part = (int)(off - (unsigned)s.item * k);
+      r = s.r;
+      len = s.len;
+      nb = s.nb;
+      row_u = s.row_u;
+      const int k = parts_of(nb);
+      const unsigned off = (unsigned)(at - row_p);  // (below parts of an item * items of a row, on the short path)
+      item = (int)(off / (unsigned)k);
+      x.part = (int)(off - (unsigned)item * k);
       x.lo = x.part * p.least;
-      x.hi = min(x.lo + p.least, s.nb);
+      x.hi = min(x.lo + p.least, nb);
       x.parts = k;
-      x.base = k > 1 ? (int)((s.row_u + (PgCount)s.item * s.nb) / p.least) : 0;
+      x.base = k > 1 ? (int)((row_u + (PgCount)item * nb) / p.least) : 0;
     }
-    x.r = s.r;
-    x.h = p.by_tiles(s.item);
-    x.i0 = (s.item - x.h * p.tiles) * p.tile;
+    x.r = r;
+    x.h = p.by_tiles(item);
+    x.i0 = (item - x.h * p.tiles) * p.tile;
     x.nq = min(p.tile, p.group - x.i0);
-    x.len = s.len;
-    if (s.cut) {
-      s.at += x.hi - x.lo;
-      if (x.hi == s.nb) ++s.item;
-    } else {
-      s.at += p.workers;
-    }
+    x.len = len;
     __syncwarp();
-    if (lane == 0) st = s;
+    if (lane == 0) {
+      st.at = at + step;
+      st.item = cut && x.hi == nb ? item + 1 : item;
+      if (moved) {
+        st.r = r;
+        st.len = len;
+        st.nb = nb;
+        st.row_u = row_u;
+      }
+    }
     __syncwarp();
     return true;
   }

@@ -76,6 +76,6 @@ int paged_mma_ctas(int dim, int group);  // CTAs that an SM holds
 // any types; vec: f32 queries, every stride and address a multiple of 16 bytes, the vectors of 16
 cudaError_t launch_paged_simt(PagedParams p, int dtype, int cache, bool vec, cudaStream_t stream);
 int paged_simt_queries(int group, bool vec);
-int paged_simt_ctas(bool vec, int tile);
+int paged_simt_ctas(bool vec, bool codes, int tile);
 
 }  // namespace lsb

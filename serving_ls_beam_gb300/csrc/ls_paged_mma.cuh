@@ -248,17 +248,16 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
         }
       }
   };
-  // the queries of the ring's part `slot` into the half of the warp's buffer that its parity says
+  // the queries of the ring's part `slot` into its half of the warp's buffer
   auto fetch_queries = [&](int slot) {
     const PgPart& y = ring[warp][slot];
     unsigned char* to = my_q + (slot & 1) * 8 * NQ * QROW;
     const unsigned char* from = p.q.data + (long long)y.r * p.q.row + (long long)(y.h * p.group + y.i0) * p.q.head;
     constexpr int CH = DP / 8;  // 16-byte pieces
     const int nq = y.nq;
-#pragma unroll
-    for (int n = 0; n < 8 * NQ * CH; n += 32) {
-      const int q = (n + lane) / CH, c = (n + lane) % CH;
-      const bool there = q < nq && c * 8 < p.dim;
+    for (int n = lane; n < nq * CH; n += 32) {
+      const int q = n / CH, c = n % CH;
+      const bool there = c * 8 < p.dim;
       cp_async16_fill(smem_addr(to + q * QROW + c * 16), there ? from + (long long)q * p.q.head + c * 16 : p.q.data, there ? 16 : 0);
     }
     cp_async_commit();
@@ -328,7 +327,8 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i) {
           // 16-bit pages: 16 bytes t + 4 i; codes: 32 bytes t + 4 (i / 2), in halves
-          const uint4 d = *reinterpret_cast<const uint4*>(src + a * 8 * QROW + (CODES ? (t + 4 * (i / 2)) * 32 + (i % 2) * 16 : (t + 4 * i) * 16));
+          const uint4 d = a * 8 + g < x.nq ? *reinterpret_cast<const uint4*>(src + a * 8 * QROW + (CODES ? (t + 4 * (i / 2)) * 32 + (i % 2) * 16 : (t + 4 * i) * 16))
+                                           : make_uint4(0u, 0u, 0u, 0u);
           f[4 * i] = d.x;
           f[4 * i + 1] = d.y;
           f[4 * i + 2] = d.z;
@@ -357,11 +357,12 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
         if constexpr (S::QREG) {
 #pragma unroll
           for (int i = 0; i < DP / 8; ++i) qf[a][i] = f[i];
-        } else if constexpr (CODES) {  // (as f16, in place)
+        } else {  // (as f16, and zeros past the last query, in place)
           unsigned char* to = my_q + (cp & 1) * 8 * NQ * QROW + (a * 8 + g) * QROW;
 #pragma unroll
           for (int i = 0; i < DP / 32; ++i)
-            *reinterpret_cast<uint4*>(to + (t + 4 * (i / 2)) * 32 + (i % 2) * 16) = make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            *reinterpret_cast<uint4*>(to + (CODES ? (t + 4 * (i / 2)) * 32 + (i % 2) * 16 : (t + 4 * i) * 16)) =
+                make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         }
         m[a][0] = m[a][1] = z[a][0] = z[a][1] = -INFINITY;
         l[a][0] = l[a][1] = 0.0f;
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
         }
       }
     }
-    const bool out_bf = dtype == DT_BF16;
+    const bool out_bf = CODES ? dtype == DT_BF16 : BF;
     if (by_warp) {
 #pragma unroll
       for (int a = 0; a < NQ; ++a)

@@ -86,12 +86,12 @@ __device__ __forceinline__ void store16(unsigned char* at, const uint4& x) { *re
 
 // A lane's 16 elements of type DT, and back.
 template <int DT>
-__device__ __forceinline__ void load_floats(const unsigned char* at, float (&x)[16]) {
+__device__ __forceinline__ void floats_of(const uint4 (&raw)[kBytes<DT>], float (&x)[16]) {
   constexpr int E = Traits<DT>::kVec;
 #pragma unroll
   for (int v = 0; v < 16 / E; ++v) {
     float y[E];
-    unpack<DT>(load16(at + 16 * v), y);
+    unpack<DT>(raw[v], y);
 #pragma unroll
     for (int e = 0; e < E; ++e) x[v * E + e] = y[e];
   }
@@ -129,6 +129,20 @@ __global__ void __launch_bounds__(kMvThreads) page_move_kernel(const __grid_cons
   const long long n = ((long long)blockIdx.x * kMvThreads + threadIdx.x) / G;
   const bool any = n < p.vectors;  // (whole warps go on: the exchanges are theirs)
   const int t = any ? p.by_head((int)n) : 0, h = any ? (int)n - t * p.heads : 0, r = p.by_token(t), i = t - r * p.tokens;
+  // a write's tokens are under way while their places are looked up (those past the count come for nothing)
+  constexpr int RAW = READ ? 1 : B;
+  uint4 rk[RAW], rv[RAW];
+  if constexpr (!READ) {
+    if (any && lane * 16 < p.dim) {
+      const unsigned char* from_k = p.key.data + dense_at(p.key, r, i, h) + lane * 16 * B;
+      const unsigned char* from_v = p.value.data + dense_at(p.value, r, i, h) + lane * 16 * B;
+#pragma unroll
+      for (int v = 0; v < B; ++v) {
+        rk[v] = load16(from_k + 16 * v);
+        rv[v] = load16(from_v + 16 * v);
+      }
+    }
+  }
   Places at{};
   if (any) at = place_of(p, r, i, h, lane == 0 && h == 0);
   const bool mine = at.ok && lane * 16 < p.dim;
@@ -138,18 +152,24 @@ __global__ void __launch_bounds__(kMvThreads) page_move_kernel(const __grid_cons
   unsigned char* pv = p.pages.value.data + at.value + lane * 16 * BC;
   if constexpr (CT == DT) {
     if (!mine) return;
-    const unsigned char *sk = READ ? pk : dk, *sv = READ ? pv : dv;
-    unsigned char *tk = READ ? dk : pk, *tv = READ ? dv : pv;
-    uint4 a[B], b[B];
+    if constexpr (READ) {
+      uint4 a[B], b[B];
 #pragma unroll
-    for (int v = 0; v < B; ++v) {
-      a[v] = load16(sk + 16 * v);
-      b[v] = load16(sv + 16 * v);
-    }
+      for (int v = 0; v < B; ++v) {
+        a[v] = load16(pk + 16 * v);
+        b[v] = load16(pv + 16 * v);
+      }
 #pragma unroll
-    for (int v = 0; v < B; ++v) {
-      store16(tk + 16 * v, a[v]);
-      store16(tv + 16 * v, b[v]);
+      for (int v = 0; v < B; ++v) {
+        store16(dk + 16 * v, a[v]);
+        store16(dv + 16 * v, b[v]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < B; ++v) {
+        store16(pk + 16 * v, rk[v]);
+        store16(pv + 16 * v, rv[v]);
+      }
     }
   } else if constexpr (READ) {
     if (!mine) return;
@@ -181,9 +201,9 @@ __global__ void __launch_bounds__(kMvThreads) page_move_kernel(const __grid_cons
     }
   } else {
     float xk[16] = {}, xv[16] = {};
-    if (mine) {
-      load_floats<DT>(dk, xk);
-      load_floats<DT>(dv, xv);
+    if (any && lane * 16 < p.dim) {
+      floats_of<DT>(rk, xk);
+      floats_of<DT>(rv, xv);
     }
     float ak = 0.0f, av = 0.0f;
 #pragma unroll
@@ -206,6 +226,27 @@ __global__ void __launch_bounds__(kMvThreads) page_move_kernel(const __grid_cons
     for (int kv = 0; kv < 2; ++kv) {
       const float s = kv ? sv : sk, inv = 1.0f / s;  // exact for a power of two
       uint32_t w[4];
+      if constexpr (CT == CT_I8) {
+        // the estimates, as the low bytes of a sum with 1.5 * 2^23; one by one where a remainder says that one of them
+        // is not the nearest, or a tie
+        constexpr float kMagic = 12582912.0f;
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = kv ? xv[4 * j + e] : xk[4 * j + e], f = fmaf(y, inv, kMagic);
+            most = fmaxf(most, fabsf(fmaf(-__fsub_rn(f, kMagic), s, y)));
+            b[e] = __float_as_uint(f);
+          }
+          w[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        }
+        if (most + most < s) {
+          store16(kv ? pv : pk, make_uint4(w[0], w[1], w[2], w[3]));
+          continue;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float y[4];

@@ -101,8 +101,11 @@ __device__ __forceinline__ int reversed(int l) {
   return N == 8 ? (l & 1) << 2 | (l & 2) | (l >> 2 & 1) : (l & 1) << 1 | (l >> 1 & 1);
 }
 
+// CTAs of an SM, by the registers that two blocks' loads and the queries take
+constexpr int paged_simt_ctas_of(bool vec, bool codes, int queries) { return !vec || (codes && queries > 1) ? 2 : queries > 1 || codes ? 3 : 4; }
+
 template <int CT, bool VEC, int LPK, int V, int MQ>
-__global__ void __launch_bounds__(kPgThreads, MQ == 1 ? 3 : 2) paged_simt_kernel(const __grid_constant__ PagedParams p, int dtype) {
+__global__ void __launch_bounds__(kPgThreads, paged_simt_ctas_of(VEC, kBytes<CT> == 1, MQ)) paged_simt_kernel(const __grid_constant__ PagedParams p, int dtype) {
   constexpr int B = kBytes<CT>, E = 16 / B, EV = E * V, U = 8 / V, KPL = 32 / LPK, KB = U * KPL, STEP = LPK * E;
   constexpr bool Q8 = B == 1;
   __shared__ float wm[kPgWarps][MQ], wl[kPgWarps][MQ];
@@ -116,8 +119,15 @@ __global__ void __launch_bounds__(kPgThreads, MQ == 1 ? 3 : 2) paged_simt_kernel
   bool bad = false;
   __shared__ PgShare share;
   PgWalk<KB> walk(p, share, blockIdx.x, warp, lane);
-  PgPart x;
-  while (walk.next(x)) {
+  __shared__ PgPart parts[kPgWarps];  // (the warps' own, all the same)
+  while (true) {
+    {
+      PgPart y;
+      if (!walk.next(y)) break;
+      if (lane == 0) parts[warp] = y;
+      __syncwarp();
+    }
+    const PgPart& x = parts[warp];
     const long long table = (long long)x.r * p.pages.table_row;
     const unsigned char* kh = p.pages.key.data + (long long)x.h * p.pages.key.head;
     const unsigned char* vh = p.pages.value.data + (long long)x.h * p.pages.value.head;
@@ -329,7 +339,7 @@ cudaError_t run_simt_dim(const PagedParams& p, int dtype, cudaStream_t stream) {
 }  // namespace
 
 int paged_simt_queries(int group, bool vec) { return vec && group == 1 ? 1 : 4; }
-int paged_simt_ctas(bool vec, int tile) { return vec && tile == 1 ? 3 : 2; }
+int paged_simt_ctas(bool vec, bool codes, int tile) { return paged_simt_ctas_of(vec, codes, tile); }
 
 cudaError_t launch_paged_simt(PagedParams p, int dtype, int cache, bool vec, cudaStream_t stream) {
   if (vec) {  // f32 queries
