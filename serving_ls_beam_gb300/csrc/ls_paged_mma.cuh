@@ -11,14 +11,24 @@
 // through no shared memory: the order of the head's elements within a product's contraction is free as
 // long as the queries have the same one, so lane (g, t) takes 16 bytes t, t + 4, .. of keys g and g + 8, and
 // of the values 16 bytes g, g + 8, .. of keys 2t, 2t + 1, 2t + 8, 2t + 9, whose pairs it puts together itself.  A load
-// instruction covers 64 (keys) or 128 bytes (values) of a head vector in a row, whatever the page size: the
-// lanes look up one key's page each, two blocks ahead.  Keys are loaded again as soon as a block's scores are
-// formed, values as soon as its sums are.
+// instruction covers 64 (keys) or 128 bytes (values) of a head vector in a row, whatever the page size.  Where 16
+// positions lie in one page (TILES) the lanes share its number and keep their places; otherwise lane n looks up key
+// n's page.  Numbers are looked up two blocks ahead; keys are loaded again as soon as a block's scores are formed,
+// values as soon as its sums are; a worker's next part has its queries and its first page numbers under way while
+// the one before is at work.
 //
 // 8-bit codes become f16, exactly, in registers; a key's scale multiplies its scores.  A value's scale
 // cannot go into its f16 elements nor, by itself, into an f16 weight (a key with nearly all the weight may have
 // values 2^-20 of the others'), so the weights of the second product are 2^(score + log2 scale - reference) with a
 // reference of their own, the largest such exponent, apart from the maximum that the sum is taken with.
+//
+// What bounds it: the instructions around the products (some 250 per warp for a block of 4 KB of 16-bit keys and values,
+// twice that for codes, whose conversion is the most of it; 750 per part) and the latency that 8 to 16 warps per SM leave.
+// 256 rows x 8 key heads of 128 codes, 4 queries, 501 to 4000 positions: 1.22 GB in 219 us, 0.82 of the measured copy rate
+// (a CTA's four warps per part 238; page numbers through shuffles for every key 235); one row of 131000 bf16 positions
+// 89 us, 0.88 (the parts joined by one thread per element 114); 32 rows of 2000 to 8000 105 us, 0.92; 64 rows x 16 heads of
+// 64 int8, 300 to 999 positions: 36 us, 0.37; 1024 rows x 16 heads of 64 f16, 48 to 63 positions: 55 us, 0.63.  Blocks of 32
+// keys for 16-bit heads of 64: no faster; a fifth CTA per SM for them spills (int8 36 -> 48 us).
 #pragma once
 
 #include "ls_paged.cuh"

@@ -13,6 +13,10 @@
 // products of a lane group are reduced together, each exchange halving the products that a lane still
 // holds, which leaves every lane with the score of its own key.  Four warps take a part's blocks in turn
 // and merge through shared memory.
+//
+// What bounds it: the bytes under way (12 to 16 warps of 8 KB less what is at work) and, with four queries or codes,
+// instructions.  64 rows x 16 heads of 64 f32, 100 to 700 positions: 66 us, 0.47 of the measured copy rate (three CTAs per
+// SM 76); x 8 key heads of 128 with 4 queries 83 us, 0.38; e4m3 pages of 300 to 2700 positions 160 us, 0.19.
 #include "ls_paged.cuh"
 
 namespace lsb {
