@@ -378,7 +378,8 @@ LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_
  *  logits      [rows, vocab], logit_dtype (f32, f16 or bf16), device: row r at logits + r *
  *              row_stride elements (row_stride >= vocab); bias [vocab] f32 or NULL.
  *  u           [rows] f32 in [0, 1).
- *  temperature [rows] f32 or NULL (1): 0 gives the first largest x with log-probability 0.
+ *  temperature [rows] f32 or NULL (1): 0 gives the first largest x with log-probability 0; infinity
+ *              makes the finite ones equally likely.
  *  top_k       [rows] int32 or NULL: 0, or vocab and more, keeps all.
  *  top_p       [rows] f32 or NULL: in (0, 1]; 1 keeps all.
  *  min_p       [rows] f32 or NULL: in [0, 1]; 0 keeps all.
@@ -388,7 +389,7 @@ LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_
  *              as 0, such a filter as off.
  *  Logits of -inf are never drawn, and NaN counts as -inf; a row of nothing else gives token -1 with
  *  log-probability -inf.  +inf is not supported (no fault; the result is unspecified).  The weights
- *  are formed to some 2^-30 of their value and summed in integers, in units of at most 2^-44 of the
+ *  are formed to some 2^-28 of their value and summed in integers, in units of at most 2^-44 of the
  *  largest (vocab up to 2^18; one bit coarser for each doubling): the result does not depend on the
  *  order of any sum.  A w below that unit counts as 0.
  *  vocab 1..2^28.  rows == 0 is a no-op.  Nothing is allocated.
@@ -407,8 +408,8 @@ LS_API ls_status ls_sample_filtered(const void* logits, ls_dtype logit_dtype, in
  *              page to page, `pos` from place to place), device.
  *  dtype       f32, f16 or bf16: the keys and values as they are.  LS_DTYPE_E4M3 or LS_DTYPE_I8:
  *              8-bit codes, a head vector being its codes times its scale.
- *  key_scale, value_scale  views [num_pages, page_size, kv_heads] of f32 (the same strides, in f32
- *              elements), for the 8-bit types; not read otherwise.
+ *  key_scale, value_scale  views [num_pages, page_size, kv_heads] of f32 (strides in f32 elements), for
+ *              the 8-bit types; not read otherwise.  Scales are finite and not negative.
  *  table       [rows, max_pages] int32, device, `table_row` elements from row to row (>= 0).  Of a row
  *              only the pages of the positions in use are looked up.
  */
@@ -472,11 +473,13 @@ LS_API ls_status ls_paged_read(const ls_pages* pages, const int32_t* start, cons
  *  heads       a multiple of kv_heads; head_dim 1..256.
  *  workspace   >= ls_paged_attention_workspace_size(rows, heads, kv_heads, head_dim) bytes, 256-byte
  *              aligned, initialised once by ls_workspace_init; the size grows with heads / kv_heads (up
- *              to 16) and head_dim only.  Calls sharing it must be ordered.
+ *              to 16) and head_dim only.  Calls sharing it must be ordered.  It is these calls' own: of
+ *              the other entry points only ls_paged_write, ls_paged_read and ls_sample_filtered may be
+ *              given it too (its counters are zero between calls, and others would overwrite them).
  *  Inputs that a query reads are finite; otherwise its result is unspecified (no fault).  rows == 0 is a
  *  no-op.  Fastest with q in 16 bits, strides and addresses that are multiples of 16 bytes, head_dim of
- *  16 (16-bit pages: 8), and pages of a multiple of 8 positions.  rows * heads above 2^31 - 1, or max_pages *
- *  page_size above 2^31 - 1024, returns LS_ERR_UNSUPPORTED.
+ *  16 (16-bit pages: 8), and pages of a multiple of 16 positions.  rows * heads or max_pages * page_size
+ *  above 2^31 - 1024 returns LS_ERR_UNSUPPORTED.
  */
 LS_API size_t ls_paged_attention_workspace_size(int rows, int heads, int kv_heads, int head_dim);
 LS_API ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int32_t* len, ls_dtype dtype,

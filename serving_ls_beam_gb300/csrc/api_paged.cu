@@ -152,7 +152,7 @@ ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int3
   if (s != LS_OK) return s;
   if (heads % pages->kv_heads != 0) return LS_ERR_INVALID_ARG;
   if (rows == 0) return LS_OK;
-  if ((long long)rows * heads > INT_MAX) return LS_ERR_UNSUPPORTED;
+  if ((long long)rows * heads > kPgMaxPlaces) return LS_ERR_UNSUPPORTED;  // (rows are counted on by up to 128)
   const int es = bytes_of(dtype);
   if (!q || !out || !view_fits(*q, es, false, rows, 1, heads) || !view_fits(*out, es, true, rows, 1, heads) || !len || misaligned(len, 4))
     return LS_ERR_INVALID_ARG;

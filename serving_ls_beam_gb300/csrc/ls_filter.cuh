@@ -113,7 +113,7 @@ struct Shared {  // fixed part of a CTA's shared memory
   Cut cut;
   int drawn;                // the list gave the token
   float2 min_cut;           // T ln(min_p), as a pair
-  int found, kept;
+  int found, kept, token;
   u64 rest;
 };
 
@@ -132,7 +132,7 @@ struct Sampler {
   int row, rank, lead, vectors, first_vec;
   const unsigned char* base;  // the row's first 16-byte vector
   RowScale sc;
-  int tid, warp, lane, flip;
+  int tid, warp, lane, flip, turn;
 
   __device__ __forceinline__ void sync() const {
     if constexpr (CL)
@@ -297,11 +297,11 @@ struct Sampler {
   // the cluster's sum of the CTAs' sums `here` (each the same in all of its threads)
   __device__ __forceinline__ u64 row_sum_of(u64 here) {
     if constexpr (!CL) return here;
-    if (tid == 0) s.publish_sum[1] = here;
+    turn ^= 1;  // (two places in turn: whoever writes one again has passed the barrier behind the reads of it)
+    if (tid == 0) s.publish_sum[turn] = here;
     sync();
     u64 all = 0;
-    for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[1], c);
-    sync();
+    for (int c = 0; c < ctas(); ++c) all += *at(&s.publish_sum[turn], c);
     return all;
   }
 
@@ -656,7 +656,7 @@ struct Sampler {
     sync();
     const bool drawn = *at(&s.drawn, 0);
     cut = *at(&s.cut, 0);
-    sync();
+    if (CL && drawn) sync();  // (the first CTA stays until this is read)
     return drawn;
   }
   __device__ __forceinline__ void write(int token, u64 w, u64 all) const {
@@ -696,7 +696,7 @@ struct Sampler {
     if (tid == 0) {
       s.publish_sum[2] = mine;
       s.found = -1;
-      s.cut.index = -1;
+      s.token = -1;
     }
     sync();
     u64 before = 0;
@@ -748,7 +748,7 @@ struct Sampler {
               for (int e = 0; e < E; ++e) {
                 if (run <= rest && run + w[e] > rest) {
                   s.publish_sum[3] = w[e];
-                  s.cut.index = index_of(v, e);
+                  s.token = index_of(v, e);
                 }
                 run += w[e];
               }
@@ -760,7 +760,7 @@ struct Sampler {
       }
     }
     sync();
-    const int token = *at(&s.cut.index, owner);
+    const int token = *at(&s.token, owner);
     value = *at(&s.publish_sum[3], owner);
     sync();
     return token;
@@ -926,9 +926,8 @@ struct Sampler {
     }
     sync();
     const int lo = *at(&s.found, 0), hi = *at(&s.kept, 0);
-    u64* list = at(hist, 0);
+    u64* list = at(hist, 0);  // (in the place of the steps, which the first CTA has read)
     unsigned* listed = at(&s.listed, 0);
-    sync();  // (the steps are done with; the list takes their place)
     u64 run = 0, all = 0;
     each_unit(
         [&](float top) {
@@ -970,10 +969,10 @@ struct Sampler {
           run = 0;
         });
     const u64 above = row_sum_of(block_total(lane == 0 ? all : 0));
-    sync();
+    if constexpr (!CL) __syncthreads();  // (in a cluster the sum has had its barrier)
     const unsigned n = *listed;
-    sync();
     if (n > kSfList) {
+      sync();
       cut = select<true>(limit, within);
       return false;
     }
@@ -1006,7 +1005,6 @@ struct Sampler {
     }
     sync();
     cut = *at(&s.cut, 0);
-    sync();
     return true;
   }
 
@@ -1166,7 +1164,7 @@ struct Sampler {
     constexpr double kSteps = kSfSteps * 1.4426950408889634073599;
     constexpr float kStepsHi = (float)kSteps, kStepsLo = (float)(kSteps - (double)kStepsHi);
     sc.hi = fminf(__fdiv_rn(kStepsHi, temp), 1e30f);
-    sc.lo = sc.hi < 1e30f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-sc.hi, temp, kStepsHi), kStepsLo), temp) : 0.0f;
+    sc.lo = sc.hi < 1e30f && temp < INFINITY ? __fdiv_rn(__fadd_rn(__fmaf_rn(-sc.hi, temp, kStepsHi), kStepsLo), temp) : 0.0f;
     float least = -INFINITY;  // the smallest x with w >= min_p: M + T ln(min_p), rounded up
     if (min_p > 0.0f) {
       const float2 sum = two_sum(m, s.min_cut.x);
@@ -1226,7 +1224,6 @@ struct Sampler {
       float bound = __fsub_rd(m, __fdiv_rn((float)(step + 1) * 1.001f, per_step * sc.hi));
       if (step < 0 || !(bound <= m)) bound = -INFINITY;
       const unsigned n = gather_from(bound, mine);
-      if constexpr (CL) sync();  // (the first CTA's counter has been read)
       if (n <= kSfList) {
         open = false;
         summed = true;
@@ -1289,7 +1286,7 @@ __global__ void __launch_bounds__(kSfThreads, 1024 / kSfThreads) sample_filter_k
   const int lead = (int)(lead_bytes / S::B);
   S s{p, shared, sf_raw, unit_sum, hist, sorted, ranks, index_rank, row, rank, lead, (int)(((long long)lead + p.vocab + S::E - 1) / S::E),
       rank * p.units * p.unit_vecs * 32, at - lead_bytes, RowScale{}, (int)threadIdx.x, (int)threadIdx.x >> 5,
-      (int)threadIdx.x & 31, 0};
+      (int)threadIdx.x & 31, 0, 0};
   s.run();
 }
 

@@ -107,6 +107,7 @@ def test_attention_refusals(lsb):
     assert call(ws=None) == E and call(ws=P + 16) == E and call(size=4096) == E
     assert call(rows=0) == 0
     assert call(rows=1 << 30) == UNSUPPORTED
+    assert call(pages(lsb, heads=1), rows=(1 << 31) - 1000, heads=1) == UNSUPPORTED  # the walks over rows go on by up to 128
     assert call(pages(lsb, size=1 << 16, most=1 << 15)) == UNSUPPORTED
 
 

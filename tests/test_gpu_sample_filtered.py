@@ -138,7 +138,7 @@ def test_uniforms_at_the_ends(dev, kernel):
 def test_temperatures(dev, kernel):
     """From none (the first largest) over very small to very large."""
     g = np.random.default_rng(5)
-    t = np.array([0.0, 1e-30, 1e-3, 0.05, 1.0, 30.0, 1e6, 1e30])
+    t = np.array([0.0, 1e-30, 1e-3, 0.05, 1.0, 30.0, 1e6, 1e30, 3e38, np.inf])
     x = normal(g, len(t), 4000, "f32", dev, 3.0)
     x[:, 77] = x[:, 1234] = x.max() + 1
     for f in (dict(), dict(k=20), dict(p=0.9), dict(m=0.9)):
