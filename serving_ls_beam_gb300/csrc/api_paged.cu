@@ -188,7 +188,7 @@ ls_status ls_paged_attention(const ls_view* q, const ls_pages* pages, const int3
   if (dbg.ctas > 0 && dbg.ctas < ctas) ctas = dbg.ctas;
   const bool by_warp = mma && (dbg.warps ? dbg.warps == 1 : paged_mma_warps(p));
   p.workers = by_warp ? ctas * kPgWarps : ctas;
-  p.least = dbg.least > 0 ? dbg.least : by_warp ? 4 : 8;
+  p.least = dbg.least > 0 && dbg.least < 1 << 20 ? dbg.least : by_warp ? 4 : 8;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return report_cuda(mma ? launch_paged_mma(p, dtype, pages->dtype, by_warp, st) : launch_paged_simt(p, dtype, pages->dtype, vec, st));
 }
