@@ -479,29 +479,42 @@ struct Sampler {
     if (mine >= bound) ranks[to] = tid;
     __syncthreads();
     const unsigned per = p.thread_vecs, all = s.threads * per;
-    for (unsigned n = tid; n < all; n += kSfThreads) {
-      const unsigned who = fast_div(n, p.thread_magic, p.thread_shift), k = n - who * per, of = ranks[who];
-      unsigned un = of / 32 + k * kSfWarps, i = 0;
-      if (p.unit_vecs > 1) {
-        un = of / 32 + k / p.unit_vecs * kSfWarps;
-        i = k % p.unit_vecs;
-      }
-      if (un >= (unsigned)p.units) continue;
-      const int v = (int)(un * p.unit_vecs + i) * 32 + (int)(of & 31);
-      const Vec y = get(v);
-      if (!(max_of(y) >= bound)) continue;
-      float x[E];
-      values_of(y, x);
-      unsigned hits = 0;
+    constexpr int AHEAD = BIAS ? 2 : 3;  // (where the row is not in shared memory, loads from L2)
+    for (unsigned n0 = tid; n0 < all; n0 += kSfThreads * AHEAD) {
+      Vec y[AHEAD];
+      int v[AHEAD];
 #pragma unroll
-      for (int e = 0; e < E; ++e) hits |= (x[e] >= bound && x[e] > -INFINITY ? 1u : 0u) << e;
-      unsigned put = hits ? atomicAdd(listed, (unsigned)__popc(hits)) : 0u;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if ((hits >> e) & 1u) {
-          if (put < kSfList) list[put] = list_key(x[e], index_of(v, e));
-          ++put;
+      for (int a = 0; a < AHEAD; ++a) {
+        const unsigned n = n0 + a * kSfThreads;
+        v[a] = -1;
+        if (n >= all) continue;
+        const unsigned who = fast_div(n, p.thread_magic, p.thread_shift), k = n - who * per, of = ranks[who];
+        unsigned un = of / 32 + k * kSfWarps, i = 0;
+        if (p.unit_vecs > 1) {
+          un = of / 32 + k / p.unit_vecs * kSfWarps;
+          i = k % p.unit_vecs;
         }
+        if (un < (unsigned)p.units) {
+          v[a] = (int)(un * p.unit_vecs + i) * 32 + (int)(of & 31);
+          y[a] = get(v[a]);
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        if (v[a] < 0 || !(max_of(y[a]) >= bound)) continue;
+        float x[E];
+        values_of(y[a], x);
+        unsigned hits = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) hits |= (x[e] >= bound && x[e] > -INFINITY ? 1u : 0u) << e;
+        unsigned put = hits ? atomicAdd(listed, (unsigned)__popc(hits)) : 0u;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((hits >> e) & 1u) {
+            if (put < kSfList) list[put] = list_key(x[e], index_of(v[a], e));
+            ++put;
+          }
+      }
     }
     sync();
     return *listed;
