@@ -870,9 +870,11 @@ struct Sampler {
   // The nucleus of the tokens `within`: the cut, and the units' sums of what is kept.  False where equal values are so
   // many that it takes select(), which gives the cut alone.
   //
-  // One pass sums the weights and counts them in coarse whole numbers in the histogram's steps (2^-31 of an upper
-  // bound of the sum; what each loses is less than one, so the steps between which the limit must be passed are
-  // known, few of them).  A second one sums the units' weights above those steps and lists what lies in them.
+  // One pass counts the weights in coarse whole numbers in the histogram's steps (2^-31 of an upper bound of the sum).
+  // They are formed in f32 alone: t is off by three roundings at most, of up to 32 octaves 5.7e-6, the exponent's
+  // by 2^-19 octaves, the power by 2^-22, together less than 2^-17 of a weight; and cut to a whole number each loses
+  // less than one.  So the steps between which the limit must be passed are known, few of them.  A second pass sums the
+  // weights exactly, of everything and of the units above those steps, and lists what lies in them.
   template <bool ALL>  // within is everything
   __device__ __forceinline__ bool nucleus(float top_p, const Cut& within, Cut& cut) {
     auto* steps = reinterpret_cast<uint32_t*>(hist);
@@ -885,25 +887,24 @@ struct Sampler {
     // (2^12 to one, rounded up, so that whole numbers can be added up)
     const u64 bound = row_sum_of(block_total((u64)(most * 4096.0f) + 1)) * E;
     const int down = max(64 - __clzll((long long)bound) - 12 + 29 + p.shift - 31, 0);
-    u64 total = 0;
+    const float unit = (float)(29 + p.shift - down);  // a weight of 1 in coarse whole numbers is 2^unit
     each_unit([&](float top) { return top >= within.value && steps_below(top) < sc.t_end; },
               [&](int v, const float(&x)[E]) {
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
-                  u64 w[2];
-                  float2 below;
-                  weigh(make_float2(x[e], x[e + 1]), w, below);
+                  const auto both = [](float y) { return make_float2(y, y); };
+                  const float2 t = __fmul2_rn(__ffma2_rn(make_float2(x[e], x[e + 1]), both(-1.0f), both(sc.top)), both(sc.hi));
+                  const float2 y = __ffma2_rn(t, both(-1.0f / kSfSteps), both(unit));
 #pragma unroll
                   for (int k = 0; k < 2; ++k) {
                     if (!ALL && !within.keeps(x[e + k], index_of(v, e + k))) continue;
-                    total += w[k];
-                    const uint32_t coarse = (uint32_t)(w[k] >> down);
-                    if (coarse) atomicAdd(steps + bin_of(-(k ? below.y : below.x)), coarse);
+                    const uint32_t coarse = __float2uint_rz(fast_exp2(k ? y.y : y.x));  // (NaN: 0)
+                    if (coarse) atomicAdd(steps + bin_of(k ? t.y : t.x), coarse);
                   }
                 }
               },
               [](int) {});
-    const u64 limit = share_of(top_p, row_sum_of(block_total(total)));
+    if (tid == 0) s.listed = 0;
     sync();
     if (rank == 0) {
       constexpr int PER = kSfBins / kSfThreads;
@@ -926,27 +927,28 @@ struct Sampler {
       if (tid == 0) {
         s.found = kSfBins - 1;
         s.kept = kSfBins - 1;
-        s.listed = 0;
       }
       u64 run = scan(here) - here;
-      const u64 sure = (limit + (1ull << down) - 1) >> down, maybe = limit >> down;
+      // what the whole numbers' sum is at least and at most where the coarse one's is c
+      const auto at_least = [&](u64 c) { return (u64)max((long long)(c - (c >> 17)) - (p.vocab >> down) - 1, 0ll); };
+      const auto at_most = [&](u64 c) { return c + (c >> 17) + p.vocab + 1; };
+      const u64 all = block_total(here);
+      bool cut_off;
+      const u64 maybe = part_of(top_p, at_least(all), cut_off), sure = part_of(top_p, at_most(all), cut_off) + 2;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {  // passed at this step: possibly, certainly
         run += h[i];
-        if (run + p.vocab >= maybe) atomicMin(&s.found, tid * PER + i);
-        if (run >= sure) atomicMin(&s.kept, tid * PER + i);
+        if (at_most(run) >= maybe) atomicMin(&s.found, tid * PER + i);
+        if (at_least(run) >= sure) atomicMin(&s.kept, tid * PER + i);
       }
     }
     sync();
     const int lo = *at(&s.found, 0), hi = *at(&s.kept, 0);
-    u64* list = at(hist, 0);  // (in the place of the steps, which the first CTA has read)
-    unsigned* listed = at(&s.listed, 0);
-    u64 run = 0, all = 0;
+    u64* list = hist;  // (in the place of the steps, which the first CTA has read)
+    unsigned* listed = &s.listed;
+    u64 run = 0, all = 0, total = 0;
     each_unit(
-        [&](float top) {
-          const float t = steps_below(top);
-          return top >= within.value && t < sc.t_end && bin_of(t) <= hi;
-        },
+        [&](float top) { return top >= within.value && steps_below(top) < sc.t_end; },
         [&](int v, const float(&x)[E]) {
           unsigned hits = 0;
 #pragma unroll
@@ -959,6 +961,7 @@ struct Sampler {
               const float t = -(k ? below.y : below.x);
               if (!(t < sc.t_end) || (!ALL && !within.keeps(x[e + k], index_of(v, e + k)))) continue;
               const int b = bin_of(t);
+              total += w[k];
               if (b < lo)
                 run += w[k];
               else if (b <= hi)
@@ -981,9 +984,18 @@ struct Sampler {
           all += t;
           run = 0;
         });
-    const u64 above = row_sum_of(block_total(lane == 0 ? all : 0));
+    all = block_total(lane == 0 ? all : 0);
+    if (CL && rank != 0) {  // each CTA's list behind the first's (entry by entry, every one would wait for the other SM)
+      const unsigned n = *listed;
+      if (tid == 0) s.kept = (int)atomicAdd(at(&s.listed, 0), n);
+      __syncthreads();
+      const unsigned to = s.kept;
+      for (unsigned i = tid; i < min(n, (unsigned)kSfList) && to + i < kSfList; i += kSfThreads) at(hist, 0)[to + i] = list[i];
+    }
+    const u64 above = row_sum_of(all);
+    const u64 limit = share_of(top_p, row_sum_of(block_total(total)));
     if constexpr (!CL) __syncthreads();  // (in a cluster the sum has had its barrier)
-    const unsigned n = *listed;
+    const unsigned n = *at(&s.listed, 0);
     if (n > kSfList) {
       sync();
       cut = select<true>(limit, within);
