@@ -797,10 +797,11 @@ struct Sampler {
 
   // Of a long list only the entries among which the sum from `base_sum` on reaches `limit` are left (their number is
   // returned, with base_sum what lies before them); the weights of those before go to their units.  By steps of the
-  // keys' bits, 2 kSfRank of them; the first CTA's threads.
+  // keys' bits, one per thread; the first CTA's threads.
   __device__ __forceinline__ unsigned narrow_list(unsigned n, u64 limit, u64& base_sum) {
-    constexpr int STEPS = 2 * kSfRank, PER = STEPS / kSfThreads, MINE = kSfList / kSfThreads;
-    u64* sums = sorted;
+    constexpr int STEPS = kSfThreads, MINE = kSfList / kSfThreads, PIECE = 21;
+    static_assert(3 * STEPS * 4 <= 2 * kSfRank * 8 && kSfList <= 1 << (32 - PIECE), "the sums' pieces");
+    auto* sums = reinterpret_cast<uint32_t*>(sorted);  // [3][STEPS], of 21 bits each: whole words are added natively
     uint32_t least = ~0u, most = 0;
     u64 mine[MINE];
 #pragma unroll
@@ -820,7 +821,7 @@ struct Sampler {
       s.crossing = STEPS - 1;
       s.kept = 0;
     }
-    for (int i = tid; i < STEPS; i += kSfThreads) sums[i] = 0;
+    for (int i = tid; i < 3 * STEPS; i += kSfThreads) sums[i] = 0;
     __syncthreads();
     if (lane == 0) {
       atomicMin(&s.publish_key[0], least);
@@ -834,21 +835,23 @@ struct Sampler {
     // (the keys rise as x falls)
 #pragma unroll
     for (int i = 0; i < MINE; ++i)
-      if (i * kSfThreads + tid < n) atomicAdd(sums + (((uint32_t)(mine[i] >> 32) - least) >> down), weight(list_x(mine[i])));
-    __syncthreads();
-    u64 h[PER], here = 0;
+      if (i * kSfThreads + tid < n) {
+        const u64 w = weight(list_x(mine[i]));
+        uint32_t* to = sums + (((uint32_t)(mine[i] >> 32) - least) >> down);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) here += h[i] = sums[tid * PER + i];
-    u64 run = scan(here) - here + base_sum;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (run < limit && run + h[i] >= limit) {
-        s.crossing = tid * PER + i;
-        s.rest = run;
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t piece = (uint32_t)(w >> (k * PIECE)) & ((1u << PIECE) - 1);
+          if (piece) atomicAdd(to + k * STEPS, piece);
+        }
       }
-      run += h[i];
-      if (tid == kSfThreads - 1 && i == PER - 1 && run < limit) s.rest = run - h[i];  // not reached: the last step
+    __syncthreads();
+    const u64 here = sums[tid] + ((u64)sums[STEPS + tid] << PIECE) + ((u64)sums[2 * STEPS + tid] << (2 * PIECE));
+    const u64 run = scan(here) - here + base_sum;
+    if (run < limit && run + here >= limit) {
+      s.crossing = tid;
+      s.rest = run;
     }
+    if (tid == kSfThreads - 1 && run + here < limit) s.rest = run;  // not reached: the last step
     __syncthreads();
     const uint32_t crossing = s.crossing;
     base_sum = s.rest;
@@ -944,6 +947,9 @@ struct Sampler {
     }
     sync();
     const int lo = *at(&s.found, 0), hi = *at(&s.kept, 0);
+    // as bounds of t, a little wider: what lies above is above in the steps too, what lies below below
+    const float t_lo = lo > 0 ? __fdiv_rn((float)lo - 0.5f, sc.per_bin) * (1.0f - 0x1p-20f) : -1.0f;
+    const float t_hi = hi < kSfBins - 1 ? __fdiv_rn((float)hi + 0.5f, sc.per_bin) * (1.0f + 0x1p-20f) : INFINITY;
     u64* list = hist;  // (in the place of the steps, which the first CTA has read)
     unsigned* listed = &s.listed;
     u64 run = 0, all = 0, total = 0;
@@ -960,11 +966,10 @@ struct Sampler {
             for (int k = 0; k < 2; ++k) {
               const float t = -(k ? below.y : below.x);
               if (!(t < sc.t_end) || (!ALL && !within.keeps(x[e + k], index_of(v, e + k)))) continue;
-              const int b = bin_of(t);
               total += w[k];
-              if (b < lo)
+              if (t < t_lo)
                 run += w[k];
-              else if (b <= hi)
+              else if (t <= t_hi)
                 hits |= 1u << (e + k);
             }
           }
