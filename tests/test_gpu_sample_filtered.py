@@ -233,3 +233,25 @@ def test_captured(dev):
         got = token.clone(), logprob.clone()
         call()
         assert torch.equal(got[0], token) and torch.equal(got[1], logprob)
+
+
+@pytest.mark.parametrize("dtype,vocab", [("f32", 40000), ("bf16", 120000)])
+@pytest.mark.parametrize("p", [1e-6, 0.02, 0.5, 0.99])
+def test_nucleus_of_long_rows(dev, kernel, dtype, vocab, p):
+    g = np.random.default_rng(vocab + 9)
+    check(dev, normal(g, 6, vocab, dtype, dev, 2.5), g.random(6), t=[0.05, 0.3, 1.0, 1.0, 2.0, 4.0], p=p)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("p", [1e-30, 0.05, 0.9, 0.9999, 0.99999, 1.0 - 2.0 ** -24])
+@pytest.mark.parametrize("k", [0, 3000])
+def test_nucleus_does_not_depend_on_the_split(dev, monkeypatch, dtype, p, k):
+    g = np.random.default_rng(31)
+    logits, u = normal(g, 24, 33001, dtype, dev, 2.5), g.random(24)
+    t = np.resize([0.02, 0.5, 1.0, 1.3, 30.0, 1e30, np.inf, 3e38], 24)
+    got = []
+    for split in ("sfcluster=1", "sfcluster=2", "sfcluster=8"):
+        monkeypatch.setenv("LS_BEAM_DEBUG", split)
+        got.append(run(dev, logits, u, t=t, p=p, k=k or None))
+    for token, logprob in got[1:]:
+        assert (token == got[0][0]).all() and (logprob == got[0][1]).all()
