@@ -10,9 +10,9 @@
 //     largest from below (the hierarchical method's first pass).  What lies above is a short list; it is
 //     sorted, its weights are added up, and the draw is from the list itself where up to 256 tokens are kept.
 //   larger top-k: counts of x in 2048 equal steps; the step that holds the k-th is the list.
-//   top-p: one pass sums the weights exactly and adds them in coarse whole numbers to 2048 steps, which says between
-//     which steps the limit is passed; a second one sums the units (of 32 vectors) above them and lists what
-//     lies between.
+//   top-p: one pass adds the weights, from f32 alone, in coarse whole numbers to 2048 steps, which says between which
+//     steps the limit must be passed; a second one sums them exactly, all and by units (of 32 vectors) above those
+//     steps, and lists what lies between.
 //   A list that overflows (many equal values) is cut again by the bits of x, and equal values by their indices.
 // The token is then found by the sums of the units, and in its unit by a prefix sum.
 //
@@ -24,10 +24,11 @@
 // largest; sums of whole numbers are exact in any order, so one CTA and eight give the same bits.
 //
 // What bounds it: with a short list the chain of a row's phases (load, bound, list, sort, draw; some 20000 clocks)
-// over the four rows that an SM has at once: 1024 rows of 40000 f16, top-k 64, top-p 0.95: 38 us, 0.32 of the copy
+// over the four rows that an SM has at once: 1024 rows of 40000 f16, top-k 64, top-p 0.95: 37 us, 0.32 of the copy
 // rate (with the row in shared memory, two rows per SM, 57; 512 threads per row 45).  Without top-k the weights: some
-// 36 instructions each, once for temperature alone (86 us), twice for the nucleus (200 us; weights added to the steps
-// in 64 bits one by one, 254; 64 rows of 120000 bf16 75 us).  4 rows of 40000 f32, eight CTAs each: 10 us.
+// 36 instructions each, once for temperature alone (86 us), and for the nucleus a dozen more and an atomic each (153
+// us; formed exactly twice 200, added to the steps in 64 bits one by one 254; 64 rows of 120000 bf16 60 us).  4 rows of
+// 40000 f32, eight CTAs each: 10 us.
 #pragma once
 
 #include <cooperative_groups.h>
