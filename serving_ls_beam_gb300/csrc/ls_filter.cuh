@@ -1251,8 +1251,9 @@ struct Sampler {
       }
       sync();
       const int step = *at(&s.crossing, 0);
-      // (a little below the step: a lower bound is all it has to be)
-      float bound = __fsub_rd(m, __fdiv_rn((float)(step + 1) * 1.001f, per_step * sc.hi));
+      // (a little below the step: a lower bound is all it has to be; the last one holds all that has a weight)
+      const float deep = step < kSfCoarse - 1 ? __fdiv_rn((float)(step + 1) * 1.001f, per_step * sc.hi) : __fdiv_rn(sc.t_end * 1.001f, sc.hi);
+      float bound = __fsub_rd(m, deep);
       if (step < 0 || !(bound <= m)) bound = -INFINITY;
       const unsigned n = gather_from(bound, mine);
       if (n <= kSfList) {
