@@ -1155,7 +1155,8 @@ struct Sampler {
       clear_units();
       if (tid == 0) s.threads = 0;
       if (min_p > 0.0f && tid == kSfThreads - 1) {  // (once: FP64 is slow)
-        const double cut = (double)temp * log((double)min_p);
+        // (an infinite temperature keeps everything: infinity times log(1) would be NaN)
+        const double cut = temp < INFINITY ? (double)temp * log((double)min_p) : -INFINITY;
         const float high = (float)cut;
         s.min_cut = make_float2(high, isfinite(high) ? (float)(cut - (double)high) : 0.0f);
       }
