@@ -4,11 +4,14 @@ One step evaluates one token per row.  For each layer the caller projects querie
 ``attention``: the token's keys and values go to the row's next position (``ls_paged_write``, quantised where the
 pages have 8 bits) and the queries read the row's positions with it (``ls_paged_attention``).  ``finish`` takes the
 logits and draws every row's next token with settings of its own (``ls_sample_filtered``).  A row that draws
-``eos_id`` is finished: it writes, reads and advances no more, and its token stays ``eos_id``.
+``eos_id`` is finished: it writes and advances no more, its token stays ``eos_id``, and its queries read what it holds
+until it is released.
 
-A prompt is stored layer by layer with ``store`` and counted once with ``advance``; ``restore`` gives a layer's cache
-back as dense tensors (``ls_paged_read``).  Which pages a row has is kept on the host: ``reserve`` before the positions
-are written, ``release`` when the sequence is done.
+A sequence takes an idle row, with length 0, by that row's first ``reserve``, and leaves it by ``release``.  An idle row
+takes part in every step with nothing: it writes nothing, its attention is zeros and its token ``eos_id``.  A prompt is
+stored layer by layer with ``store`` and counted once with ``advance``, before the next step; ``restore`` gives a
+layer's cache back as dense tensors (``ls_paged_read``).  Which pages a row has is kept on the host: ``reserve`` before
+the positions are written, ``release`` when the sequence is done.
 
 The tables, lengths and settings are tensors of fixed places, so that a step can be captured in a CUDA graph (the
 memory-reuse rule of the LightSeq inference article, 31duo.com, itemid-283120, as in ``loop.py``) and replayed after
@@ -45,8 +48,8 @@ class PagedDecoder:
         self.pages = [ls_pages(self.key[i], self.value[i], self.table, self.key_scale[i] if coded else None,
                                self.value_scale[i] if coded else None) for i in range(layers)]
         self.length = words(rows)      # positions held
-        self.live = words(rows) + 1    # 0: finished
-        self.seen = words(rows) + 1    # positions with the step's own
+        self.live = words(rows)        # 1: a sequence that goes on; 0: finished, or none
+        self.seen = words(rows)        # positions with the step's own
         self.next_token = words(rows)
         self.logprob = torch.zeros(rows, device=dev)
         self.attended = torch.empty((rows, heads, head_dim), dtype=dtype, device=dev)
@@ -57,8 +60,8 @@ class PagedDecoder:
         self.held = [[] for _ in range(rows)]
 
     def reserve(self, row: int, positions: int, stream=None) -> None:
-        """Pages for the first `positions` positions of a row.  ValueError where the row or the pool has no room; nothing is
-        taken then."""
+        """Pages for the first `positions` positions of a row; a sequence begins with the row's first page.  ValueError where the
+        row or the pool has no room; nothing is taken then."""
         need = -(-positions // self.page_size) - len(self.held[row])
         if need <= 0:
             return
@@ -71,26 +74,32 @@ class PagedDecoder:
         self.held[row] += new
         with _torch_on(stream, self.table.device):
             self.table[row, first:first + need].copy_(torch.tensor(new, dtype=torch.int32))
+            if first == 0:
+                self.live[row] = 1
+                self.seen[row] = 1
 
     def release(self, row: int, stream=None) -> None:
-        """The row's pages back to the pool; the row is empty and live again."""
+        """The row's pages back to the pool; the row is idle until it gets pages again."""
         self.free += reversed(self.held[row])
         self.held[row] = []
         with _torch_on(stream, self.table.device):
             self.table[row].fill_(-1)
             self.length[row] = 0
-            self.live[row] = 1
-            self.seen[row] = 1
+            self.live[row] = 0
+            self.seen[row] = 0
 
     def store(self, layer: int, key, value, count=None, stream=None) -> None:
         """A prompt's keys and values [rows, tokens, kv_heads, head_dim] behind what the rows hold, the first count [rows]
-        int32 of each row; the lengths stay until advance."""
+        int32 of each row (None: all, of the live rows); the lengths stay until advance."""
+        if count is None:
+            with _torch_on(stream, self.table.device):
+                count = self.live * key.shape[1]
         check(ls_paged_write(key, value, self.length, count, self.pages[layer], self.workspace, stream), "ls_paged_write")
 
     def advance(self, count, stream=None) -> None:
-        """Lengths after a prompt has been stored in every layer: count [rows] int32, or a number for all rows."""
+        """Lengths of the live rows after a prompt has been stored in every layer: count [rows] int32, or a number for all."""
         with _torch_on(stream, self.table.device):
-            self.length.add_(count)
+            self.length.add_(self.live * count)
             torch.add(self.length, self.live, out=self.seen)
 
     def restore(self, layer: int, key, value, stream=None) -> None:
@@ -108,7 +117,7 @@ class PagedDecoder:
 
     def finish(self, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> torch.Tensor:
         """logits [rows, vocab], u [rows] f32 and the rows' settings (None: off): the next token of every row [rows] int32
-        (logprob: of its probability), and the rows' lengths advanced."""
+        (logprob: of its probability; of rows that are not live it says nothing), and the rows' lengths advanced."""
         check(ls_sample_filtered(logits, None, u, temperature, top_k, top_p, min_p, self.next_token, self.logprob,
                                  self.workspace, stream), "ls_sample_filtered")
         with _torch_on(stream, self.table.device):
