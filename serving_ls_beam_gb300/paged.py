@@ -4,8 +4,8 @@ One step evaluates one token per row.  For each layer the caller projects querie
 ``attention``: the token's keys and values go to the row's next position (``ls_paged_write``, quantised where the
 pages have 8 bits) and the queries read the row's positions with it (``ls_paged_attention``).  ``finish`` takes the
 logits and draws every row's next token with settings of its own (``ls_sample_filtered``).  A row that draws
-``eos_id`` is finished: it writes and advances no more, its token stays ``eos_id``, and its queries read what it holds
-until it is released.
+``eos_id``, or finds nothing to draw (-1), is finished: it writes and advances no more, its token is ``eos_id`` from
+then on, and its queries read what it holds until it is released.
 
 A sequence takes an idle row, with length 0, by that row's first ``reserve``, and leaves it by ``release``.  An idle row
 takes part in every step with nothing: it writes nothing, its attention is zeros and its token ``eos_id``.  A prompt is
@@ -123,6 +123,6 @@ class PagedDecoder:
         with _torch_on(stream, self.table.device):
             self.next_token.masked_fill_(self.live == 0, self.eos_id)
             self.length.add_(self.live)
-            self.live.mul_(self.next_token != self.eos_id)
+            self.live.mul_((self.next_token != self.eos_id) & (self.next_token >= 0))
             torch.add(self.length, self.live, out=self.seen)
         return self.next_token

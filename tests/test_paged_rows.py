@@ -103,3 +103,12 @@ def test_a_prompt_for_all_rows_leaves_idle_ones_out(calls):
     assert calls.writes[-1] == ([0, 0, 0], [5, 0, 5])
     dec.advance(5)
     assert dec.length.tolist() == [5, 0, 5]
+
+
+def test_nothing_to_draw_ends_a_row(calls):
+    dec = decoder()
+    for r in range(3):
+        dec.reserve(r, 8)
+    assert step(dec, calls, [7, -1, 7]) == [7, -1, 7]
+    assert dec.live.tolist() == [1, 0, 1]
+    assert step(dec, calls, [7, 7, 7]) == [7, EOS, 7] and dec.length.tolist() == [2, 1, 2]
