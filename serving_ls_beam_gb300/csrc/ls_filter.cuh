@@ -875,10 +875,11 @@ struct Sampler {
   // many that it takes select(), which gives the cut alone.
   //
   // One pass counts the weights in coarse whole numbers in the histogram's steps (2^-31 of an upper bound of the sum).
-  // They are formed in f32 alone: t is off by three roundings at most, of up to 32 octaves 5.7e-6, the exponent's
-  // by 2^-19 octaves, the power by 2^-22, together less than 2^-17 of a weight; and cut to a whole number each loses
-  // less than one.  So the steps between which the limit must be passed are known, few of them.  A second pass sums the
-  // weights exactly, of everything and of the units above those steps, and lists what lies in them.
+  // They are formed in f32 alone: t carries four roundings (64 log2(e), its quotient by T, the difference, the product),
+  // of up to 32 octaves 4 * 2^-24 * 32 = 2^-17 octaves; the exponent below 32 one more of 2^-20; the power is good to
+  // 2^-22: (2^-17 + 2^-20) ln 2 + 2^-22 = 0.9 * 2^-17 of a weight.  And cut to a whole number each loses less than one.
+  // So the steps between which the limit must be passed are known, few of them.  A second pass sums the weights exactly, of
+  // everything and of the units above those steps, and lists what lies in them.
   template <bool ALL>  // within is everything
   __device__ __forceinline__ bool nucleus(float top_p, const Cut& within, Cut& cut) {
     auto* steps = reinterpret_cast<uint32_t*>(hist);
@@ -935,7 +936,7 @@ struct Sampler {
       u64 run = scan(here) - here;
       // what the whole numbers' sum is at least and at most where the coarse one's is c
       const auto at_least = [&](u64 c) { return (u64)max((long long)(c - (c >> 17)) - (p.vocab >> down) - 1, 0ll); };
-      const auto at_most = [&](u64 c) { return c + (c >> 17) + p.vocab + 1; };
+      const auto at_most = [&](u64 c) { return c + (c >> 17) + p.vocab + (p.vocab >> 17) + 2; };  // (what was cut off is as uncertain)
       const u64 all = block_total(here);
       bool cut_off;
       const u64 maybe = part_of(top_p, at_least(all), cut_off), sure = part_of(top_p, at_most(all), cut_off) + 2;
