@@ -1254,7 +1254,8 @@ struct Sampler {
       sync();
       const int step = *at(&s.crossing, 0);
       // (a little below the step: a lower bound is all it has to be; the last one holds all that has a weight)
-      const float deep = step < kSfCoarse - 1 ? __fdiv_rn((float)(step + 1) * 1.001f, per_step * sc.hi) : __fdiv_rn(sc.t_end * 1.001f, sc.hi);
+      const bool last = step >= kSfCoarse - 1;
+      const float deep = __fdiv_rn((last ? sc.t_end : (float)(step + 1)) * 1.001f, last ? sc.hi : per_step * sc.hi);
       float bound = __fsub_rd(m, deep);
       if (step < 0 || !(bound <= m)) bound = -INFINITY;
       const unsigned n = gather_from(bound, mine);
