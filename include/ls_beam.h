@@ -467,9 +467,9 @@ LS_API ls_status ls_paged_read(const ls_pages* pages, const int32_t* start, cons
  *  len         [rows] int32, device.  A length outside [0, max_pages * page_size] is clamped, and a
  *              page outside [0, num_pages) is left out; both set LS_ERR_INTERNAL in the status word.
  *  Positions at or past len are not used, whatever they hold.  Scores, softmax and sums are f32; with q
- *  in 16 bits the softmax weights are rounded for the product with the values, to f16 for 8-bit pages
- *  and else to their type (in f16 those under 2^-32 of the largest count in the sum alone), and the
- *  result is rounded once.
+ *  in 16 bits a softmax weight goes into the product with the values in two pieces, of f16 for 8-bit
+ *  pages and else of their type (f16: good to 2^-22 of it and 2^-31 of the largest; bf16: 2^-16), with
+ *  bf16 q over 8-bit pages in one of f16 (2^-11), and the result is rounded once.
  *  heads       a multiple of kv_heads; head_dim 1..256.
  *  workspace   >= ls_paged_attention_workspace_size(rows, heads, kv_heads, head_dim) bytes, 256-byte
  *              aligned, initialised once by ls_workspace_init; the size grows with heads / kv_heads (up

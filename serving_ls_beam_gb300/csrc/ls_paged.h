@@ -69,7 +69,8 @@ struct PagedParams {
 };
 // 16-bit queries; every stride and address a multiple of 16 bytes, the vectors of 16
 cudaError_t launch_paged_mma(const PagedParams& p, int dtype, int cache, bool by_warp, cudaStream_t stream);
-cudaError_t launch_paged_mma_codes(const PagedParams& p, int dtype, int cache, bool by_warp, cudaStream_t stream);
+cudaError_t launch_paged_mma_e4m3(const PagedParams& p, int dtype, bool by_warp, cudaStream_t stream);
+cudaError_t launch_paged_mma_i8(const PagedParams& p, int dtype, bool by_warp, cudaStream_t stream);
 bool paged_mma_warps(const PagedParams& p);
 int paged_mma_queries(int dim, int group);
 int paged_mma_ctas(int dim, int group);  // CTAs that an SM holds

@@ -22,6 +22,13 @@
 // values 2^-20 of the others'), so the weights of the second product are 2^(score + log2 scale - reference) with a
 // reference of their own, the largest such exponent, apart from the maximum that the sum is taken with.
 //
+// A weight goes into that product in two pieces (REST), rounded and what the rounding left: in f16 together good to 2^-22,
+// in bf16 to 2^-16 of it.  The sum takes it as it is, in f32.  With the first piece alone the weights' rounding would count
+// as much as the result's (relative errors against 64 bits, one piece and two: bf16 2.3e-3 and 1.7e-3, f16 over int8 2.9e-4
+// and 2.1e-4, f16 1.07e-4 and 0.93e-4); the second costs a product per fragment (131000 bf16 positions 90.3 -> 90.5 us,
+// int8 36.1 -> 36.5, 1024 short f16 rows 54.7 -> 55.4).  With bf16 queries over codes one f16 piece is 2^-11 of a weight
+// beside a result rounded to 2^-8 of its value (1.67e-3 and 1.66e-3; 219 and 227 us), and is all there is.
+//
 // What bounds it: the instructions around the products (some 250 per warp for a block of 4 KB of 16-bit keys and values,
 // twice that for codes, whose conversion is the most of it; 750 per part) and the latency that 8 to 16 warps per SM leave.
 // 256 rows x 8 key heads of 128 codes, 4 queries, 501 to 4000 positions: 1.22 GB in 219 us, 0.82 of the measured copy rate
@@ -83,6 +90,16 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     return half2_bits(lo, hi);
   }
 }
+// What pack_pair's rounding left of a pair of weights, rounded itself.
+template <bool BF>
+__device__ __forceinline__ uint32_t rest_of(float lo, float hi, uint32_t rounded) {
+  if constexpr (BF) {
+    return pack_pair<BF>(lo - __uint_as_float(rounded << 16), hi - __uint_as_float(rounded & 0xffff0000u));
+  } else {
+    const __half2 h = *reinterpret_cast<const __half2*>(&rounded);
+    return pack_pair<BF>(lo - __low2float(h), hi - __high2float(h));
+  }
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -126,7 +143,7 @@ struct PmShape {
   static constexpr bool QREG = DP <= 128;               // the queries' fragments stay in registers
 };
 
-template <int KIND, int DP, int NQ, bool TILES>
+template <int KIND, int DP, int NQ, bool TILES, bool REST>
 __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
     paged_mma_kernel(const __grid_constant__ PagedParams p, int dtype, int by_warp) {
   using S = PmShape<KIND, DP, NQ>;
@@ -508,7 +525,7 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
           }
         }
       }
-      uint32_t pb[KT][NQ][2];
+      uint32_t pb[KT][NQ][2], pr[KT][NQ][2];  // the weights, and (REST) their remainders
 #pragma unroll
       for (int a = 0; a < NQ; ++a) {
         float sub[2], subz[2];
@@ -528,7 +545,9 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
               l[a][e] += w1;
               w[e] = CODES ? fast_exp2(y + lv[k][hf] - subz[e]) : w1;
             }
-            pb[k][a][hf] = transpose8(pack_pair<BF>(w[0], w[1]));
+            const uint32_t most = pack_pair<BF>(w[0], w[1]);
+            pb[k][a][hf] = transpose8(most);
+            if constexpr (REST) pr[k][a][hf] = transpose8(rest_of<BF>(w[0], w[1], most));
           }
       }
 
@@ -547,14 +566,19 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
                 codes_half<KIND>(__byte_perm(v0, v1, hh ? 0x7362 : 0x5140), a0, a1);
                 codes_half<KIND>(__byte_perm(v2, v3, hh ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-                for (int a = 0; a < NQ; ++a)
+                for (int a = 0; a < NQ; ++a) {
                   mma16816<BF>(o[(i * VW + w) * 2 + hh][a], a0, a1, a2, a3, pb[k][a][0], pb[k][a][1]);
+                  if constexpr (REST) mma16816<BF>(o[(i * VW + w) * 2 + hh][a], a0, a1, a2, a3, pr[k][a][0], pr[k][a][1]);
+                }
               }
             } else {
               const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
               const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
-              for (int a = 0; a < NQ; ++a) mma16816<BF>(o[i * VW + w][a], a0, a1, a2, a3, pb[k][a][0], pb[k][a][1]);
+              for (int a = 0; a < NQ; ++a) {
+                mma16816<BF>(o[i * VW + w][a], a0, a1, a2, a3, pb[k][a][0], pb[k][a][1]);
+                if constexpr (REST) mma16816<BF>(o[i * VW + w][a], a0, a1, a2, a3, pr[k][a][0], pr[k][a][1]);
+              }
             }
           }
       if (more) {
@@ -697,12 +721,12 @@ __global__ void __launch_bounds__(kPgThreads, PmShape<KIND, DP, NQ>::CTAS)
   }
 }
 
-template <int KIND, int DP, int NQ>
+template <int KIND, int DP, int NQ, bool REST>
 cudaError_t run_paged(const PagedParams& p, int dtype, bool by_warp, cudaStream_t stream) {
   const unsigned grid = (unsigned)(by_warp ? p.workers / kPgWarps : p.workers);
   constexpr int QUERIES = kPgWarps * 2 * 8 * NQ * (DP * 2 + 16), SUMS = kPgWarps * 8 * NQ * DP * 4;
   const int bytes = QUERIES + (by_warp ? 0 : SUMS);
-  auto kernel = p.pages.page_size % 16 == 0 ? paged_mma_kernel<KIND, DP, NQ, true> : paged_mma_kernel<KIND, DP, NQ, false>;
+  auto kernel = p.pages.page_size % 16 == 0 ? paged_mma_kernel<KIND, DP, NQ, true, REST> : paged_mma_kernel<KIND, DP, NQ, false, REST>;
   static std::atomic<uint64_t> allowed[2];
   const cudaError_t e = allow_shared(kernel, QUERIES + SUMS, allowed[p.pages.page_size % 16 == 0]);
   if (e != cudaSuccess) return e;
@@ -710,11 +734,11 @@ cudaError_t run_paged(const PagedParams& p, int dtype, bool by_warp, cudaStream_
   return cudaGetLastError();
 }
 
-template <int KIND>
+template <int KIND, bool REST>
 cudaError_t run_paged_dim(const PagedParams& p, int dtype, bool by_warp, cudaStream_t stream) {
-  if (p.dim <= 64) return p.tile <= 8 ? run_paged<KIND, 64, 1>(p, dtype, by_warp, stream) : run_paged<KIND, 64, 2>(p, dtype, by_warp, stream);
-  if (p.dim <= 128) return p.tile <= 8 ? run_paged<KIND, 128, 1>(p, dtype, by_warp, stream) : run_paged<KIND, 128, 2>(p, dtype, by_warp, stream);
-  return run_paged<KIND, 256, 1>(p, dtype, by_warp, stream);
+  if (p.dim <= 64) return p.tile <= 8 ? run_paged<KIND, 64, 1, REST>(p, dtype, by_warp, stream) : run_paged<KIND, 64, 2, REST>(p, dtype, by_warp, stream);
+  if (p.dim <= 128) return p.tile <= 8 ? run_paged<KIND, 128, 1, REST>(p, dtype, by_warp, stream) : run_paged<KIND, 128, 2, REST>(p, dtype, by_warp, stream);
+  return run_paged<KIND, 256, 1, REST>(p, dtype, by_warp, stream);
 }
 
 }  // namespace

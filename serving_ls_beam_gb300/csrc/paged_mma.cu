@@ -13,9 +13,9 @@ bool paged_mma_warps(const PagedParams& p) {
 }
 
 cudaError_t launch_paged_mma(const PagedParams& p, int dtype, int cache, bool by_warp, cudaStream_t stream) {
-  if (cache == LS_DTYPE_F16) return run_paged_dim<KIND_F16>(p, dtype, by_warp, stream);
-  if (cache == LS_DTYPE_BF16) return run_paged_dim<KIND_BF16>(p, dtype, by_warp, stream);
-  return launch_paged_mma_codes(p, dtype, cache, by_warp, stream);
+  if (cache == LS_DTYPE_F16) return run_paged_dim<KIND_F16, true>(p, dtype, by_warp, stream);
+  if (cache == LS_DTYPE_BF16) return run_paged_dim<KIND_BF16, true>(p, dtype, by_warp, stream);
+  return cache == LS_DTYPE_E4M3 ? launch_paged_mma_e4m3(p, dtype, by_warp, stream) : launch_paged_mma_i8(p, dtype, by_warp, stream);
 }
 
 }  // namespace lsb
