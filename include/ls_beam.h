@@ -379,7 +379,8 @@ LS_API ls_status ls_tree_commit(void* cache_key, void* cache_value, const int32_
  *              row_stride elements (row_stride >= vocab); bias [vocab] f32 or NULL.
  *  u           [rows] f32 in [0, 1).
  *  temperature [rows] f32 or NULL (1): 0 gives the first largest x with log-probability 0; infinity
- *              makes the finite ones equally likely.
+ *              makes the finite ones equally likely; one between 0 and 1e-28 counts as about that.
+ *              An x that lies below M by more than f32 holds is never drawn.
  *  top_k       [rows] int32 or NULL: 0, or vocab and more, keeps all.
  *  top_p       [rows] f32 or NULL: in (0, 1]; 1 keeps all.
  *  min_p       [rows] f32 or NULL: in [0, 1]; 0 keeps all.

@@ -49,7 +49,10 @@ constexpr int kSfBins = 2048;
 constexpr int kSfList = 2048;        // entries of the list, in the histogram's place
 constexpr int kSfRank = kSfThreads;  // lists up to this are ranked and drawn from; longer ones sorted by exchanges
 constexpr int kSfCoarse = kSfThreads;  // steps of the histogram of maxima, one per thread
-constexpr int kSfListed = 1000;      // the largest top-k that goes by a list alone
+// The largest top-k that goes by a list alone: more overflow the list too often.  By the list and by the counts, us: of 1024
+// rows of 40000 top-k 64 36 and 159, 400 90 and 210, 1000 166 and 223, 2000 233 both (it overflows); 64 rows of 120000
+// top-k 1000 62 and 85, 2000 104 and 83; 4 rows of 40000 f32 1000 37 and 43, 2000 52 and 44.
+constexpr int kSfListed = 1000;
 constexpr int kSfSteps = 64;         // steps of an octave in the table of powers
 constexpr float kSfMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number in the low bits
 constexpr uint32_t kSfMagicBits = 0x4b400000u;
@@ -675,7 +678,7 @@ struct Sampler {
   }
   __device__ __forceinline__ void write(int token, u64 w, u64 all) const {
     p.out_token[row] = token;
-    // (near 1 from what is missing)
+    // (near 1 from what is missing; f32 quotients of the exact sums, three roundings: 2^-22 absolute with the logarithm's own)
     if (p.out_logprob) p.out_logprob[row] = w > all / 2 ? log1pf(-((float)(all - w) / (float)all)) : logf((float)w / (float)all);
   }
   // f * all, f in [0, 1], rounded down to a whole number; rest: whether anything was cut off.  (f is a whole
@@ -1211,7 +1214,9 @@ struct Sampler {
     bool summed = false;  // the units' sums of what is kept are there
     if (top_k > 0 && top_k <= kSfListed && (top_k <= kSfThreads * ctas() / 4 || top_k <= vectors / 4)) {
       // The k-th largest of the threads' maxima, or of the vectors', by coarse steps: at least k tokens lie there
-      // or above, and not many more.
+      // or above, and not many more.  The threads' are at hand, and good enough while k is few of them: by the threads' and
+      // by the vectors', us, 1024 rows of 40000 top-k 30 30 and 41, 64 36 and 46; 64 rows of 120000 over four CTAs top-k 200 27
+      // and 31.  (Up to half of the threads they would be still, by less: top-k 100 45 and 50, 500 36 and 45.)
       const float per_step = (float)kSfCoarse / fminf(sc.t_end, 48.0f * sc.hi);
       auto* steps = reinterpret_cast<uint32_t*>(at(hist, 0));
       auto count = [&](float top) {

@@ -25,16 +25,16 @@
 // A weight goes into that product in two pieces (REST), rounded and what the rounding left: in f16 together good to 2^-22,
 // in bf16 to 2^-16 of it.  The sum takes it as it is, in f32.  With the first piece alone the weights' rounding would count
 // as much as the result's (relative errors against 64 bits, one piece and two: bf16 2.3e-3 and 1.7e-3, f16 over int8 2.9e-4
-// and 2.1e-4, f16 1.07e-4 and 0.93e-4); the second costs a product per fragment (131000 bf16 positions 90.3 -> 90.5 us,
-// int8 36.1 -> 36.5, 1024 short f16 rows 54.7 -> 55.4).  With bf16 queries over codes one f16 piece is 2^-11 of a weight
+// and 2.1e-4, f16 1.07e-4 and 0.93e-4); the second costs a product per fragment (131000 bf16 positions 90.2 -> 90.3 us,
+// int8 36.0 -> 36.7, 1024 short f16 rows 54.8 -> 55.6).  With bf16 queries over codes one f16 piece is 2^-11 of a weight
 // beside a result rounded to 2^-8 of its value (1.67e-3 and 1.66e-3; 219 and 227 us), and is all there is.
 //
-// What bounds it: the instructions around the products (some 250 per warp for a block of 4 KB of 16-bit keys and values,
+// What bounds it: the instructions around the products (some 260 per warp for a block of 4 KB of 16-bit keys and values,
 // twice that for codes, whose conversion is the most of it; 750 per part) and the latency that 8 to 16 warps per SM leave.
 // 256 rows x 8 key heads of 128 codes, 4 queries, 501 to 4000 positions: 1.22 GB in 219 us, 0.82 of the measured copy rate
 // (a CTA's four warps per part 238; page numbers through shuffles for every key 235); one row of 131000 bf16 positions
-// 89 us, 0.88 (the parts joined by one thread per element 114); 32 rows of 2000 to 8000 105 us, 0.92; 64 rows x 16 heads of
-// 64 int8, 300 to 999 positions: 36 us, 0.37; 1024 rows x 16 heads of 64 f16, 48 to 63 positions: 55 us, 0.63.  Blocks of 32
+// 90 us, 0.88 (the parts joined by one thread per element 114); 32 rows of 2000 to 8000 105 us, 0.92; 64 rows x 16 heads of
+// 64 int8, 300 to 999 positions: 37 us, 0.37; 1024 rows x 16 heads of 64 f16, 48 to 63 positions: 56 us, 0.62.  Blocks of 32
 // keys for 16-bit heads of 64: no faster; a fifth CTA per SM for them spills (int8 36 -> 48 us).
 #pragma once
 

@@ -8,11 +8,16 @@
 // put right by the remainder x - code * scale, which f32 holds exactly.
 //
 // A group of lanes has one head vector of keys and the same of values, 16 elements per lane, so that its
-// loads are under way together and the page is looked up once (a write's tokens come while it is); the largest element
-// is found by exchanges within the group.  Bound by memory, with reads and writes mixed: 16 prompts of 1201 to 2048 tokens
-// x 8 heads of 128 bf16 into e4m3 161 MB in 33 us, 0.72 of the measured copy rate, into int8 41 us (each code
-// checked by itself 50), as they are 213 MB in 40 us; 16 rows of 1001 to 4000 positions of int8 back to bf16 248 MB in 44.5 us,
-// 0.82 (CTAs of 64 threads; of 128, 46).  1024 single tokens x 16 heads of 64 f16 into int8: 4.3 us.
+// loads are under way together and the page is looked up once; the largest element is found by exchanges within the group.
+// A write's tokens are loaded while their places are looked up, before the count is known: single tokens wait for one
+// thing less, but of prompts the tokens past a row's count are read for nothing.
+//
+// Bound by memory, with reads and writes mixed, and close to it by instructions where codes are made: 16 prompts of 1201 to
+// 2048 tokens x 8 heads of 128 bf16 as they are 213 MB, and 28 MB of tokens past the counts, in 40 us, 0.89 of the measured
+// copy rate; into e4m3 161 and 28 MB in 33 us, 0.84 (what is needed alone 0.72), 72 % of the issue slots in use; into int8
+// 189 MB in 41 us, 0.68 (each code checked by itself 50).
+// 16 rows of 1001 to 4000 positions of int8 back to bf16 248 MB in 44.5 us, 0.82 (CTAs of 64 threads; of 128, 46).  1024 single
+// tokens x 16 heads of 64 f16 into int8: 4.3 us.
 #include <cuda_fp8.h>
 
 #include "ls_paged.cuh"
