@@ -477,7 +477,8 @@ LS_API ls_status ls_paged_read(const ls_pages* pages, const int32_t* start, cons
  *              to 16) and head_dim only.  Calls sharing it must be ordered.  It is these calls' own: of
  *              the other entry points only ls_paged_write, ls_paged_read and ls_sample_filtered may be
  *              given it too (its counters are zero between calls, and others would overwrite them).
- *  Inputs that a query reads are finite; otherwise its result is unspecified (no fault).  rows == 0 is a
+ *  Inputs that a query reads are finite, its scores too, and 2^9 times its row's length times its
+ *  largest |value| is within f32's range; otherwise its result is unspecified (no fault).  rows == 0 is a
  *  no-op.  Fastest with q in 16 bits, strides and addresses that are multiples of 16 bytes, head_dim of
  *  16 (16-bit pages: 8), and pages of a multiple of 16 positions.  rows * heads or max_pages * page_size
  *  above 2^31 - 1024 returns LS_ERR_UNSUPPORTED.
